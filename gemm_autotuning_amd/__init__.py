@@ -17,6 +17,8 @@ F32, F16, BF16, FP8_E4M3 = 0, 1, 2, 3
 NN, NT, TN, TT = 0, 1, 2, 3
 DTYPES = {"f32": F32, "f16": F16, "bf16": BF16, "e4m3": FP8_E4M3}
 LAYOUTS = {"NN": NN, "NT": NT, "TN": TN, "TT": TT}
+QUANT = {"none": 0, "tensor": 1, "row": 2}
+W4_FORMATS = {"int4": 0, "e2m1": 1}
 STATUS = {0: "GT_OK", 1: "GT_ERR_INVALID_ARG", 2: "GT_ERR_UNSUPPORTED", 3: "GT_ERR_HIP", 4: "GT_ERR_NOT_FOUND",
           5: "GT_ERR_IO", 6: "GT_ERR_VALIDATION", 7: "GT_ERR_OOM", 8: "GT_ERR_NO_DEVICE"}
 
@@ -33,6 +35,33 @@ class Desc(ctypes.Structure):
                 ("lda", ctypes.c_int64), ("ldb", ctypes.c_int64), ("ldc", ctypes.c_int64),
                 ("layout", ctypes.c_int32), ("in_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
                 ("scale_a", ctypes.c_float), ("scale_b", ctypes.c_float), ("stream", ctypes.c_void_p)]
+
+
+class RmsNormDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("x", "residual", "weight", "sum_out", "y", "rstd", "row_scale")] + [
+        (n, ctypes.c_int64) for n in ("M", "N", "ldx", "ldr", "lds", "ldy")] + [
+        (n, ctypes.c_int32) for n in ("in_dtype", "weight_dtype", "out_dtype", "quant")] + [
+        (n, ctypes.c_float) for n in ("eps", "weight_offset", "scale")] + [("stream", ctypes.c_void_p)]
+
+
+class RmsNormBwdDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("dy", "h", "weight", "rstd", "dsum", "dx", "dweight")] + [
+        (n, ctypes.c_int64) for n in ("M", "N", "lddy", "ldh", "ldds", "lddx")] + [
+        (n, ctypes.c_int32) for n in ("in_dtype", "dy_dtype", "weight_dtype", "dweight_dtype")] + [
+        ("weight_offset", ctypes.c_float), ("stream", ctypes.c_void_p)]
+
+
+class W4Desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("x", "row_scale", "qweight", "scales", "y")] + [
+        (n, ctypes.c_int64) for n in ("M", "N", "K", "ldx", "ldq", "ldy", "scale_ldn", "scale_ldg")] + [
+        (n, ctypes.c_int32) for n in ("x_dtype", "out_dtype", "format", "scale_dtype", "group")] + [
+        ("x_scale", ctypes.c_float), ("stream", ctypes.c_void_p)]
+
+
+class W4ExpandDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("qweight", "scales", "out")] + [
+        (n, ctypes.c_int64) for n in ("N", "K", "ldq", "ldo", "scale_ldn", "scale_ldg")] + [
+        (n, ctypes.c_int32) for n in ("out_dtype", "format", "scale_dtype", "group")] + [("stream", ctypes.c_void_p)]
 
 
 class TuneFileReport(ctypes.Structure):
@@ -88,6 +117,10 @@ def lib():
             "gemm_tuned": [p, p, p, i64, i64, i64, i32, i32],
             "gemm_tuned_ex": [P(Desc)],
             "gemm_tuned_noalloc": [P(Desc)],
+            "gt_rmsnorm": [P(RmsNormDesc)],
+            "gt_rmsnorm_backward": [P(RmsNormBwdDesc)],
+            "gt_w4_matmul": [P(W4Desc)],
+            "gt_w4_expand": [P(W4ExpandDesc)],
             "gt_test_alloc_count": [P(ctypes.c_uint64), P(ctypes.c_uint64)],
             "gt_make_key": [P(Desc), p, ctypes.c_char_p, ctypes.c_size_t],
             "gt_key_display": [P(Desc), ctypes.c_char_p, ctypes.c_size_t],
@@ -225,6 +258,139 @@ def tune_results():
         _check(lib().tune_results(buf, cap, ctypes.byref(need)))
         if need.value <= cap:  # the table may have grown between the calls
             return buf.value.decode()
+
+
+# ---- operators around the product
+_TORCH_DTYPES = {"torch.float32": F32, "torch.float16": F16, "torch.bfloat16": BF16,
+                 "torch.float8_e4m3fn": FP8_E4M3}
+
+
+def _type_of(t, what):
+    code = _TORCH_DTYPES.get(str(t.dtype))
+    if code is None:
+        raise ValueError("%s: %s is no type of this library" % (what, t.dtype))
+    return code
+
+
+def _matrix(t, shape, what, dtype=None):
+    """Leading dimension of a matrix of this shape (and type) whose rows are contiguous."""
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s has shape %s, not %s" % (what, tuple(t.shape), tuple(shape)))
+    if dtype is not None and _type_of(t, what) != dtype:
+        raise ValueError("%s is %s" % (what, t.dtype))
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError("%s: the elements of a row must be contiguous" % what)
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _vector(t, n, what, dtype=None):
+    if t is None:
+        return
+    if tuple(t.shape) != (n,) or (n > 1 and t.stride(0) != 1):
+        raise ValueError("%s must be %d contiguous elements" % (what, n))
+    if dtype is not None and _type_of(t, what) != dtype:
+        raise ValueError("%s is %s" % (what, t.dtype))
+
+
+def _same_device(first, *others):
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError("tensors on %s and %s" % (first.device, t.device))
+
+
+def make_rmsnorm_desc(x, weight, y, residual=None, sum_out=None, rstd=None, row_scale=None, quant="none", eps=1e-6,
+                      scale=1.0, weight_offset=0.0, stream=None):
+    """Descriptor of gt_rmsnorm from tensors (M x N; strides and types are
+    theirs).  It holds their addresses and keeps them alive."""
+    M, N = x.shape
+    dt = _type_of(x, "x")
+    d = RmsNormDesc(_ptr(x), _ptr(residual), _ptr(weight), _ptr(sum_out), _ptr(y), _ptr(rstd), _ptr(row_scale), M, N,
+                    _matrix(x, (M, N), "x"), 0 if residual is None else _matrix(residual, (M, N), "residual", dt),
+                    0 if sum_out is None else _matrix(sum_out, (M, N), "sum_out", dt), _matrix(y, (M, N), "y"), dt,
+                    -1 if weight is None else _type_of(weight, "weight"), _type_of(y, "y"), _code(quant, QUANT), eps,
+                    weight_offset, scale, _ptr(stream))
+    _vector(weight, N, "weight")
+    _vector(rstd, M, "rstd", F32)
+    _vector(row_scale, M, "row_scale", F32)
+    _same_device(x, weight, y, residual, sum_out, rstd, row_scale)
+    d.tensors = (x, weight, y, residual, sum_out, rstd, row_scale)
+    return d
+
+
+def make_rmsnorm_bwd_desc(dy, h, weight, rstd, dx, dweight=None, dsum=None, weight_offset=0.0, stream=None):
+    """Descriptor of gt_rmsnorm_backward from tensors; dx or dweight may be None."""
+    M, N = h.shape
+    dt = _type_of(h, "h")
+    d = RmsNormBwdDesc(_ptr(dy), _ptr(h), _ptr(weight), _ptr(rstd), _ptr(dsum), _ptr(dx), _ptr(dweight), M, N,
+                       _matrix(dy, (M, N), "dy"), _matrix(h, (M, N), "h"),
+                       0 if dsum is None else _matrix(dsum, (M, N), "dsum", dt),
+                       0 if dx is None else _matrix(dx, (M, N), "dx", dt), dt, _type_of(dy, "dy"),
+                       -1 if weight is None else _type_of(weight, "weight"),
+                       -1 if dweight is None else _type_of(dweight, "dweight"), weight_offset, _ptr(stream))
+    _vector(weight, N, "weight")
+    _vector(rstd, M, "rstd", F32)
+    _vector(dweight, N, "dweight")
+    _same_device(dy, h, weight, rstd, dsum, dx, dweight)
+    d.tensors = (dy, h, weight, rstd, dsum, dx, dweight)
+    return d
+
+
+def _w4_weights(qweight, scales, K, group, format):
+    """(ldq, scale strides, scale type) of N x ceil(K/2) bytes and N x
+    ceil(K/group) scales (any strides: a transposed view is taken as it is)."""
+    if group not in (32, 64, 128):
+        raise ValueError("group must be 32, 64 or 128")
+    N, G = qweight.shape[0], -(-K // group)
+    if str(qweight.dtype) != "torch.uint8":
+        raise ValueError("qweight must be bytes (torch.uint8)")
+    ldq = _matrix(qweight, (N, -(-K // 2)), "qweight")
+    if tuple(scales.shape) != (N, G):
+        raise ValueError("scales has shape %s, not %s" % (tuple(scales.shape), (N, G)))
+    if (N > 1 and scales.stride(0) < 1) or (G > 1 and scales.stride(1) < 1):
+        raise ValueError("scales: broadcast strides are not taken")
+    # the stride along a dimension of one element says nothing
+    return N, ldq, scales.stride(0) if N > 1 else max(1, G), scales.stride(1) if G > 1 else 1, _type_of(scales, "scales")
+
+
+def make_w4_desc(x, qweight, scales, y, format="int4", group=128, row_scale=None, x_scale=1.0, stream=None):
+    """Descriptor of gt_w4_matmul: y (M x N) = x (M x K) times 4-bit weights
+    (N x K) in bytes (N x ceil(K/2)) with scales (N x ceil(K/group))."""
+    M, K = x.shape
+    N, ldq, sn, sg, sdt = _w4_weights(qweight, scales, K, group, format)
+    d = W4Desc(_ptr(x), _ptr(row_scale), _ptr(qweight), _ptr(scales), _ptr(y), M, N, K, _matrix(x, (M, K), "x"), ldq,
+               _matrix(y, (M, N), "y"), sn, sg, _type_of(x, "x"), _type_of(y, "y"), _code(format, W4_FORMATS), sdt,
+               group, x_scale, _ptr(stream))
+    _vector(row_scale, M, "row_scale", F32)
+    _same_device(x, qweight, scales, y, row_scale)
+    d.tensors = (x, qweight, scales, y, row_scale)
+    return d
+
+
+def make_w4_expand_desc(qweight, scales, out, format="int4", group=128, stream=None):
+    """Descriptor of gt_w4_expand: out (N x K) from 4-bit weights as in make_w4_desc."""
+    N, K = out.shape
+    n, ldq, sn, sg, sdt = _w4_weights(qweight, scales, K, group, format)
+    d = W4ExpandDesc(_ptr(qweight), _ptr(scales), _ptr(out), N, K, ldq, _matrix(out, (n, K), "out"), sn, sg,
+                     _type_of(out, "out"), _code(format, W4_FORMATS), sdt, group, _ptr(stream))
+    _same_device(qweight, scales, out)
+    d.tensors = (qweight, scales, out)
+    return d
+
+
+def gt_rmsnorm(desc):
+    _check(lib().gt_rmsnorm(ctypes.byref(desc)))
+
+
+def gt_rmsnorm_backward(desc):
+    _check(lib().gt_rmsnorm_backward(ctypes.byref(desc)))
+
+
+def gt_w4_matmul(desc):
+    _check(lib().gt_w4_matmul(ctypes.byref(desc)))
+
+
+def gt_w4_expand(desc):
+    _check(lib().gt_w4_expand(ctypes.byref(desc)))
 
 
 # ---- control

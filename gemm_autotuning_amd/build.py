@@ -31,7 +31,10 @@ HIP_FLAGS = ["--offload-arch=" + ARCH, "-O3", "-std=c++17", "-fPIC", "-Wno-unuse
              "-I", KDIR, "-I", CSRC, "-I", GEN]
 HOST_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-function", "-D__HIP_PLATFORM_AMD__",
               "-I", os.path.join(ROCM, "include"), "-I", CSRC, "-I", GEN]
-HOST_SOURCES = ["key.cpp", "candidates.cpp", "tuner.cpp", "cache.cpp", "device.cpp", "heuristic.cpp", "offline.cpp", "api.cpp"]
+HOST_SOURCES = ["key.cpp", "candidates.cpp", "tuner.cpp", "cache.cpp", "device.cpp", "heuristic.cpp", "offline.cpp", "api.cpp",
+                "operators.cpp"]
+# the kernels written out by hand; the tile kernels are generated beside them
+HIP_SOURCES = ["small_kernels.hip", "gemv.hip", "scratch.hip", "rmsnorm.hip", "w4.hip"]
 
 
 def _headers(kernel=False):
@@ -76,7 +79,7 @@ def _resources(out):
 def kernel_objects():
     """The HIP objects the library links (the current generation's shards
     only; a shard left from a larger earlier family is not among them)."""
-    srcs = [os.path.join(KDIR, "small_kernels.hip"), os.path.join(KDIR, "gemv.hip"), os.path.join(KDIR, "scratch.hip")]
+    srcs = [os.path.join(KDIR, n) for n in HIP_SOURCES]
     srcs += sorted(glob.glob(os.path.join(GEN, "tiles_*.hip")))
     return [os.path.join(BUILD, os.path.basename(x) + ".o") for x in srcs]
 
@@ -90,8 +93,7 @@ def build(force=False, jobs=None, verbose=False):
     os.makedirs(BUILD, exist_ok=True)
     tile_files = gen_kernels.generate(GEN)
     headers, kheaders = _headers(), _headers(kernel=True)
-    hip_sources = [os.path.join(KDIR, "small_kernels.hip"), os.path.join(KDIR, "gemv.hip"),
-                   os.path.join(KDIR, "scratch.hip")] + tile_files
+    hip_sources = [os.path.join(KDIR, n) for n in HIP_SOURCES] + tile_files
     jobs_list, objs = [], []
     for src in hip_sources:
         obj = os.path.join(BUILD, os.path.basename(src) + ".o")

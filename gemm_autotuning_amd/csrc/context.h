@@ -162,6 +162,9 @@ gt_status throughput_limit(DeviceState& d, const Problem& p, void* stream, doubl
 // that use the buffer).
 gt_status get_workspace(DeviceState& d, void* stream, size_t bytes, void** ptr, size_t* have,
                         std::mutex** launch_mu);
+// Whether the stream's workspace already holds `bytes` (get_workspace would
+// allocate nothing).
+bool workspace_ready(DeviceState& d, void* stream, size_t bytes);
 // Tune one key on the device (the caller holds its pending slot).  *winner
 // is the chosen candidate (0, the naive kernel, when no round produced a
 // valid result); *median_us its measured median per launch (NaN if none).

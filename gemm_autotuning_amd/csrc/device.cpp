@@ -176,6 +176,20 @@ gt_status get_workspace(DeviceState& d, void* stream, size_t bytes, void** ptr, 
   return GT_OK;
 }
 
+bool workspace_ready(DeviceState& d, void* stream, size_t bytes) {
+  std::lock_guard<std::mutex> g(d.ws_mu);
+  const uintptr_t key = (uintptr_t)stream + 1;
+  const WsSlot* slot = nullptr;
+  for (int i = 0; i < kWsSlots && !slot; ++i)
+    if (d.ws_slots[i].key.load(std::memory_order_relaxed) == key) slot = &d.ws_slots[i];
+  if (!slot) {
+    auto it = d.ws_overflow.find(stream);
+    if (it != d.ws_overflow.end()) slot = it->second.get();
+  }
+  const WsBuf* b = slot ? slot->buf.load(std::memory_order_relaxed) : nullptr;
+  return b && b->bytes >= bytes;
+}
+
 int launch_candidate(DeviceState& d, const Candidate& c, const Problem& p, void* fixed_ws, size_t fixed_bytes) {
   if (d.fake) {
     const std::vector<double>& t = d.fake_times[c.dtype];

@@ -35,6 +35,67 @@ struct LaunchArgs {
   size_t ws_bytes;
 };
 
+// RMS norm of M rows of N elements (rmsnorm.hip): h = x + r, rstd =
+// 1/sqrt(mean h^2 + eps), y = h * rstd * (w + offset).  r, w, sum, rstd and
+// row_scale may be null.
+struct NormArgs {
+  const void* x;
+  const void* r;
+  const void* w;
+  void* sum;
+  void* y;
+  float* rstd;
+  float* row_scale;
+  int64_t M, N, ldx, ldr, lds, ldy;
+  int in_dtype, w_dtype, out_dtype;
+  int quant;  // gt_quant
+  float eps, offset, scale;
+  hipStream_t stream;
+};
+
+// Its backward pass: dx (may be null) and dw (may be null).  ws: blocks x N
+// fp32 partial sums of dw when dw is wanted.
+struct NormBwdArgs {
+  const void* dy;
+  const void* h;
+  const void* w;
+  const float* rstd;
+  const void* dsum;
+  void* dx;
+  void* dw;
+  int64_t M, N, lddy, ldh, ldds, lddx;
+  int in_dtype, dy_dtype, w_dtype, dw_dtype;
+  float offset;
+  float* ws;
+  int cus;
+  hipStream_t stream;
+};
+
+// Rows times 4-bit weights (w4.hip), and the expansion of such weights.
+struct W4Weights {
+  const uint8_t* q;    // N rows of (K + 1) / 2 bytes, ldq bytes apart
+  const void* scales;  // (n, g) at n * lds_n + g * lds_g
+  int64_t N, K, ldq, lds_n, lds_g;
+  int format, scale_dtype, group;
+};
+struct W4Args {
+  W4Weights w;
+  const void* x;
+  const float* row_scale;
+  void* y;
+  int64_t M, ldx, ldy;
+  int x_dtype, out_dtype;
+  float x_scale;
+  hipStream_t stream;
+};
+struct W4ExpandArgs {
+  W4Weights w;
+  void* y;
+  int64_t ldy;
+  int out_dtype;
+  hipStream_t stream;
+};
+
 // Launcher status codes (0 = launched).
 enum LaunchStatus { LS_OK = 0, LS_UNSUPPORTED = 1, LS_HIP_ERROR = 2 };
 

@@ -29,6 +29,13 @@ int launch_probe_write(void* dst, int64_t bytes, int blocks, uint32_t v, hipStre
 int launch_icache_flush(int blocks, hipStream_t stream);
 int launch_probe_mfma(int dtype, float* out, int iters, int blocks, hipStream_t stream, double* flops_per_launch);
 
+// the operators around the product: rmsnorm.hip, w4.hip
+int launch_rmsnorm(const NormArgs& a);
+int launch_rmsnorm_bwd(const NormBwdArgs& a);
+size_t rmsnorm_bwd_workspace_bytes(const NormBwdArgs& a);
+int launch_w4_matmul(const W4Args& a);
+int launch_w4_expand(const W4ExpandArgs& a);
+
 // Workspace layout shared by every candidate: a fixed region of counters
 // first (GEMV slice counters; zero between launches, each launch leaves them
 // zero), then the data region (fp32 partial sums).  Nothing but those

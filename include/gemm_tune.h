@@ -227,6 +227,151 @@ typedef struct gt_tune_file_report {
 } gt_tune_file_report;
 gt_status gt_tune_file(const char* untuned_path, const char* results_path, gt_tune_file_report* report);
 
+/* ---- operators around the product --------------------------------------- */
+
+/* What a language model runs directly before and around a product of this
+ * library: the RMS norm with the residual's addition, whose output is a
+ * product's left operand (e4m3 with its scales included), that norm's
+ * backward pass, the product of a few rows with 4-bit weights, and the
+ * expansion of such weights into a right operand of gemm_tuned.
+ *
+ * They follow the conventions above (row-major, leading dimensions in
+ * elements with <= 0 for dense, caller-owned device pointers, the stream of
+ * the descriptor or of gt_set_stream, every failure a gt_status).  No table
+ * and no tuning is involved; nothing is launched when a check fails.
+ * Pointers must be aligned to their element.  Inputs and outputs must not
+ * overlap, except where a descriptor says so.  Results do not depend on the
+ * order in which workgroups run: equal inputs give equal bits. */
+
+/* How gt_rmsnorm's output is stored in 8 bits (e4m3, round to nearest even):
+ * not at all; over one given scale, saturating at +-448; or over a scale per
+ * row, max(max |y|, 2^-100) / 448, which the call writes. */
+typedef enum gt_quant { GT_QUANT_NONE = 0, GT_QUANT_TENSOR = 1, GT_QUANT_ROW = 2 } gt_quant;
+
+/* h = x + residual, rstd[m] = 1 / sqrt(mean_n h[m,n]^2 + eps),
+ * y = h * rstd * (weight + weight_offset), all in fp32 and rounded once.
+ * sum_out receives h rounded to in_dtype (the norm itself uses the unrounded
+ * h).  A product of the stored e4m3 rows takes the scale back as scale_a
+ * (GT_QUANT_TENSOR, gemm_tuned_ex) or row_scale (GT_QUANT_ROW,
+ * gt_w4_matmul). */
+typedef struct gt_rmsnorm_desc {
+  const void* x;        /* M x N, ldx                                        */
+  const void* residual; /* M x N, ldr, or NULL                               */
+  const void* weight;   /* N, or NULL for y = h * rstd                       */
+  void* sum_out;        /* M x N, lds, or NULL; may be x or residual itself
+                           (same leading dimension)                          */
+  void* y;              /* M x N, ldy; may be x itself (same type and ld)    */
+  float* rstd;          /* M, or NULL                                        */
+  float* row_scale;     /* M; required by and only used with GT_QUANT_ROW    */
+  int64_t M, N;         /* N <= 65536                                        */
+  int64_t ldx, ldr, lds, ldy;
+  int32_t in_dtype;     /* f32, f16, bf16: x, residual, sum_out              */
+  int32_t weight_dtype; /* f32, f16, bf16; -1: in_dtype                      */
+  int32_t out_dtype;    /* f32, f16, bf16, or e4m3 with a gt_quant; -1: e4m3
+                           with a gt_quant, in_dtype without                 */
+  int32_t quant;        /* gt_quant                                          */
+  float eps;            /* finite, >= 0                                      */
+  float weight_offset;  /* 0, or 1 where weights are stored less one         */
+  float scale;          /* GT_QUANT_TENSOR: finite, > 0                      */
+  void* stream;
+} gt_rmsnorm_desc;
+
+/* GT_ERR_INVALID_ARG: NULL x or y, a bad enum, dimension, leading dimension,
+ * eps or scale, a misaligned pointer, e4m3 output without a gt_quant (or the
+ * reverse), GT_QUANT_ROW without row_scale.  GT_ERR_UNSUPPORTED: e4m3 inputs
+ * or weights, N > 65536.  M == 0 or N == 0 is a no-op. */
+gt_status gt_rmsnorm(const gt_rmsnorm_desc* d);
+
+/* The gradients of y = h * rstd * (weight + weight_offset), given dy, the h
+ * and the rstd of the forward pass: with g = dy * (weight + weight_offset)
+ * and n = h * rstd,
+ *   dx = rstd * (g - n * mean_n(g * n)) + dsum,  dweight = sum_m dy * n.
+ * dx is the gradient of x and of the residual alike; dsum is the gradient
+ * that reaches h past the norm (sum_out's other uses).  dweight is summed
+ * in fp32 in a fixed order; its partial sums take a workspace of the stream,
+ * which the first (largest) call allocates: make that call outside stream
+ * capture. */
+typedef struct gt_rmsnorm_bwd_desc {
+  const void* dy;       /* M x N, lddy                                       */
+  const void* h;        /* M x N, ldh: sum_out, or x without a residual      */
+  const void* weight;   /* N, or NULL                                        */
+  const float* rstd;    /* M                                                 */
+  const void* dsum;     /* M x N, ldds, or NULL                              */
+  void* dx;             /* M x N, lddx, or NULL; may be dy, h or dsum itself
+                           (same type and leading dimension)                 */
+  void* dweight;        /* N, or NULL                                        */
+  int64_t M, N;         /* N <= 65536                                        */
+  int64_t lddy, ldh, ldds, lddx;
+  int32_t in_dtype;      /* f32, f16, bf16: h, dsum, dx                      */
+  int32_t dy_dtype;      /* in_dtype or f32; -1: in_dtype                    */
+  int32_t weight_dtype;  /* f32, f16, bf16; -1: in_dtype                     */
+  int32_t dweight_dtype; /* f32, f16, bf16; -1: f32                          */
+  float weight_offset;
+  void* stream;
+} gt_rmsnorm_bwd_desc;
+
+/* GT_ERR_INVALID_ARG: NULL dy, h or rstd, neither dx nor dweight, and as
+ * gt_rmsnorm; also when the workspace would have to grow while the stream is
+ * being captured.  GT_ERR_OOM: no memory for the workspace.  M == 0 writes
+ * zeros to dweight; N == 0 is a no-op. */
+gt_status gt_rmsnorm_backward(const gt_rmsnorm_bwd_desc* d);
+
+/* 4-bit weights: row n holds weight (n, k) in byte k / 2, the even k in the
+ * low nibble; (K + 1) / 2 bytes a row, rows ldq bytes apart.  A nibble is a
+ * two's complement integer (-8..7), or an e2m1 float (sign, then 0, 0.5, 1,
+ * 1.5, 2, 3, 4, 6).  Every `group` of consecutive k in a row shares a scale:
+ * weight = scale * value. */
+typedef enum gt_w4_format { GT_W4_INT4 = 0, GT_W4_E2M1 = 1 } gt_w4_format;
+
+/* y[m,n] = x_scale * row_scale[m] * sum_k x[m,k] * weight[n,k]: a product
+ * with a transposed right operand (GT_NT) for a few rows, as one token or a
+ * decode batch has.  The nibbles are expanded exactly, the products are
+ * summed per group in fp32 and the scales applied to the fp32 sums.  Any M
+ * is taken; for a prompt's rows, gt_w4_expand and gemm_tuned are faster. */
+typedef struct gt_w4_desc {
+  const void* x;          /* M x K, ldx                                      */
+  const float* row_scale; /* M, or NULL                                      */
+  const void* qweight;    /* N x K in 4 bits, ldq bytes (<= 0: (K + 1) / 2)  */
+  const void* scales;     /* N x ceil(K / group): (n, g) at
+                             n * scale_ldn + g * scale_ldg                   */
+  void* y;                /* M x N, ldy                                      */
+  int64_t M, N, K;
+  int64_t ldx, ldq, ldy;
+  int64_t scale_ldn, scale_ldg; /* elements; <= 0: ceil(K / group) and 1     */
+  int32_t x_dtype;     /* f16, bf16, e4m3                                    */
+  int32_t out_dtype;   /* f32, f16, bf16; -1: x_dtype, f32 for e4m3          */
+  int32_t format;      /* gt_w4_format                                       */
+  int32_t scale_dtype; /* f32, f16, bf16                                     */
+  int32_t group;       /* 32, 64 or 128                                      */
+  float x_scale;       /* 1, or the scale of e4m3 rows                       */
+  void* stream;
+} gt_w4_desc;
+
+/* GT_ERR_INVALID_ARG: a NULL operand, a bad enum, dimension, leading
+ * dimension or group, a misaligned pointer; also when a workspace would have
+ * to grow while the stream is being captured.  GT_ERR_UNSUPPORTED: f32 rows,
+ * e4m3 output or scales.  GT_ERR_OOM: no memory for the workspace.  M == 0 or
+ * N == 0 is a no-op; K == 0 writes zeros. */
+gt_status gt_w4_matmul(const gt_w4_desc* d);
+
+/* out[n,k] = weight (n, k), rounded once to out_dtype: N x K row-major, the
+ * right operand of a GT_NT product. */
+typedef struct gt_w4_expand_desc {
+  const void* qweight;
+  const void* scales;
+  void* out;           /* N x K, ldo                                         */
+  int64_t N, K;
+  int64_t ldq, ldo, scale_ldn, scale_ldg;
+  int32_t out_dtype;   /* f32, f16, bf16                                     */
+  int32_t format;
+  int32_t scale_dtype;
+  int32_t group;
+  void* stream;
+} gt_w4_expand_desc;
+
+/* Errors as gt_w4_matmul.  N == 0 or K == 0 is a no-op. */
+gt_status gt_w4_expand(const gt_w4_expand_desc* d);
+
 /* ---- control ------------------------------------------------------------ */
 
 /* Enable or disable tuning on a miss (the enable-vs-tuning split of the
