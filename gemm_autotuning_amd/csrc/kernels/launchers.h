@@ -33,7 +33,9 @@ int launch_probe_mfma(int dtype, float* out, int iters, int blocks, hipStream_t 
 int launch_rmsnorm(const NormArgs& a);
 int launch_rmsnorm_bwd(const NormBwdArgs& a);
 size_t rmsnorm_bwd_workspace_bytes(const NormBwdArgs& a);
-int launch_w4_matmul(const W4Args& a);
+// ws: w4_workspace_bytes of the stream's workspace, or null when that is 0
+int launch_w4_matmul(const W4Args& a, void* ws, int cus);
+size_t w4_workspace_bytes(const W4Args& a, int cus);
 int launch_w4_expand(const W4ExpandArgs& a);
 
 // Workspace layout shared by every candidate: a fixed region of counters

@@ -1,0 +1,7 @@
+// w4_bf16_e2m1.hip -- the 4-bit weight product's kernels for bf16 rows and e2m1 weights.
+#include "launchers.h"
+#include "w4_mma.h"
+
+namespace gt {
+GT_W4_LAUNCHER(w4_mma_bf16_e2m1, DT_BF16, gtk::W4_E2M1)
+}  // namespace gt

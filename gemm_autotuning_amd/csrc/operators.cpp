@@ -225,7 +225,13 @@ gt_status w4_matmul(const gt_w4_desc* d) {
   GT_CHECK(current_device(&dev));
   if (dev->fake) return GT_OK;
   if (d->K == 0) return launched(launch_zero(a.y, a.M, a.w.N, a.ldy, a.out_dtype, a.stream), "gt_w4_matmul");
-  return launched(launch_w4_matmul(a), "gt_w4_matmul");
+  const size_t need = w4_workspace_bytes(a, dev->cus);
+  if (need == 0) return launched(launch_w4_matmul(a, nullptr, dev->cus), "gt_w4_matmul");
+  void* ws = nullptr;
+  std::mutex* mu = nullptr;
+  GT_CHECK(operator_workspace(*dev, a.stream, need, &ws, &mu));
+  std::lock_guard<std::mutex> g(*mu);
+  return launched(launch_w4_matmul(a, ws, dev->cus), "gt_w4_matmul");
 }
 
 gt_status w4_expand(const gt_w4_expand_desc* d) {
