@@ -50,6 +50,7 @@ struct NormArgs {
   int in_dtype, w_dtype, out_dtype;
   int quant;  // gt_quant
   float eps, offset, scale;
+  int cus;
   hipStream_t stream;
 };
 

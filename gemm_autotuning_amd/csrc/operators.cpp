@@ -115,6 +115,7 @@ gt_status rmsnorm(const gt_rmsnorm_desc* d) {
   a.stream = stream_of(d->stream);
   DeviceState* dev = nullptr;
   GT_CHECK(current_device(&dev));
+  a.cus = dev->cus;
   if (dev->fake) return GT_OK;
   return launched(launch_rmsnorm(a), "gt_rmsnorm");
 }
