@@ -31,6 +31,22 @@ __device__ __forceinline__ void nibble_pair(uint32_t u, int pair, float* v) {
   }
 }
 
+// Rows too short for a lane's 16 bytes (one group each): a thread to an output.
+__global__ __launch_bounds__(256) void w4_short_kernel(gt::W4Args a) {
+  for (int64_t m = blockIdx.y; m < a.M; m += gridDim.y)
+    for (int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x; n < a.w.N; n += (int64_t)gridDim.x * 256) {
+      float sum = 0.f;
+      for (int64_t k = 0; k < a.w.K; ++k) {
+        const uint32_t b = a.w.q[n * a.w.ldq + (k >> 1)];
+        const float v = a.w.format == W4_INT4 ? nibble_value<W4_INT4>(b, k & 1) : nibble_value<W4_E2M1>(b, k & 1);
+        const int64_t i = m * a.ldx + k;
+        sum += v * (a.x_dtype == DT_E4M3 ? e4m3_bits_to_f32(static_cast<const uint8_t*>(a.x)[i]) : load_any(a.x, i, a.x_dtype));
+      }
+      sum *= load_any(a.w.scales, n * a.w.lds_n, a.w.scale_dtype);
+      store_out(a.y, m * a.ldy + n, sum * a.x_scale * (a.row_scale ? a.row_scale[m] : 1.f), a.out_dtype);
+    }
+}
+
 // Expansion: out[n,k] = s[n,k/G] * v(q[n,k]) rounded once.  The stores bound
 // it (four bytes written for one read at 16 bits), so a thread makes whole
 // 16-byte stores, from a piece of E weights; a group is a whole number of
@@ -95,7 +111,7 @@ namespace {
 constexpr int kRowBlock = 64;  // rows of one launch: four blocks of 16
 
 struct W4Plan {
-  int T, C, waves, S, tiles, tiles_per_wg, chunks;
+  int T, C, waves, S, tiles, chunks;
   dim3 grid;
 };
 
@@ -105,14 +121,13 @@ bool w4_plan(const W4Args& a, int64_t rows, int cus, W4Plan* p) {
   p->chunks = (int)chunks;
   p->tiles = (int)tiles;
   p->T = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4);
-  p->C = p->T == 1 ? (chunks <= gtk::kW4Waves ? 1 : 4) : 2;
+  p->C = p->T > 1 ? 2 : (chunks <= gtk::kW4Waves ? 1 : (chunks <= 4 * gtk::kW4Waves ? 4 : 8));
   p->waves = (int)(chunks < gtk::kW4Waves ? chunks : gtk::kW4Waves);
   const int per = p->waves * p->C;
   p->S = (int)((chunks + per - 1) / per);
-  int64_t wgs = 2 * (int64_t)cus / p->S;
+  int64_t wgs = (p->C == 1 ? 2 : 1) * (int64_t)cus / p->S;
   if (wgs < 1) wgs = 1;
-  p->tiles_per_wg = (int)((tiles + wgs - 1) / wgs);
-  p->grid = dim3((unsigned)((tiles + p->tiles_per_wg - 1) / p->tiles_per_wg), (unsigned)p->S, 1);
+  p->grid = dim3((unsigned)(tiles < wgs ? tiles : wgs), (unsigned)p->S, 1);
   return p->S <= 65535 && (p->S == 1 || (int)p->grid.x <= kMaxCounterBlocks);
 }
 }  // namespace
@@ -120,11 +135,17 @@ bool w4_plan(const W4Args& a, int64_t rows, int cus, W4Plan* p) {
 size_t w4_workspace_bytes(const W4Args& a, int cus) {
   W4Plan p;
   const int64_t rows = a.M < kRowBlock ? a.M : kRowBlock;
-  if (!w4_plan(a, rows, cus, &p) || p.S == 1) return 0;
+  if (a.w.K < gtk::kW4LeastK || !w4_plan(a, rows, cus, &p) || p.S == 1) return 0;
   return kCounterRegion + (size_t)p.S * rows * a.w.N * 4;
 }
 
 int launch_w4_matmul(const W4Args& all, void* ws, int cus) {
+  if (all.w.K < gtk::kW4LeastK) {
+    const int64_t wgs = (all.w.N + 255) / 256;
+    const dim3 g((unsigned)(wgs < (1 << 22) ? wgs : 1 << 22), (unsigned)(all.M < 65535 ? all.M : 65535));
+    hipLaunchKernelGGL(gtk::w4_short_kernel, g, dim3(256), 0, all.stream, all);
+    return hipGetLastError() == hipSuccess ? LS_OK : LS_HIP_ERROR;
+  }
   for (int64_t m0 = 0; m0 < all.M; m0 += kRowBlock) {
     W4Args a = all;
     a.M = all.M - m0 < kRowBlock ? all.M - m0 : kRowBlock;
@@ -140,7 +161,6 @@ int launch_w4_matmul(const W4Args& all, void* ws, int cus) {
     p.S = pl.S;
     p.waves = pl.waves;
     p.tiles = pl.tiles;
-    p.tiles_per_wg = pl.tiles_per_wg;
     p.chunks = pl.chunks;
     const bool int4 = a.w.format == gtk::W4_INT4;
     int rc;

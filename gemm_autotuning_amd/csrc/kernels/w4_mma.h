@@ -6,15 +6,15 @@
 // everything else is arranged around that stream.  A wave owns a slice of K
 // (at most C chunks of 128) and keeps the rows' slice in registers, as the A
 // operands of 16x16x32 matrix-core blocks (T blocks of 16 rows); it then
-// walks tiles of 16 columns, loading 16 bytes per lane and chunk (a column's
-// 32 consecutive k), one tile ahead of the arithmetic.  The workgroup's waves
-// hold consecutive slices, so a tile ends with a sum over the waves in LDS;
-// when K is longer than a workgroup's slices, S workgroups share a tile and
-// the last to finish adds their partial sums in order (slices.h).
+// walks tiles of 16 columns, loading 16 bytes per lane and chunk (32
+// consecutive k of a column) D tiles ahead of the arithmetic.  The
+// workgroup's waves hold consecutive slices, so tiles end with a sum over the
+// waves in LDS, several tiles to a barrier; when K is longer than a
+// workgroup's slices, S workgroups share a tile and the last to finish adds
+// their partial sums in order (slices.h).
 //
-// The values are expanded exactly: integers through e4m3 (below), e2m1
-// through the conversion instructions.  A group's products are summed in the
-// matrix core's fp32 accumulators and the group's scale multiplies that sum.
+// The values are expanded exactly, and a group's products are summed in the
+// matrix core's fp32 accumulators before the group's scale multiplies them.
 #pragma once
 
 #include "elements.h"
@@ -24,14 +24,15 @@ namespace gtk {
 
 constexpr int kW4Waves = 8;     // most waves of a workgroup
 constexpr int kW4Chunk = 128;   // k of one 16-byte load of the four lanes of a column
+constexpr int kW4LeastK = 32;   // 16 bytes of a row: what a lane loads
 enum { W4_INT4 = 0, W4_E2M1 = 1 };
 
 struct W4Params {
   gt::W4Args a;
   float* ws;           // S x M x N partial sums (S > 1)
-  unsigned* counters;  // one per workgroup of columns and rows, zero between launches (S > 1)
+  unsigned* counters;  // one per workgroup of columns, zero between launches (S > 1)
   int S, waves;
-  int tiles, tiles_per_wg, chunks;
+  int tiles, chunks;
 };
 
 // The low nibble of each byte, two's complement, as four e4m3 bytes of value
@@ -42,268 +43,414 @@ __device__ __forceinline__ uint32_t int4_to_e4m3(uint32_t u) {
   const uint32_t t = u & 0x08080808u, one = t >> 3;
   return (((u & 0x07070707u) ^ (t - one)) + one) | (t << 4);
 }
-// The operands of one 16x16x32 matrix-core block: eight k of a lane.  Rows of
-// f16 stay f16; bf16 rows and e4m3 rows (exact in bf16) run as bf16.  The
-// 8-bit matrix-core instructions would take e4m3 rows as they are, but their
-// sums are held in fewer bits than fp32: on rows with a few large elements
-// they were off by 2^-16 of the terms' magnitudes.
+template <class V>
+__device__ __forceinline__ uint32_t bits_of(V v) {
+  uint32_t r;
+  __builtin_memcpy(&r, &v, 4);
+  return r;
+}
+
+// A row's operand of one 16x16x32 block: eight k of a lane.  f16 rows stay
+// f16 and bf16 rows bf16; e4m3 rows run as f16, which holds them exactly.
+// The 8-bit matrix-core instructions would take e4m3 rows as they are, but
+// their sums are held in fewer bits than fp32: on rows with a few large
+// elements they were off by 2^-16 of the terms' magnitudes.
 template <int XT>
 struct W4Rows {
-  static constexpr bool kF16 = XT == DT_F16;
+  static constexpr bool kF16 = XT != DT_BF16;
+  static constexpr int kBytes = XT == DT_E4M3 ? 1 : 2;
+  struct Raw {
+    uint32_t w[2 * kBytes];
+  };
   static __device__ __forceinline__ void mma(f32x4& acc, const Chunk& x, const Chunk& w) {
     if constexpr (kF16)
       Mfma16<TraitsF16>::mma(acc, x, w);
     else
       Mfma16<TraitsBF16>::mma(acc, x, w);
   }
-  template <class V>
-  static __device__ __forceinline__ uint32_t bits(V v) {
-    uint32_t r;
-    __builtin_memcpy(&r, &v, 4);
+  static __device__ __forceinline__ Raw load(const void* p, int64_t i) {
+    Raw r;
+    __builtin_memcpy(&r, static_cast<const char*>(p) + i * kBytes, sizeof(r));
     return r;
   }
-  // two e4m3 bytes times 2^e (scale = 2^e), the low or the high half of b
-  template <bool HIGH>
-  static __device__ __forceinline__ uint32_t from_e4m3(uint32_t b, float scale) {
-    if constexpr (kF16)
-      return bits(__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, scale, HIGH));
-    else
-      return bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, scale, HIGH));
+  // the elements d.. of r in front (0 <= d), zeros after them, then the
+  // first lo zeroed: both count to 8 and past it
+  static __device__ __forceinline__ Raw window(const Raw& r, int d, int lo) {
+    unsigned __int128 v = 0;
+    __builtin_memcpy(&v, &r, sizeof(r));
+    constexpr int kBits = 8 * kBytes;
+    v = d < 8 ? v >> (kBits * d) : 0;
+    if (lo > 0) v = lo < 8 ? v >> (kBits * lo) << (kBits * lo) : 0;
+    Raw o;
+    __builtin_memcpy(&o, &v, sizeof(o));
+    return o;
   }
-  // eight elements of a row, `valid` of them inside it
-  static __device__ __forceinline__ Chunk load(const void* p, int64_t i, int valid) {
-    Chunk f = {{0, 0, 0, 0}};
+  static __device__ __forceinline__ Chunk widen(const Raw& r) {
+    Chunk f;
     if constexpr (XT == DT_E4M3) {
-      const uint8_t* s = reinterpret_cast<const uint8_t*>(p) + i;
-      uint32_t b[2] = {0, 0};
-      if (valid >= 8) {
-        __builtin_memcpy(b, s, 8);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (e < valid) b[e >> 2] |= (uint32_t)s[e] << (8 * (e & 3));
-      }
-      f.w[0] = from_e4m3<false>(b[0], 1.f);
-      f.w[1] = from_e4m3<true>(b[0], 1.f);
-      f.w[2] = from_e4m3<false>(b[1], 1.f);
-      f.w[3] = from_e4m3<true>(b[1], 1.f);
+      f.w[0] = bits_of(__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(r.w[0], 1.f, false));
+      f.w[1] = bits_of(__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(r.w[0], 1.f, true));
+      f.w[2] = bits_of(__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(r.w[1], 1.f, false));
+      f.w[3] = bits_of(__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(r.w[1], 1.f, true));
     } else {
-      const uint16_t* s = reinterpret_cast<const uint16_t*>(p) + i;
-      if (valid >= 8) {
-        __builtin_memcpy(&f, s, 16);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (e < valid) f.w[e >> 1] |= (uint32_t)s[e] << (16 * (e & 1));
-      }
+      __builtin_memcpy(&f, &r, 16);
     }
     return f;
   }
 };
 
 // Eight weights from a dword of nibbles, and the rows' elements in the order
-// of k they come in.
+// of k they come in.  Instructions per dword, which the arithmetic of one row
+// block hardly hides: e2m1 four (conversions); integers with f16 rows nine;
+// with bf16 rows seven for value + 8, seventeen for the value.
 template <int XT, int FMT>
 struct W4Operand : W4Rows<XT> {
   typedef W4Rows<XT> R;
+  // the value itself
   static __device__ __forceinline__ Chunk weights(uint32_t u) {
     Chunk f;
-    if constexpr (FMT == W4_INT4) {
-      const uint32_t lo = int4_to_e4m3(u), hi = int4_to_e4m3(u >> 4);
-      f.w[0] = R::template from_e4m3<false>(lo, 512.f);
-      f.w[1] = R::template from_e4m3<true>(lo, 512.f);
-      f.w[2] = R::template from_e4m3<false>(hi, 512.f);
-      f.w[3] = R::template from_e4m3<true>(hi, 512.f);
+    if constexpr (FMT == W4_E2M1) {
+      if constexpr (R::kF16) {
+        f.w[0] = bits_of(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(u, 1.f, 0));
+        f.w[1] = bits_of(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(u, 1.f, 1));
+        f.w[2] = bits_of(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(u, 1.f, 2));
+        f.w[3] = bits_of(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(u, 1.f, 3));
+      } else {
+        f.w[0] = bits_of(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(u, 1.f, 0));
+        f.w[1] = bits_of(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(u, 1.f, 1));
+        f.w[2] = bits_of(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(u, 1.f, 2));
+        f.w[3] = bits_of(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(u, 1.f, 3));
+      }
     } else if constexpr (R::kF16) {
-      f.w[0] = R::bits(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(u, 1.f, 0));
-      f.w[1] = R::bits(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(u, 1.f, 1));
-      f.w[2] = R::bits(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(u, 1.f, 2));
-      f.w[3] = R::bits(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(u, 1.f, 3));
+      // a nibble with its sign bit flipped is value + 8; under the exponent of
+      // 1024 it adds that (or 16 times that) to 1024, and one fused step
+      // takes the rest off, exactly
+      const uint32_t h = u >> 8;
+      f.w[0] = low(u & 0x000f000fu);
+      f.w[1] = high(u & 0x00f000f0u);
+      f.w[2] = low(h & 0x000f000fu);
+      f.w[3] = high(h & 0x00f000f0u);
     } else {
-      f.w[0] = R::bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(u, 1.f, 0));
-      f.w[1] = R::bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(u, 1.f, 1));
-      f.w[2] = R::bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(u, 1.f, 2));
-      f.w[3] = R::bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(u, 1.f, 3));
+      const uint32_t lo = int4_to_e4m3(u), hi = int4_to_e4m3(u >> 4);
+      f.w[0] = bits_of(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.f, false));
+      f.w[1] = bits_of(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.f, true));
+      f.w[2] = bits_of(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.f, false));
+      f.w[3] = bits_of(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.f, true));
     }
     return f;
   }
-  // integers: the low nibbles (even k), then the high ones; e2m1: as stored
+  static __device__ __forceinline__ uint32_t low(uint32_t b) {
+    b ^= 0x64086408u;
+    f16x2v f;
+    __builtin_memcpy(&f, &b, 4);
+    return bits_of(f + f16x2v{(_Float16)-1032.f, (_Float16)-1032.f});
+  }
+  static __device__ __forceinline__ uint32_t high(uint32_t b) {
+    b ^= 0x64806480u;
+    f16x2v f;
+    __builtin_memcpy(&f, &b, 4);
+    return bits_of(__builtin_elementwise_fma(f, f16x2v{(_Float16)0.0625f, (_Float16)0.0625f},
+                                             f16x2v{(_Float16)-72.f, (_Float16)-72.f}));
+  }
+  // integers with bf16 rows: value + 8
+  static __device__ __forceinline__ Chunk weights_plus_8(uint32_t u) {
+    const uint32_t lo = (u & 0x0f0f0f0fu) ^ 0x08080808u, hi = (u >> 4 & 0x0f0f0f0fu) ^ 0x08080808u;
+    Chunk f;
+    f.w[0] = bits_of(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.f, false));
+    f.w[1] = bits_of(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.f, true));
+    f.w[2] = bits_of(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.f, false));
+    f.w[3] = bits_of(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.f, true));
+    return f;
+  }
+  // e2m1: as stored.  Integers: f16 pairs k with k + 4; bf16 takes the even
+  // k (the bytes' low nibbles), then the odd ones.
   static __device__ __forceinline__ Chunk order(const Chunk& x) {
     if constexpr (FMT == W4_E2M1) return x;
     Chunk f;
-    f.w[0] = __builtin_amdgcn_perm(x.w[1], x.w[0], 0x05040100u);
-    f.w[1] = __builtin_amdgcn_perm(x.w[3], x.w[2], 0x05040100u);
-    f.w[2] = __builtin_amdgcn_perm(x.w[1], x.w[0], 0x07060302u);
-    f.w[3] = __builtin_amdgcn_perm(x.w[3], x.w[2], 0x07060302u);
+    if constexpr (R::kF16) {
+      f.w[0] = __builtin_amdgcn_perm(x.w[2], x.w[0], 0x05040100u);
+      f.w[1] = __builtin_amdgcn_perm(x.w[2], x.w[0], 0x07060302u);
+      f.w[2] = __builtin_amdgcn_perm(x.w[3], x.w[1], 0x05040100u);
+      f.w[3] = __builtin_amdgcn_perm(x.w[3], x.w[1], 0x07060302u);
+    } else {
+      f.w[0] = __builtin_amdgcn_perm(x.w[1], x.w[0], 0x05040100u);
+      f.w[1] = __builtin_amdgcn_perm(x.w[3], x.w[2], 0x05040100u);
+      f.w[2] = __builtin_amdgcn_perm(x.w[1], x.w[0], 0x07060302u);
+      f.w[3] = __builtin_amdgcn_perm(x.w[3], x.w[2], 0x07060302u);
+    }
     return f;
   }
 };
 
-// Dwords of a 4 x 4 grid (16-lane row of the wave, index) transposed: lane
-// row r's d[j] becomes lane row j's d[r].
+// Exchanges between the wave's four rows of 16 lanes: swap32 gives a's upper
+// two rows for b's lower two, swap16 a's odd rows for b's even ones.
+__device__ __forceinline__ void swap32(uint32_t& a, uint32_t& b) {
+  const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  a = r[0];
+  b = r[1];
+}
+__device__ __forceinline__ void swap16(uint32_t& a, uint32_t& b) {
+  const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+  a = r[0];
+  b = r[1];
+}
+// Dwords of a 4 x 4 grid (lane row, index) transposed: lane row r's d[j]
+// becomes lane row j's d[r].
 __device__ __forceinline__ void transpose_lane_rows(uint32_t (&d)[4]) {
-  auto swap32 = [](uint32_t& a, uint32_t& b) {
-    const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
-    a = r[0];
-    b = r[1];
-  };
-  auto swap16 = [](uint32_t& a, uint32_t& b) {
-    const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
-    a = r[0];
-    b = r[1];
-  };
   swap32(d[0], d[2]);
   swap32(d[1], d[3]);
   swap16(d[0], d[1]);
   swap16(d[2], d[3]);
 }
 
-// What a wave loads of one tile: C chunks of its columns and their scales.
-template <int G, int C>
-struct W4Tile {
-  Chunk q[C];
-  uint32_t s[C][kW4Chunk / G];
+// What a lane loads of a chunk of a tile: 16 bytes of its column, and one of
+// the column's scales (of the group that its 32 k are in).
+struct W4Piece {
+  Chunk q;
+  uint32_t s;
 };
 
-// Bytes [0, valid) of 16 at p (the rest zero: the rows are zero there).
-__device__ __forceinline__ Chunk load_nibbles(const uint8_t* p, int valid) {
-  Chunk c = {{0, 0, 0, 0}};
-  if (valid >= 16) {
-    __builtin_memcpy(&c, p, 16);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 16; ++e)
-      if (e < valid) c.w[e >> 2] |= (uint32_t)p[e] << (8 * (e & 3));
-  }
-  return c;
-}
-
-template <int XT, int FMT, int G, int WIDE, int T, int C>
+template <int XT, int FMT, int G, int WIDE, int T, int C, int D>
 __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
   typedef W4Operand<XT, FMT> Op;
-  constexpr int kPer = kW4Chunk / G;  // groups of a chunk
-  __shared__ float red[2][kW4Waves][T][256];
+  constexpr int kPer = kW4Chunk / G;          // groups of a chunk
+  constexpr int kBatch = 4 / T < D ? 4 / T : D;  // tiles to a barrier
+  // Integers under bf16 rows: value + 8, with the accumulators started at -8
+  // times the row's sum.  Exact products either way; the sums are about three
+  // times as large.  Past two row blocks the matrix cores have no time for
+  // the second product.
+  constexpr bool kPlus8 = XT == DT_BF16 && FMT == W4_INT4 && T <= 2;
+  constexpr bool kKeepStart = kPlus8 && kPer == 1 && C < 8;  // else made again where used, for want of registers
+  static_assert(D % kBatch == 0, "a round is a whole number of batches");
+  __shared__ float red[2][kBatch][kW4Waves][T][256];
   __shared__ int is_last;
   const gt::W4Args& a = p.a;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, kq = lane >> 4;
   const int slice = blockIdx.y * p.waves + wave;
-  // the slices' chunks differ by at most one
+  // the slices' chunks differ by at most one, and so do the workgroups' tiles
   const int c0 = (int)((int64_t)slice * p.chunks / (p.S * p.waves));
   const int nc = (int)((int64_t)(slice + 1) * p.chunks / (p.S * p.waves)) - c0;
-  const int64_t m0 = (int64_t)blockIdx.z * (16 * T);
+  const int tile0 = (int)((int64_t)blockIdx.x * p.tiles / gridDim.x);
+  const int tile1 = (int)((int64_t)(blockIdx.x + 1) * p.tiles / gridDim.x);
   const int64_t K = a.w.K, N = a.w.N;
-  // the k of step j of a chunk: with one group to a chunk a lane's 32
-  // consecutive k give four steps of eight; with more, a step's 32 k must
-  // be of one group, so the dwords are exchanged between the lane rows
-  auto k_of = [&](int c, int j) { return (int64_t)(c0 + c) * kW4Chunk + (G == kW4Chunk ? 32 * kq + 8 * j : 32 * j + 8 * kq); };
+  const int rows = (int)a.M;
+
+  // A lane's 16 bytes in a chunk start at byte 16 kq of it, but end with the
+  // row: in the last chunk lanes reach back over bytes of others, and the
+  // rows' elements at those places are zero.  With one group to a chunk a
+  // lane's 32 k give four steps of eight; with more, a step's 32 k must be of
+  // one group, so the dwords are exchanged between the lane rows.
+  const int64_t row_bytes = (K + 1) / 2;
+  auto byte_of = [&](int c, int lane_row) {
+    const int64_t b = (int64_t)(c0 + c) * (kW4Chunk / 2) + 16 * lane_row;
+    return b < row_bytes - 16 ? b : row_bytes - 16;
+  };
+  auto k_of = [&](int c, int j) { return 2 * byte_of(c, G == kW4Chunk ? kq : j) + 8 * (G == kW4Chunk ? j : kq); };
+  typename Op::Raw raw[C][4][T];
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+    if (c < nc) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int64_t k = k_of(c, j);
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+          const int m = 16 * t + r;  // a row past the last is computed and not stored
+          raw[c][j][t] = Op::load(a.x, (int64_t)(m < rows ? m : rows - 1) * a.ldx + (k < K - 8 ? k : K - 8));
+        }
+      }
+    }
+
+  // A lane's places in a tile: its column's bytes and scales in the wave's
+  // first chunk.  Later chunks are constant steps on, but for the chunk that
+  // K ends in, whose lanes may have to reach back.
+  constexpr int kScale = WIDE ? 4 : 2;
+  const int groups = (int)((K + G - 1) / G), slot = kq * kPer / 4;
+  const int tail = (int64_t)(c0 + nc) * kW4Chunk > K ? nc - 1 : -1;
+  const int tail_back = tail < 0 ? 0 : (int)((int64_t)(c0 + tail) * (kW4Chunk / 2) + 16 * kq - byte_of(tail, kq));
+  const int tail_over = max((c0 + tail) * kPer + slot - (groups - 1), 0);
+  const int64_t scale_step = kPer * a.w.lds_g * kScale;
+  struct Place {
+    const uint8_t* q;
+    const char* s;
+  };
+  auto place = [&](int tile) {
+    // a column past the last is computed and not stored
+    const int64_t n = min((int64_t)tile * 16 + r, N - 1);
+    return Place{a.w.q + n * a.w.ldq + (int64_t)c0 * (kW4Chunk / 2) + 16 * kq,
+                 static_cast<const char*>(a.w.scales) + (n * a.w.lds_n + ((int64_t)c0 * kPer + slot) * a.w.lds_g) * kScale};
+  };
+  auto load_piece = [&](const Place& at, int c, W4Piece& w) {
+    const uint8_t* q = at.q + c * (kW4Chunk / 2);
+    const char* s = at.s + c * scale_step;
+    if (c == tail) {
+      q -= tail_back;
+      s -= tail_over * a.w.lds_g * kScale;
+    }
+    __builtin_memcpy(&w.q, q, 16);
+    if constexpr (WIDE)
+      w.s = *reinterpret_cast<const uint32_t*>(s);
+    else
+      w.s = *reinterpret_cast<const uint16_t*>(s);
+  };
+  W4Piece ring[D][C];
+#pragma unroll
+  for (int d = 0; d < D; ++d)
+    if (tile0 + d < tile1) {
+      const Place at = place(tile0 + d);
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+        if (c < nc) load_piece(at, c, ring[d][c]);
+    }
 
   Chunk x[C][4][T];
 #pragma unroll
-  for (int c = 0; c < C; ++c)
+  for (int c = 0; c < C; ++c) {
+    if (c < nc && (int64_t)(c0 + c + 1) * kW4Chunk > K) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int64_t k = k_of(c, j), first = (int64_t)(c0 + c) * kW4Chunk + 32 * (G == kW4Chunk ? kq : j);
+        const int d = (int)(k < K - 8 ? 0 : k - (K - 8)), lo = (int)(first - k);
+#pragma unroll
+        for (int t = 0; t < T; ++t) raw[c][j][t] = Op::window(raw[c][j][t], d, lo);
+      }
+    }
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int t = 0; t < T; ++t) {
-        const int64_t m = m0 + 16 * t + r, k = k_of(c, j);
-        const int64_t left = m < a.M && c < nc ? K - k : 0;
-        x[c][j][t] = Op::order(Op::load(a.x, m * a.ldx + k, (int)(left < 8 ? (left < 0 ? 0 : left) : 8)));
-      }
-
-  const int64_t row_bytes = (K + 1) / 2;
-  const int groups = (int)((K + G - 1) / G);
-  auto load_tile = [&](int tile, W4Tile<G, C>& w) {
-    int64_t n = (int64_t)tile * 16 + r;
-    if (n >= N) n = N - 1;  // a column past the last is computed and not stored
-    const uint8_t* q = a.w.q + n * a.w.ldq;
+      for (int t = 0; t < T; ++t) x[c][j][t] = Op::order(Op::widen(raw[c][j][t]));
+  }
+  const Chunk minus8 = {{0xc100c100u, 0xc100c100u, 0xc100c100u, 0xc100c100u}};  // bf16
+  f32x4 start[kKeepStart ? C : 1][T];
+  bool wild = false;  // an element infinite, or so large that eight times it might not be finite
+  if constexpr (kPlus8) {
+    f32x4 total[T];
+#pragma unroll
+    for (int t = 0; t < T; ++t) total[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int c = 0; c < C; ++c)
       if (c < nc) {
-        const int64_t b = (int64_t)(c0 + c) * (kW4Chunk / 2) + 16 * kq;
-        if ((int64_t)(c0 + c + 1) * kW4Chunk <= K) {
-          __builtin_memcpy(&w.q[c], q + b, 16);
-        } else {
-          const int64_t left = row_bytes - b;
-          w.q[c] = load_nibbles(q + b, (int)(left < 16 ? (left < 0 ? 0 : left) : 16));
-        }
 #pragma unroll
-        for (int g = 0; g < kPer; ++g) {
-          const int gi = (c0 + c) * kPer + g;
-          const int64_t i = n * a.w.lds_n + (gi < groups ? gi : groups - 1) * a.w.lds_g;
-          if constexpr (WIDE)
-            w.s[c][g] = reinterpret_cast<const uint32_t*>(a.w.scales)[i];
-          else
-            w.s[c][g] = reinterpret_cast<const uint16_t*>(a.w.scales)[i];
-          if (gi >= groups) w.s[c][g] = 0;  // past K: nothing times zero, whatever the last group's scale is
+        for (int t = 0; t < T; ++t) {
+          f32x4 sum = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) Op::mma(sum, x[c][j][t], minus8);
+          if constexpr (kKeepStart) start[c][t] = sum;
+          total[t] += sum;
         }
       }
-  };
-
-  const int tile0 = blockIdx.x * p.tiles_per_wg;
-  const int tile1 = min(tile0 + p.tiles_per_wg, p.tiles);
-  const bool bf16_scales = a.w.scale_dtype == DT_BF16;
-  W4Tile<G, C> cur, next;
-  load_tile(tile0, cur);
-  for (int tile = tile0; tile < tile1; ++tile) {
-    if (tile + 1 < tile1) load_tile(tile + 1, next);
-    f32x4 acc[T];
-#pragma unroll
-    for (int t = 0; t < T; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int c = 0; c < C; ++c)
-      if (c < nc) {
-        uint32_t d[4] = {cur.q[c].w[0], cur.q[c].w[1], cur.q[c].w[2], cur.q[c].w[3]};
-        if constexpr (G < kW4Chunk) transpose_lane_rows(d);
-#pragma unroll
-        for (int g = 0; g < kPer; ++g) {
-          f32x4 sum[T];
-#pragma unroll
-          for (int t = 0; t < T; ++t) sum[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int j = 0; j < 4 / kPer; ++j) {
-            const Chunk w = Op::weights(d[g * (4 / kPer) + j]);
-#pragma unroll
-            for (int t = 0; t < T; ++t) Op::mma(sum[t], x[c][g * (4 / kPer) + j][t], w);
-          }
-          const uint32_t sb = cur.s[c][g];
-          const float s = WIDE ? __uint_as_float(sb) : (bf16_scales ? bf16_bits_to_f32((uint16_t)sb) : f16_bits_to_f32((uint16_t)sb));
-#pragma unroll
-          for (int t = 0; t < T; ++t)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[t][i] += s * sum[t][i];
-        }
-      }
-    // the waves' sums of this tile; the two buffers take turns, so one
-    // barrier a tile keeps a buffer's readers ahead of its next writers
-    const int buf = (tile - tile0) & 1;
 #pragma unroll
     for (int t = 0; t < T; ++t)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) red[buf][wave][t][64 * i + lane] = acc[t][i];
-    __syncthreads();
-    for (int o = tid; o < 256 * T; o += 64 * p.waves) {
-      const int t = o >> 8, e = o & 255;
-      float v = 0.f;
-      for (int w = 0; w < p.waves; ++w) v += red[buf][w][t][e];
-      const int64_t m = m0 + 16 * t + 4 * ((e >> 4) & 3) + (e >> 6), n = (int64_t)tile * 16 + (e & 15);
-      if (m < a.M && n < N) {
-        if (p.S == 1)
-          store_out(a.y, m * a.ldy + n, v * a.x_scale * (a.row_scale ? a.row_scale[m] : 1.f), a.out_dtype);
-        else
-          __hip_atomic_store(&p.ws[((int64_t)blockIdx.y * a.M + m) * N + n], v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      for (int i = 0; i < 4; ++i) wild |= !(fabsf(total[t][i]) < 0x1p120f);
+    wild = __any(wild);
+  }
+  const bool bf16_scales = a.w.scale_dtype == DT_BF16;
+
+  int buf = 0;
+  for (int tile = tile0; tile < tile1; tile += D) {
+#pragma unroll
+    for (int b = 0; b < D; b += kBatch) {
+      if (tile + b >= tile1) break;
+#pragma unroll
+      for (int d = b; d < b + kBatch; ++d) {
+        if (tile + d >= tile1) break;
+        const bool more = tile + d + D < tile1;
+        const Place at = place(tile + d + D);
+        f32x4 acc[T];
+#pragma unroll
+        for (int t = 0; t < T; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+          if (c < nc) {
+            const W4Piece pc = ring[d][c];
+            if (more) load_piece(at, c, ring[d][c]);
+            uint32_t u[4] = {pc.q.w[0], pc.q.w[1], pc.q.w[2], pc.q.w[3]};
+            if constexpr (kPer > 1) transpose_lane_rows(u);
+            // the chunk's scales, each lane row holding those of its own k
+            uint32_t s[4];
+            s[0] = WIDE ? pc.s
+                        : __float_as_uint(bf16_scales ? bf16_bits_to_f32((uint16_t)pc.s) : f16_bits_to_f32((uint16_t)pc.s));
+            if constexpr (kPer > 1) {
+              // past K: nothing times zero, whatever the last group's scale is
+              if ((c0 + c) * kPer + slot >= groups) s[0] = 0;
+              s[kPer / 2] = s[0];
+              swap32(s[0], s[kPer / 2]);
+            }
+            if constexpr (kPer == 4) {
+              s[1] = s[0];
+              swap16(s[0], s[1]);
+              s[3] = s[2];
+              swap16(s[2], s[3]);
+            }
+#pragma unroll
+            for (int g = 0; g < kPer; ++g) {
+              constexpr int kSteps = 4 / kPer;
+              Chunk w[kSteps];
+              f32x4 sum[T];
+#pragma unroll
+              for (int t = 0; t < T; ++t) sum[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+              if (kPlus8 && !wild) {
+#pragma unroll
+                for (int j = 0; j < kSteps; ++j) w[j] = Op::weights_plus_8(u[g * kSteps + j]);
+#pragma unroll
+                for (int t = 0; t < T; ++t) {
+                  if constexpr (kKeepStart) {
+                    sum[t] = start[c][t];
+                  } else {
+#pragma unroll
+                    for (int j = 0; j < kSteps; ++j) Op::mma(sum[t], x[c][g * kSteps + j][t], minus8);
+                  }
+                }
+              } else {
+#pragma unroll
+                for (int j = 0; j < kSteps; ++j) w[j] = Op::weights(u[g * kSteps + j]);
+              }
+#pragma unroll
+              for (int j = 0; j < kSteps; ++j)
+#pragma unroll
+                for (int t = 0; t < T; ++t) Op::mma(sum[t], x[c][g * kSteps + j][t], w[j]);
+#pragma unroll
+              for (int t = 0; t < T; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[t][i] += __uint_as_float(s[g]) * sum[t][i];
+            }
+          }
+#pragma unroll
+        for (int t = 0; t < T; ++t)
+          if (16 * t + 4 * kq < rows) *reinterpret_cast<f32x4*>(&red[buf][d - b][wave][t][4 * lane]) = acc[t];
       }
+      // the waves' sums of the batch; the two buffers take turns, so one
+      // barrier a batch keeps a buffer's readers ahead of its next writers
+      __syncthreads();
+      constexpr int kCols = 16 * kBatch;
+      for (int o = tid; o < kCols * rows; o += 64 * p.waves) {
+        const int m = o / kCols, col = o % kCols;
+        const float* part = &red[buf][col >> 4][0][m >> 4][16 * (m & 12) + 4 * (col & 15) + (m & 3)];
+        float v = 0.f;
+        for (int w = 0; w < p.waves; ++w) v += part[w * (T * 256)];
+        const int64_t n = (int64_t)(tile + b) * 16 + col;
+        if (tile + b + (col >> 4) < tile1 && n < N) {
+          if (p.S == 1)
+            store_out(a.y, m * a.ldy + n, v * a.x_scale * (a.row_scale ? a.row_scale[m] : 1.f), a.out_dtype);
+          else
+            __hip_atomic_store(&p.ws[((int64_t)blockIdx.y * rows + m) * N + n], v, __ATOMIC_RELAXED,
+                               __HIP_MEMORY_SCOPE_AGENT);
+        }
+      }
+      buf ^= 1;
     }
-    cur = next;
   }
   if (p.S == 1) return;
-  unsigned* counter = p.counters + blockIdx.z * gridDim.x + blockIdx.x;
+  unsigned* counter = p.counters + blockIdx.x;
   last_slice_handshake(counter, p.S, tid, is_last);
   if (!is_last) return;
-  const int cols = (int)(min((int64_t)tile1 * 16, N) - (int64_t)tile0 * 16);
-  const int rows = (int)min((int64_t)(16 * T), a.M - m0);
+  const int64_t n0 = (int64_t)tile0 * 16;
+  const int cols = (int)(min((int64_t)tile1 * 16, N) - n0);
   for (int o = tid; o < rows * cols; o += 64 * p.waves) {
-    const int64_t m = m0 + o / cols, n = (int64_t)tile0 * 16 + o % cols;
-    const float v = sum_slices<8>(p.ws + m * N + n, a.M * N, p.S);
+    const int64_t m = o / cols, n = n0 + o % cols;
+    const float v = sum_slices<8>(p.ws + m * N + n, rows * N, p.S);
     store_out(a.y, m * a.ldy + n, v * a.x_scale * (a.row_scale ? a.row_scale[m] : 1.f), a.out_dtype);
   }
   if (tid == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -313,16 +460,17 @@ __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
 template <int XT, int FMT, int G, int WIDE>
 int w4_mma_sizes(const W4Params& p, dim3 grid, int T, int C) {
   const dim3 block(64 * p.waves);
-  if (T == 1 && C == 1)
-    hipLaunchKernelGGL((w4_mma_kernel<XT, FMT, G, WIDE, 1, 1>), grid, block, 0, p.a.stream, p);
-  else if (T == 1 && C == 4)
-    hipLaunchKernelGGL((w4_mma_kernel<XT, FMT, G, WIDE, 1, 4>), grid, block, 0, p.a.stream, p);
-  else if (T == 2 && C == 2)
-    hipLaunchKernelGGL((w4_mma_kernel<XT, FMT, G, WIDE, 2, 2>), grid, block, 0, p.a.stream, p);
-  else if (T == 4 && C == 2)
-    hipLaunchKernelGGL((w4_mma_kernel<XT, FMT, G, WIDE, 4, 2>), grid, block, 0, p.a.stream, p);
-  else
-    return gt::LS_UNSUPPORTED;
+  switch (16 * T + C) {
+#define GT_W4_SIZE(T, C, D) \
+  case 16 * T + C: hipLaunchKernelGGL((w4_mma_kernel<XT, FMT, G, WIDE, T, C, D>), grid, block, 0, p.a.stream, p); break;
+    GT_W4_SIZE(1, 1, 4)
+    GT_W4_SIZE(1, 4, 4)
+    GT_W4_SIZE(1, 8, 1)
+    GT_W4_SIZE(2, 2, 4)
+    GT_W4_SIZE(4, 2, 2)
+#undef GT_W4_SIZE
+    default: return gt::LS_UNSUPPORTED;
+  }
   return hipGetLastError() == hipSuccess ? gt::LS_OK : gt::LS_HIP_ERROR;
 }
 template <int XT, int FMT, int G>
