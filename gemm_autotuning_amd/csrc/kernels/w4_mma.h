@@ -26,6 +26,8 @@ constexpr int kW4Waves = 8;     // most waves of a workgroup
 constexpr int kW4Chunk = 128;   // k of one 16-byte load of the four lanes of a column
 constexpr int kW4LeastK = 32;   // 16 bytes of a row: what a lane loads
 enum { W4_INT4 = 0, W4_E2M1 = 1 };
+typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
+typedef u32x4 u32x4_any __attribute__((aligned(1)));  // at any byte
 
 struct W4Params {
   gt::W4Args a;
@@ -182,38 +184,27 @@ struct W4Operand : W4Rows<XT> {
   }
 };
 
-// Exchanges between the wave's four rows of 16 lanes: swap32 gives a's upper
-// two rows for b's lower two, swap16 a's odd rows for b's even ones.
-__device__ __forceinline__ void swap32(uint32_t& a, uint32_t& b) {
-  const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
-  a = r[0];
-  b = r[1];
-}
-__device__ __forceinline__ void swap16(uint32_t& a, uint32_t& b) {
-  const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
-  a = r[0];
-  b = r[1];
-}
-// Dwords of a 4 x 4 grid (lane row, index) transposed: lane row r's d[j]
-// becomes lane row j's d[r].
-__device__ __forceinline__ void transpose_lane_rows(uint32_t (&d)[4]) {
-  swap32(d[0], d[2]);
-  swap32(d[1], d[3]);
-  swap16(d[0], d[1]);
-  swap16(d[2], d[3]);
-}
-
-// What a lane loads of a chunk of a tile: 16 bytes of its column, and one of
-// the column's scales (of the group that its 32 k are in).
-struct W4Piece {
-  Chunk q;
-  uint32_t s;
+// How a wave takes a tile from memory.  The operand layout has a column to a
+// lane and neighbouring lanes in different columns, where the L1 would serve
+// each lane's 16 bytes by themselves; so a load has kLanes neighbouring lanes
+// on one column's consecutive bytes, and the pieces go through an LDS region
+// of the wave's own, whose columns lie a piece further apart than their
+// length (the reads of 16 columns fall on different banks).  A chunk's scales
+// take the same way, already as floats.
+template <int G, int C>
+struct W4Stage {
+  static constexpr int kPer = kW4Chunk / G;  // groups of a chunk
+  static constexpr int kLanes = C < 4 ? 4 * C : 16, kCols = 64 / kLanes, kRuns = 4 * C / kLanes;
+  static constexpr int kScales = C * kPer < 4 ? 1 : C * kPer / 4;  // of a lane: every fourth
+  uint32_t q[16][(4 * C + 1) * 4];
+  alignas(16) float s[16][4 * kScales + 4];
 };
 
 template <int XT, int FMT, int G, int WIDE, int T, int C, int D>
 __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
   typedef W4Operand<XT, FMT> Op;
-  constexpr int kPer = kW4Chunk / G;          // groups of a chunk
+  typedef W4Stage<G, C> Stage;
+  constexpr int kPer = Stage::kPer;
   constexpr int kBatch = 4 / T < D ? 4 / T : D;  // tiles to a barrier
   // Integers under bf16 rows: value + 8, with the accumulators started at -8
   // times the row's sum.  Exact products either way; the sums are about three
@@ -223,6 +214,7 @@ __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
   constexpr bool kKeepStart = kPlus8 && kPer == 1 && C < 8;  // else made again where used, for want of registers
   static_assert(D % kBatch == 0, "a round is a whole number of batches");
   __shared__ float red[2][kBatch][kW4Waves][T][256];
+  __shared__ Stage stages[kW4Waves];
   __shared__ int is_last;
   const gt::W4Args& a = p.a;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -240,7 +232,7 @@ __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
   // row: in the last chunk lanes reach back over bytes of others, and the
   // rows' elements at those places are zero.  With one group to a chunk a
   // lane's 32 k give four steps of eight; with more, a step's 32 k must be of
-  // one group, so the dwords are exchanged between the lane rows.
+  // one group, so lane row i takes the i-th dword of each lane's.
   const int64_t row_bytes = (K + 1) / 2;
   auto byte_of = [&](int c, int lane_row) {
     const int64_t b = (int64_t)(c0 + c) * (kW4Chunk / 2) + 16 * lane_row;
@@ -262,47 +254,62 @@ __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
       }
     }
 
-  // A lane's places in a tile: its column's bytes and scales in the wave's
-  // first chunk.  Later chunks are constant steps on, but for the chunk that
-  // K ends in, whose lanes may have to reach back.
+  Stage& stage = stages[wave];
   constexpr int kScale = WIDE ? 4 : 2;
-  const int groups = (int)((K + G - 1) / G), slot = kq * kPer / 4;
-  const int tail = (int64_t)(c0 + nc) * kW4Chunk > K ? nc - 1 : -1;
-  const int tail_back = tail < 0 ? 0 : (int)((int64_t)(c0 + tail) * (kW4Chunk / 2) + 16 * kq - byte_of(tail, kq));
-  const int tail_over = max((c0 + tail) * kPer + slot - (groups - 1), 0);
-  const int64_t scale_step = kPer * a.w.lds_g * kScale;
-  struct Place {
-    const uint8_t* q;
-    const char* s;
-  };
-  auto place = [&](int tile) {
-    // a column past the last is computed and not stored
-    const int64_t n = min((int64_t)tile * 16 + r, N - 1);
-    return Place{a.w.q + n * a.w.ldq + (int64_t)c0 * (kW4Chunk / 2) + 16 * kq,
-                 static_cast<const char*>(a.w.scales) + (n * a.w.lds_n + ((int64_t)c0 * kPer + slot) * a.w.lds_g) * kScale};
-  };
-  auto load_piece = [&](const Place& at, int c, W4Piece& w) {
-    const uint8_t* q = at.q + c * (kW4Chunk / 2);
-    const char* s = at.s + c * scale_step;
-    if (c == tail) {
-      q -= tail_back;
-      s -= tail_over * a.w.lds_g * kScale;
+  const int groups = (int)((K + G - 1) / G);
+  const int64_t ends = row_bytes - 16 - (int64_t)c0 * (kW4Chunk / 2);  // where a column's last 16 bytes start
+  auto load_tile = [&](int tile, u32x4 (&wq)[C], uint32_t (&ws)[Stage::kScales]) {
+    const int last = (int)min(N - 1 - (int64_t)tile * 16, (int64_t)15);  // a column past it is computed and not stored
+    const uint8_t* q = a.w.q + (int64_t)tile * 16 * a.w.ldq + (int64_t)c0 * (kW4Chunk / 2);
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      const int piece = i % Stage::kRuns * Stage::kLanes + lane % Stage::kLanes;
+      const int col = min(i / Stage::kRuns * Stage::kCols + lane / Stage::kLanes, last);
+      u32x4 v = {0, 0, 0, 0};
+      if (piece < 4 * nc) v = *reinterpret_cast<const u32x4_any*>(q + col * a.w.ldq + min((int64_t)(16 * piece), ends));
+      wq[i] = v;
     }
-    __builtin_memcpy(&w.q, q, 16);
-    if constexpr (WIDE)
-      w.s = *reinterpret_cast<const uint32_t*>(s);
-    else
-      w.s = *reinterpret_cast<const uint16_t*>(s);
+    const char* s = static_cast<const char*>(a.w.scales) + (int64_t)tile * 16 * a.w.lds_n * kScale;
+#pragma unroll
+    for (int i = 0; i < Stage::kScales; ++i) {
+      const int g = 4 * i + (lane & 3);
+      const char* at = s + (min(lane >> 2, last) * a.w.lds_n + min(c0 * kPer + g, groups - 1) * a.w.lds_g) * kScale;
+      uint32_t v = 0;
+      if (g < nc * kPer) {
+        if constexpr (WIDE)
+          v = *reinterpret_cast<const uint32_t*>(at);
+        else
+          v = *reinterpret_cast<const uint16_t*>(at);
+      }
+      ws[i] = v;
+    }
   };
-  W4Piece ring[D][C];
+  const bool bf16_scales = a.w.scale_dtype == DT_BF16;
+  auto stage_tile = [&](const u32x4 (&wq)[C], const uint32_t (&ws)[Stage::kScales]) {
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      const int piece = i % Stage::kRuns * Stage::kLanes + lane % Stage::kLanes;
+      const int col = i / Stage::kRuns * Stage::kCols + lane / Stage::kLanes;
+      if (piece < 4 * nc) *reinterpret_cast<u32x4*>(&stage.q[col][4 * piece]) = wq[i];
+    }
+#pragma unroll
+    for (int i = 0; i < Stage::kScales; ++i) {
+      const int g = 4 * i + (lane & 3);
+      const float f = WIDE ? __uint_as_float(ws[i])
+                           : (bf16_scales ? bf16_bits_to_f32((uint16_t)ws[i]) : f16_bits_to_f32((uint16_t)ws[i]));
+      // past K: nothing times zero, whatever the last group's scale is
+      stage.s[lane >> 2][g] = c0 * kPer + g < groups ? f : 0.f;
+    }
+    // a wave's LDS accesses are served in order; only the compiler must keep it
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  };
+  u32x4 ring_q[D][C];
+  uint32_t ring_s[D][Stage::kScales];
 #pragma unroll
   for (int d = 0; d < D; ++d)
-    if (tile0 + d < tile1) {
-      const Place at = place(tile0 + d);
-#pragma unroll
-      for (int c = 0; c < C; ++c)
-        if (c < nc) load_piece(at, c, ring[d][c]);
-    }
+    if (tile0 + d < tile1) load_tile(tile0 + d, ring_q[d], ring_s[d]);
 
   Chunk x[C][4][T];
 #pragma unroll
@@ -346,7 +353,6 @@ __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
       for (int i = 0; i < 4; ++i) wild |= !(fabsf(total[t][i]) < 0x1p120f);
     wild = __any(wild);
   }
-  const bool bf16_scales = a.w.scale_dtype == DT_BF16;
 
   int buf = 0;
   for (int tile = tile0; tile < tile1; tile += D) {
@@ -355,34 +361,21 @@ __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
       if (tile + b >= tile1) break;
 #pragma unroll
       for (int d = b; d < b + kBatch; ++d) {
-        if (tile + d >= tile1) break;
-        const bool more = tile + d + D < tile1;
-        const Place at = place(tile + d + D);
+        if (tile + d < tile1) {
+        stage_tile(ring_q[d], ring_s[d]);
+        if (tile + d + D < tile1) load_tile(tile + d + D, ring_q[d], ring_s[d]);
         f32x4 acc[T];
 #pragma unroll
         for (int t = 0; t < T; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int c = 0; c < C; ++c)
           if (c < nc) {
-            const W4Piece pc = ring[d][c];
-            if (more) load_piece(at, c, ring[d][c]);
-            uint32_t u[4] = {pc.q.w[0], pc.q.w[1], pc.q.w[2], pc.q.w[3]};
-            if constexpr (kPer > 1) transpose_lane_rows(u);
-            // the chunk's scales, each lane row holding those of its own k
-            uint32_t s[4];
-            s[0] = WIDE ? pc.s
-                        : __float_as_uint(bf16_scales ? bf16_bits_to_f32((uint16_t)pc.s) : f16_bits_to_f32((uint16_t)pc.s));
-            if constexpr (kPer > 1) {
-              // past K: nothing times zero, whatever the last group's scale is
-              if ((c0 + c) * kPer + slot >= groups) s[0] = 0;
-              s[kPer / 2] = s[0];
-              swap32(s[0], s[kPer / 2]);
-            }
-            if constexpr (kPer == 4) {
-              s[1] = s[0];
-              swap16(s[0], s[1]);
-              s[3] = s[2];
-              swap16(s[2], s[3]);
+            uint32_t u[4];
+            if constexpr (kPer == 1) {
+              __builtin_memcpy(u, &stage.q[r][4 * (4 * c + kq)], 16);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) u[j] = stage.q[r][4 * (4 * c + j) + kq];
             }
 #pragma unroll
             for (int g = 0; g < kPer; ++g) {
@@ -414,12 +407,13 @@ __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
 #pragma unroll
               for (int t = 0; t < T; ++t)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) acc[t][i] += __uint_as_float(s[g]) * sum[t][i];
+                for (int i = 0; i < 4; ++i) acc[t][i] += stage.s[r][c * kPer + g] * sum[t][i];
             }
           }
 #pragma unroll
         for (int t = 0; t < T; ++t)
           if (16 * t + 4 * kq < rows) *reinterpret_cast<f32x4*>(&red[buf][d - b][wave][t][4 * lane]) = acc[t];
+        }
       }
       // the waves' sums of the batch; the two buffers take turns, so one
       // barrier a batch keeps a buffer's readers ahead of its next writers
