@@ -61,9 +61,8 @@ template <int XT>
 struct W4Rows {
   static constexpr bool kF16 = XT != DT_BF16;
   static constexpr int kBytes = XT == DT_E4M3 ? 1 : 2;
-  struct Raw {
-    uint32_t w[2 * kBytes];
-  };
+  typedef __attribute__((ext_vector_type(2 * kBytes))) uint32_t Raw;  // eight elements
+  typedef Raw RawAny __attribute__((aligned(1)));
   static __device__ __forceinline__ void mma(f32x4& acc, const Chunk& x, const Chunk& w) {
     if constexpr (kF16)
       Mfma16<TraitsF16>::mma(acc, x, w);
@@ -71,13 +70,11 @@ struct W4Rows {
       Mfma16<TraitsBF16>::mma(acc, x, w);
   }
   static __device__ __forceinline__ Raw load(const void* p, int64_t i) {
-    Raw r;
-    __builtin_memcpy(&r, static_cast<const char*>(p) + i * kBytes, sizeof(r));
-    return r;
+    return *reinterpret_cast<const RawAny*>(static_cast<const char*>(p) + i * kBytes);
   }
   // the elements d.. of r in front (0 <= d), zeros after them, then the
   // first lo zeroed: both count to 8 and past it
-  static __device__ __forceinline__ Raw window(const Raw& r, int d, int lo) {
+  static __device__ __forceinline__ Raw window(Raw r, int d, int lo) {
     unsigned __int128 v = 0;
     __builtin_memcpy(&v, &r, sizeof(r));
     constexpr int kBits = 8 * kBytes;
@@ -87,17 +84,14 @@ struct W4Rows {
     __builtin_memcpy(&o, &v, sizeof(o));
     return o;
   }
-  static __device__ __forceinline__ Chunk widen(const Raw& r) {
-    Chunk f;
-    if constexpr (XT == DT_E4M3) {
-      f.w[0] = bits_of(__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(r.w[0], 1.f, false));
-      f.w[1] = bits_of(__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(r.w[0], 1.f, true));
-      f.w[2] = bits_of(__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(r.w[1], 1.f, false));
-      f.w[3] = bits_of(__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(r.w[1], 1.f, true));
-    } else {
-      __builtin_memcpy(&f, &r, 16);
-    }
-    return f;
+  static __device__ __forceinline__ u32x4 widen(Raw r) {
+    if constexpr (XT == DT_E4M3)
+      return u32x4{bits_of(__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(r[0], 1.f, false)),
+                   bits_of(__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(r[0], 1.f, true)),
+                   bits_of(__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(r[1], 1.f, false)),
+                   bits_of(__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(r[1], 1.f, true))};
+    else
+      return r;
   }
 };
 
@@ -166,19 +160,19 @@ struct W4Operand : W4Rows<XT> {
   }
   // e2m1: as stored.  Integers: f16 pairs k with k + 4; bf16 takes the even
   // k (the bytes' low nibbles), then the odd ones.
-  static __device__ __forceinline__ Chunk order(const Chunk& x) {
-    if constexpr (FMT == W4_E2M1) return x;
-    Chunk f;
+  static __device__ __forceinline__ Chunk order(u32x4 x) {
+    Chunk f = {{x[0], x[1], x[2], x[3]}};
+    if constexpr (FMT == W4_E2M1) return f;
     if constexpr (R::kF16) {
-      f.w[0] = __builtin_amdgcn_perm(x.w[2], x.w[0], 0x05040100u);
-      f.w[1] = __builtin_amdgcn_perm(x.w[2], x.w[0], 0x07060302u);
-      f.w[2] = __builtin_amdgcn_perm(x.w[3], x.w[1], 0x05040100u);
-      f.w[3] = __builtin_amdgcn_perm(x.w[3], x.w[1], 0x07060302u);
+      f.w[0] = __builtin_amdgcn_perm(x[2], x[0], 0x05040100u);
+      f.w[1] = __builtin_amdgcn_perm(x[2], x[0], 0x07060302u);
+      f.w[2] = __builtin_amdgcn_perm(x[3], x[1], 0x05040100u);
+      f.w[3] = __builtin_amdgcn_perm(x[3], x[1], 0x07060302u);
     } else {
-      f.w[0] = __builtin_amdgcn_perm(x.w[1], x.w[0], 0x05040100u);
-      f.w[1] = __builtin_amdgcn_perm(x.w[3], x.w[2], 0x05040100u);
-      f.w[2] = __builtin_amdgcn_perm(x.w[1], x.w[0], 0x07060302u);
-      f.w[3] = __builtin_amdgcn_perm(x.w[3], x.w[2], 0x07060302u);
+      f.w[0] = __builtin_amdgcn_perm(x[1], x[0], 0x05040100u);
+      f.w[1] = __builtin_amdgcn_perm(x[3], x[2], 0x05040100u);
+      f.w[2] = __builtin_amdgcn_perm(x[1], x[0], 0x07060302u);
+      f.w[3] = __builtin_amdgcn_perm(x[3], x[2], 0x07060302u);
     }
     return f;
   }
@@ -196,23 +190,32 @@ struct W4Stage {
   static constexpr int kPer = kW4Chunk / G;  // groups of a chunk
   static constexpr int kLanes = C < 4 ? 4 * C : 16, kCols = 64 / kLanes, kRuns = 4 * C / kLanes;
   static constexpr int kScales = C * kPer < 4 ? 1 : C * kPer / 4;  // of a lane: every fourth
-  uint32_t q[16][(4 * C + 1) * 4];
+  alignas(16) uint32_t q[16][(4 * C + 1) * 4];
   alignas(16) float s[16][4 * kScales + 4];
 };
+
+// Between LDS accesses of a wave's lanes to each other's places: the hardware
+// serves a wave's accesses in order, and the compiler must keep it.
+__device__ __forceinline__ void wave_lds_order() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
 
 template <int XT, int FMT, int G, int WIDE, int T, int C, int D>
 __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
   typedef W4Operand<XT, FMT> Op;
   typedef W4Stage<G, C> Stage;
   constexpr int kPer = Stage::kPer;
-  constexpr int kBatch = 4 / T < D ? 4 / T : D;  // tiles to a barrier
+  constexpr int kBatch = 4 / T;                     // tiles to a barrier
+  constexpr int kRound = kBatch > D ? kBatch : D;  // tiles that are unrolled
   // Integers under bf16 rows: value + 8, with the accumulators started at -8
   // times the row's sum.  Exact products either way; the sums are about three
   // times as large.  Past two row blocks the matrix cores have no time for
   // the second product.
   constexpr bool kPlus8 = XT == DT_BF16 && FMT == W4_INT4 && T <= 2;
   constexpr bool kKeepStart = kPlus8 && kPer == 1 && C < 8;  // else made again where used, for want of registers
-  static_assert(D % kBatch == 0, "a round is a whole number of batches");
+  static_assert(kRound % kBatch == 0 && kRound % D == 0, "a round is a whole number of both");
   __shared__ float red[2][kBatch][kW4Waves][T][256];
   __shared__ Stage stages[kW4Waves];
   __shared__ int is_last;
@@ -228,30 +231,30 @@ __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
   const int64_t K = a.w.K, N = a.w.N;
   const int rows = (int)a.M;
 
-  // A lane's 16 bytes in a chunk start at byte 16 kq of it, but end with the
-  // row: in the last chunk lanes reach back over bytes of others, and the
-  // rows' elements at those places are zero.  With one group to a chunk a
-  // lane's 32 k give four steps of eight; with more, a step's 32 k must be of
-  // one group, so lane row i takes the i-th dword of each lane's.
+  // The rows.  A chunk's k come in pieces of eight, and weight bytes in 16: a
+  // column's last 16 bytes end with the row, so in the last chunk they reach
+  // back over bytes that belong to others, and the rows' elements at those
+  // places are zero.  Sixteen neighbouring lanes load a row's chunk; rows past
+  // the last are zeros (their sums are computed and not stored).
   const int64_t row_bytes = (K + 1) / 2;
-  auto byte_of = [&](int c, int lane_row) {
-    const int64_t b = (int64_t)(c0 + c) * (kW4Chunk / 2) + 16 * lane_row;
-    return b < row_bytes - 16 ? b : row_bytes - 16;
+  auto k_of = [&](int c, int piece) {
+    const int64_t b = (int64_t)(c0 + c) * (kW4Chunk / 2) + 16 * (piece >> 2);
+    return 2 * (b < row_bytes - 16 ? b : row_bytes - 16) + 8 * (piece & 3);
   };
-  auto k_of = [&](int c, int j) { return 2 * byte_of(c, G == kW4Chunk ? kq : j) + 8 * (G == kW4Chunk ? j : kq); };
-  typename Op::Raw raw[C][4][T];
+  typename Op::Raw raw[C][T][4];
 #pragma unroll
   for (int c = 0; c < C; ++c)
     if (c < nc) {
+      const int64_t k = k_of(c, r);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int64_t k = k_of(c, j);
+      for (int t = 0; t < T; ++t)
 #pragma unroll
-        for (int t = 0; t < T; ++t) {
-          const int m = 16 * t + r;  // a row past the last is computed and not stored
-          raw[c][j][t] = Op::load(a.x, (int64_t)(m < rows ? m : rows - 1) * a.ldx + (k < K - 8 ? k : K - 8));
+        for (int i = 0; i < 4; ++i) {
+          typename Op::Raw v = 0;
+          const int m = 16 * t + 4 * i + kq;
+          if (m < rows) v = Op::load(a.x, m * a.ldx + (k < K - 8 ? k : K - 8));
+          raw[c][t][i] = v;
         }
-      }
     }
 
   Stage& stage = stages[wave];
@@ -300,10 +303,7 @@ __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
       // past K: nothing times zero, whatever the last group's scale is
       stage.s[lane >> 2][g] = c0 * kPer + g < groups ? f : 0.f;
     }
-    // a wave's LDS accesses are served in order; only the compiler must keep it
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    wave_lds_order();
   };
   u32x4 ring_q[D][C];
   uint32_t ring_s[D][Stage::kScales];
@@ -311,23 +311,35 @@ __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
   for (int d = 0; d < D; ++d)
     if (tile0 + d < tile1) load_tile(tile0 + d, ring_q[d], ring_s[d]);
 
+  // Into operand layout through LDS (parts of it that are still unused): a
+  // lane has row r, and of a chunk with one group its own 32 k, eight to a
+  // step; with more groups a step's 32 k must be of one group.
   Chunk x[C][4][T];
+  {
+    constexpr int kOwn = 16 * 17;  // a chunk of 16 rows, rows a piece apart
+    static_assert((C < 4 ? sizeof(red) / kW4Waves : sizeof(stage.q)) >= kOwn * 16, "it fits");
+    u32x4* own = C < 4 ? reinterpret_cast<u32x4*>(&red[0][0][0][0][0]) + wave * kOwn : reinterpret_cast<u32x4*>(&stage.q[0][0]);
 #pragma unroll
-  for (int c = 0; c < C; ++c) {
-    if (c < nc && (int64_t)(c0 + c + 1) * kW4Chunk > K) {
+    for (int c = 0; c < C; ++c)
+      if (c < nc) {
+        const bool ends_here = (int64_t)(c0 + c + 1) * kW4Chunk > K;
+        const int64_t k = k_of(c, r);
+        const int d = (int)(k < K - 8 ? 0 : k - (K - 8)), lo = (int)((int64_t)(c0 + c) * kW4Chunk + 32 * (r >> 2) - k);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int64_t k = k_of(c, j), first = (int64_t)(c0 + c) * kW4Chunk + 32 * (G == kW4Chunk ? kq : j);
-        const int d = (int)(k < K - 8 ? 0 : k - (K - 8)), lo = (int)(first - k);
+        for (int t = 0; t < T; ++t) {
 #pragma unroll
-        for (int t = 0; t < T; ++t) raw[c][j][t] = Op::window(raw[c][j][t], d, lo);
+          for (int i = 0; i < 4; ++i) {
+            if (ends_here) raw[c][t][i] = Op::window(raw[c][t][i], d, lo);
+            own[17 * (4 * i + kq) + r] = Op::widen(raw[c][t][i]);
+          }
+          wave_lds_order();
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x[c][j][t] = Op::order(own[17 * r + (kPer == 1 ? 4 * kq + j : 4 * j + kq)]);
+          wave_lds_order();
+        }
       }
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int t = 0; t < T; ++t) x[c][j][t] = Op::order(Op::widen(raw[c][j][t]));
   }
+  if constexpr (C < 4) __syncthreads();  // every wave's rows are out of the sums' part
   const Chunk minus8 = {{0xc100c100u, 0xc100c100u, 0xc100c100u, 0xc100c100u}};  // bf16
   f32x4 start[kKeepStart ? C : 1][T];
   bool wild = false;  // an element infinite, or so large that eight times it might not be finite
@@ -355,15 +367,15 @@ __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
   }
 
   int buf = 0;
-  for (int tile = tile0; tile < tile1; tile += D) {
+  for (int tile = tile0; tile < tile1; tile += kRound) {
 #pragma unroll
-    for (int b = 0; b < D; b += kBatch) {
+    for (int b = 0; b < kRound; b += kBatch) {
       if (tile + b >= tile1) break;
 #pragma unroll
       for (int d = b; d < b + kBatch; ++d) {
         if (tile + d < tile1) {
-        stage_tile(ring_q[d], ring_s[d]);
-        if (tile + d + D < tile1) load_tile(tile + d + D, ring_q[d], ring_s[d]);
+        stage_tile(ring_q[d % D], ring_s[d % D]);
+        if (tile + d + D < tile1) load_tile(tile + d + D, ring_q[d % D], ring_s[d % D]);
         f32x4 acc[T];
 #pragma unroll
         for (int t = 0; t < T; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
