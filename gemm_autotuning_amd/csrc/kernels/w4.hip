@@ -31,19 +31,23 @@ __device__ __forceinline__ void nibble_pair(uint32_t u, int pair, float* v) {
   }
 }
 
-// Rows too short for a lane's 16 bytes (one group each): a thread to an output.
-__global__ __launch_bounds__(256) void w4_short_kernel(gt::W4Args a) {
+// Rows too short for a lane's 16 bytes, or so far apart that a tile's offsets
+// pass 32 bits: a thread to an output.
+__global__ __launch_bounds__(256) void w4_plain_kernel(gt::W4Args a) {
   for (int64_t m = blockIdx.y; m < a.M; m += gridDim.y)
     for (int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x; n < a.w.N; n += (int64_t)gridDim.x * 256) {
-      float sum = 0.f;
-      for (int64_t k = 0; k < a.w.K; ++k) {
-        const uint32_t b = a.w.q[n * a.w.ldq + (k >> 1)];
-        const float v = a.w.format == W4_INT4 ? nibble_value<W4_INT4>(b, k & 1) : nibble_value<W4_E2M1>(b, k & 1);
-        const int64_t i = m * a.ldx + k;
-        sum += v * (a.x_dtype == DT_E4M3 ? e4m3_bits_to_f32(static_cast<const uint8_t*>(a.x)[i]) : load_any(a.x, i, a.x_dtype));
+      float y = 0.f;
+      for (int64_t k0 = 0; k0 < a.w.K; k0 += a.w.group) {
+        float sum = 0.f;
+        for (int64_t k = k0; k < a.w.K && k < k0 + a.w.group; ++k) {
+          const uint32_t b = a.w.q[n * a.w.ldq + (k >> 1)];
+          const float v = a.w.format == W4_INT4 ? nibble_value<W4_INT4>(b, k & 1) : nibble_value<W4_E2M1>(b, k & 1);
+          const int64_t i = m * a.ldx + k;
+          sum += v * (a.x_dtype == DT_E4M3 ? e4m3_bits_to_f32(static_cast<const uint8_t*>(a.x)[i]) : load_any(a.x, i, a.x_dtype));
+        }
+        y += sum * load_any(a.w.scales, n * a.w.lds_n + k0 / a.w.group * a.w.lds_g, a.w.scale_dtype);
       }
-      sum *= load_any(a.w.scales, n * a.w.lds_n, a.w.scale_dtype);
-      store_out(a.y, m * a.ldy + n, sum * a.x_scale * (a.row_scale ? a.row_scale[m] : 1.f), a.out_dtype);
+      store_out(a.y, m * a.ldy + n, y * a.x_scale * (a.row_scale ? a.row_scale[m] : 1.f), a.out_dtype);
     }
 }
 
@@ -110,6 +114,13 @@ namespace gt {
 namespace {
 constexpr int kRowBlock = 64;  // rows of one launch: four blocks of 16
 
+// Whether the tiles can take these weights: 16 bytes to a row at least, and
+// 16 rows (and a wave's groups of their scales) within 31-bit byte offsets.
+bool w4_tiled(const W4Weights& w) {
+  const int64_t far = 0x7fffffff;
+  return w.K >= gtk::kW4LeastK && w.ldq <= far / 32 && w.lds_n <= far / 128 && w.lds_g <= far / 4 / 64;
+}
+
 struct W4Plan {
   int T, C, waves, S, tiles, chunks;
   dim3 grid;
@@ -121,7 +132,7 @@ bool w4_plan(const W4Args& a, int64_t rows, int cus, W4Plan* p) {
   p->chunks = (int)chunks;
   p->tiles = (int)tiles;
   p->T = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4);
-  p->C = p->T > 1 ? 2 : (chunks <= gtk::kW4Waves ? 1 : (chunks <= 4 * gtk::kW4Waves ? 4 : 8));
+  p->C = chunks <= gtk::kW4Waves ? 1 : (p->T > 1 || chunks <= 2 * gtk::kW4Waves ? 2 : (chunks <= 4 * gtk::kW4Waves ? 4 : 8));
   p->waves = (int)(chunks < gtk::kW4Waves ? chunks : gtk::kW4Waves);
   const int per = p->waves * p->C;
   p->S = (int)((chunks + per - 1) / per);
@@ -135,15 +146,15 @@ bool w4_plan(const W4Args& a, int64_t rows, int cus, W4Plan* p) {
 size_t w4_workspace_bytes(const W4Args& a, int cus) {
   W4Plan p;
   const int64_t rows = a.M < kRowBlock ? a.M : kRowBlock;
-  if (a.w.K < gtk::kW4LeastK || !w4_plan(a, rows, cus, &p) || p.S == 1) return 0;
+  if (!w4_tiled(a.w) || !w4_plan(a, rows, cus, &p) || p.S == 1) return 0;
   return kCounterRegion + (size_t)p.S * rows * a.w.N * 4;
 }
 
 int launch_w4_matmul(const W4Args& all, void* ws, int cus) {
-  if (all.w.K < gtk::kW4LeastK) {
+  if (!w4_tiled(all.w)) {
     const int64_t wgs = (all.w.N + 255) / 256;
     const dim3 g((unsigned)(wgs < (1 << 22) ? wgs : 1 << 22), (unsigned)(all.M < 65535 ? all.M : 65535));
-    hipLaunchKernelGGL(gtk::w4_short_kernel, g, dim3(256), 0, all.stream, all);
+    hipLaunchKernelGGL(gtk::w4_plain_kernel, g, dim3(256), 0, all.stream, all);
     return hipGetLastError() == hipSuccess ? LS_OK : LS_HIP_ERROR;
   }
   for (int64_t m0 = 0; m0 < all.M; m0 += kRowBlock) {
@@ -161,7 +172,10 @@ int launch_w4_matmul(const W4Args& all, void* ws, int cus) {
     p.S = pl.S;
     p.waves = pl.waves;
     p.tiles = pl.tiles;
-    p.chunks = pl.chunks;
+    p.chunks_each = pl.chunks / (pl.S * pl.waves);
+    p.chunks_rest = pl.chunks % (pl.S * pl.waves);
+    p.tiles_each = pl.tiles / (int)pl.grid.x;
+    p.tiles_rest = pl.tiles % (int)pl.grid.x;
     const bool int4 = a.w.format == gtk::W4_INT4;
     int rc;
     switch (a.x_dtype) {

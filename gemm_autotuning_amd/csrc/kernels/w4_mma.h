@@ -17,6 +17,8 @@
 // matrix core's fp32 accumulators before the group's scale multiplies them.
 #pragma once
 
+#include <type_traits>
+
 #include "elements.h"
 #include "slices.h"
 
@@ -33,8 +35,9 @@ struct W4Params {
   gt::W4Args a;
   float* ws;           // S x M x N partial sums (S > 1)
   unsigned* counters;  // one per workgroup of columns, zero between launches (S > 1)
-  int S, waves;
-  int tiles, chunks;
+  int S, waves, tiles;
+  int chunks_each, chunks_rest;  // of a wave's slice: the first `rest` slices have one more
+  int tiles_each, tiles_rest;    // of a workgroup
 };
 
 // The low nibble of each byte, two's complement, as four e4m3 bytes of value
@@ -222,94 +225,107 @@ __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
   const gt::W4Args& a = p.a;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, kq = lane >> 4;
-  const int slice = blockIdx.y * p.waves + wave;
-  // the slices' chunks differ by at most one, and so do the workgroups' tiles
-  const int c0 = (int)((int64_t)slice * p.chunks / (p.S * p.waves));
-  const int nc = (int)((int64_t)(slice + 1) * p.chunks / (p.S * p.waves)) - c0;
-  const int tile0 = (int)((int64_t)blockIdx.x * p.tiles / gridDim.x);
-  const int tile1 = (int)((int64_t)(blockIdx.x + 1) * p.tiles / gridDim.x);
+  const int slice = blockIdx.y * p.waves + wave, wg = blockIdx.x;
+  // the slices' chunks differ by at most one, and so do the workgroups'
+  // tiles; a slice has at least C / 2 chunks and at most C
+  const int c0 = slice * p.chunks_each + min(slice, p.chunks_rest), nc = p.chunks_each + (slice < p.chunks_rest);
+  const int tile0 = wg * p.tiles_each + min(wg, p.tiles_rest), tile1 = tile0 + p.tiles_each + (wg < p.tiles_rest);
   const int64_t K = a.w.K, N = a.w.N;
   const int rows = (int)a.M;
 
   // The rows.  A chunk's k come in pieces of eight, and weight bytes in 16: a
   // column's last 16 bytes end with the row, so in the last chunk they reach
   // back over bytes that belong to others, and the rows' elements at those
-  // places are zero.  Sixteen neighbouring lanes load a row's chunk; rows past
-  // the last are zeros (their sums are computed and not stored).
+  // places are zero.  Sixteen neighbouring lanes load a row's chunk; a row
+  // past the last is computed and not stored.
+  //
+  // No load is under a condition (what there is nothing for reads a place
+  // that is read anyway): the wait for one then leaves the later ones in
+  // flight, where a load that may not have happened would mean a wait for all.
+  //
+  // The wave's first chunk here is its slice's last (then the others in
+  // order), so that the special case is in one place of the code.
   const int64_t row_bytes = (K + 1) / 2;
+  auto chunk = [&](int c) { return c0 + (c ? c - 1 : nc - 1); };
   auto k_of = [&](int c, int piece) {
-    const int64_t b = (int64_t)(c0 + c) * (kW4Chunk / 2) + 16 * (piece >> 2);
+    const int64_t b = (int64_t)chunk(c) * (kW4Chunk / 2) + 16 * (piece >> 2);
     return 2 * (b < row_bytes - 16 ? b : row_bytes - 16) + 8 * (piece & 3);
   };
   typename Op::Raw raw[C][T][4];
 #pragma unroll
-  for (int c = 0; c < C; ++c)
-    if (c < nc) {
-      const int64_t k = k_of(c, r);
+  for (int c = 0; c < C; ++c) {
+    const int64_t k = k_of(c, r);
 #pragma unroll
-      for (int t = 0; t < T; ++t)
+    for (int t = 0; t < T; ++t)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          typename Op::Raw v = 0;
-          const int m = 16 * t + 4 * i + kq;
-          if (m < rows) v = Op::load(a.x, m * a.ldx + (k < K - 8 ? k : K - 8));
-          raw[c][t][i] = v;
-        }
-    }
+      for (int i = 0; i < 4; ++i)
+        raw[c][t][i] = Op::load(a.x, min(16 * t + 4 * i + kq, rows - 1) * a.ldx + (k < K - 8 ? k : K - 8));
+    if (C == 8) __builtin_amdgcn_sched_barrier(0);  // registers: no addresses of later chunks yet
+  }
 
   Stage& stage = stages[wave];
   constexpr int kScale = WIDE ? 4 : 2;
-  const int groups = (int)((K + G - 1) / G);
-  const int64_t ends = row_bytes - 16 - (int64_t)c0 * (kW4Chunk / 2);  // where a column's last 16 bytes start
-  auto load_tile = [&](int tile, u32x4 (&wq)[C], uint32_t (&ws)[Stage::kScales]) {
-    const int last = (int)min(N - 1 - (int64_t)tile * 16, (int64_t)15);  // a column past it is computed and not stored
-    const uint8_t* q = a.w.q + (int64_t)tile * 16 * a.w.ldq + (int64_t)c0 * (kW4Chunk / 2);
+  const int groups = (int)((K + G - 1) / G), g0 = c0 * kPer;
+  const int64_t b0 = min((int64_t)c0 * (kW4Chunk / 2), row_bytes - 16);
+  const uint32_t ldq = (uint32_t)a.w.ldq, lds_n = (uint32_t)a.w.lds_n * kScale, lds_g = (uint32_t)a.w.lds_g * kScale;
+  uint32_t q_off[Stage::kRuns];  // the lane's bytes of its first column
+#pragma unroll
+  for (int i = 0; i < Stage::kRuns; ++i) {
+    const int piece = i * Stage::kLanes + lane % Stage::kLanes;
+    q_off[i] = (uint32_t)(min((int64_t)chunk(piece >> 2) * (kW4Chunk / 2) + 16 * (piece & 3), row_bytes - 16) - b0) +
+               lane / Stage::kLanes * ldq;
+  }
+  auto group = [&](int i) {  // of the slice's: that of the lane's i-th scale
+    const int g = 4 * i + (lane & 3);
+    return g < kPer ? (nc - 1) * kPer + g : g - kPer;
+  };
+  const uint32_t s_most = (uint32_t)min(groups - 1 - g0, 4 * Stage::kScales) * lds_g;
+  auto load_tile = [&](int tile, u32x4 (&wq)[C], uint32_t (&ws)[Stage::kScales]) __attribute__((always_inline)) {
+    const bool some = tile < tile1;
+    const int64_t n = (int64_t)(some ? tile : tile1 - 1) * 16;
+    const uint32_t last = (uint32_t)min(N - 1 - n, (int64_t)15);  // a column past it is computed and not stored
+    const uint8_t* q = a.w.q + n * a.w.ldq + b0;
+    uint32_t most[Stage::kRuns];
+#pragma unroll
+    for (int i = 0; i < Stage::kRuns; ++i)
+      most[i] = some && i * Stage::kLanes + lane % Stage::kLanes < 4 * nc ? (last - lane / Stage::kLanes) * ldq + q_off[i] : 0;
+    uint32_t step = ldq * Stage::kCols;
+    if constexpr (C == 8) asm("" : "+s"(step));  // registers: the sums below are not kept from tile to tile
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-      const int piece = i % Stage::kRuns * Stage::kLanes + lane % Stage::kLanes;
-      const int col = min(i / Stage::kRuns * Stage::kCols + lane / Stage::kLanes, last);
-      u32x4 v = {0, 0, 0, 0};
-      if (piece < 4 * nc) v = *reinterpret_cast<const u32x4_any*>(q + col * a.w.ldq + min((int64_t)(16 * piece), ends));
-      wq[i] = v;
+      const int run = i % Stage::kRuns;
+      wq[i] = *reinterpret_cast<const u32x4_any*>(q + min(i / Stage::kRuns * step + q_off[run], most[run]));
     }
-    const char* s = static_cast<const char*>(a.w.scales) + (int64_t)tile * 16 * a.w.lds_n * kScale;
+    const char* s = static_cast<const char*>(a.w.scales) + (n * a.w.lds_n + g0 * a.w.lds_g) * kScale;
+    const uint32_t col = min((uint32_t)lane >> 2, last) * lds_n;
 #pragma unroll
     for (int i = 0; i < Stage::kScales; ++i) {
-      const int g = 4 * i + (lane & 3);
-      const char* at = s + (min(lane >> 2, last) * a.w.lds_n + min(c0 * kPer + g, groups - 1) * a.w.lds_g) * kScale;
-      uint32_t v = 0;
-      if (g < nc * kPer) {
-        if constexpr (WIDE)
-          v = *reinterpret_cast<const uint32_t*>(at);
-        else
-          v = *reinterpret_cast<const uint16_t*>(at);
-      }
-      ws[i] = v;
+      const char* at = s + (some ? col + min(group(i) * lds_g, s_most) : 0);
+      if constexpr (WIDE)
+        ws[i] = *reinterpret_cast<const uint32_t*>(at);
+      else
+        ws[i] = *reinterpret_cast<const uint16_t*>(at);
     }
   };
   const bool bf16_scales = a.w.scale_dtype == DT_BF16;
-  auto stage_tile = [&](const u32x4 (&wq)[C], const uint32_t (&ws)[Stage::kScales]) {
+  auto stage_tile = [&](const u32x4 (&wq)[C], const uint32_t (&ws)[Stage::kScales]) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < C; ++i) {
-      const int piece = i % Stage::kRuns * Stage::kLanes + lane % Stage::kLanes;
-      const int col = i / Stage::kRuns * Stage::kCols + lane / Stage::kLanes;
-      if (piece < 4 * nc) *reinterpret_cast<u32x4*>(&stage.q[col][4 * piece]) = wq[i];
-    }
+    for (int i = 0; i < C; ++i)
+      *reinterpret_cast<u32x4*>(&stage.q[i / Stage::kRuns * Stage::kCols + lane / Stage::kLanes]
+                                        [4 * (i % Stage::kRuns * Stage::kLanes + lane % Stage::kLanes)]) = wq[i];
 #pragma unroll
     for (int i = 0; i < Stage::kScales; ++i) {
-      const int g = 4 * i + (lane & 3);
       const float f = WIDE ? __uint_as_float(ws[i])
                            : (bf16_scales ? bf16_bits_to_f32((uint16_t)ws[i]) : f16_bits_to_f32((uint16_t)ws[i]));
       // past K: nothing times zero, whatever the last group's scale is
-      stage.s[lane >> 2][g] = c0 * kPer + g < groups ? f : 0.f;
+      stage.s[lane >> 2][4 * i + (lane & 3)] = g0 + group(i) < groups ? f : 0.f;
     }
     wave_lds_order();
   };
   u32x4 ring_q[D][C];
   uint32_t ring_s[D][Stage::kScales];
 #pragma unroll
-  for (int d = 0; d < D; ++d)
-    if (tile0 + d < tile1) load_tile(tile0 + d, ring_q[d], ring_s[d]);
+  for (int d = 0; d < D; ++d) load_tile(tile0 + d, ring_q[d], ring_s[d]);
 
   // Into operand layout through LDS (parts of it that are still unused): a
   // lane has row r, and of a chunk with one group its own 32 k, eight to a
@@ -320,24 +336,24 @@ __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
     static_assert((C < 4 ? sizeof(red) / kW4Waves : sizeof(stage.q)) >= kOwn * 16, "it fits");
     u32x4* own = C < 4 ? reinterpret_cast<u32x4*>(&red[0][0][0][0][0]) + wave * kOwn : reinterpret_cast<u32x4*>(&stage.q[0][0]);
 #pragma unroll
-    for (int c = 0; c < C; ++c)
-      if (c < nc) {
-        const bool ends_here = (int64_t)(c0 + c + 1) * kW4Chunk > K;
-        const int64_t k = k_of(c, r);
-        const int d = (int)(k < K - 8 ? 0 : k - (K - 8)), lo = (int)((int64_t)(c0 + c) * kW4Chunk + 32 * (r >> 2) - k);
+    for (int c = 0; c < C; ++c) {
 #pragma unroll
-        for (int t = 0; t < T; ++t) {
+      for (int t = 0; t < T; ++t) {
+        if (c == 0 && (int64_t)(chunk(0) + 1) * kW4Chunk > K) {
+          const int64_t k = k_of(0, r);
+          const int d = (int)(k < K - 8 ? 0 : k - (K - 8)), lo = (int)((int64_t)chunk(0) * kW4Chunk + 32 * (r >> 2) - k);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (ends_here) raw[c][t][i] = Op::window(raw[c][t][i], d, lo);
-            own[17 * (4 * i + kq) + r] = Op::widen(raw[c][t][i]);
-          }
-          wave_lds_order();
-#pragma unroll
-          for (int j = 0; j < 4; ++j) x[c][j][t] = Op::order(own[17 * r + (kPer == 1 ? 4 * kq + j : 4 * j + kq)]);
-          wave_lds_order();
+          for (int i = 0; i < 4; ++i) raw[c][t][i] = Op::window(raw[c][t][i], d, lo);
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) own[17 * (4 * i + kq) + r] = Op::widen(raw[c][t][i]);
+        wave_lds_order();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[c][j][t] = Op::order(own[17 * r + (kPer == 1 ? 4 * kq + j : 4 * j + kq)]);
+        wave_lds_order();
       }
+      if (C == 8) __builtin_amdgcn_sched_barrier(0);
+    }
   }
   if constexpr (C < 4) __syncthreads();  // every wave's rows are out of the sums' part
   const Chunk minus8 = {{0xc100c100u, 0xc100c100u, 0xc100c100u, 0xc100c100u}};  // bf16
@@ -348,17 +364,16 @@ __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
 #pragma unroll
     for (int t = 0; t < T; ++t) total[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int c = 0; c < C; ++c)
-      if (c < nc) {
+    for (int c = 0; c < C; ++c) {
 #pragma unroll
-        for (int t = 0; t < T; ++t) {
-          f32x4 sum = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int t = 0; t < T; ++t) {
+        f32x4 sum = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) Op::mma(sum, x[c][j][t], minus8);
-          if constexpr (kKeepStart) start[c][t] = sum;
-          total[t] += sum;
-        }
+        for (int j = 0; j < 4; ++j) Op::mma(sum, x[c][j][t], minus8);
+        if constexpr (kKeepStart) start[c][t] = sum;
+        if (c < nc) total[t] += sum;
       }
+    }
 #pragma unroll
     for (int t = 0; t < T; ++t)
 #pragma unroll
@@ -366,88 +381,108 @@ __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
     wild = __any(wild);
   }
 
-  int buf = 0;
-  for (int tile = tile0; tile < tile1; tile += kRound) {
+  // the staged tile's sums over this wave's k, into LDS
+  auto multiply = [&](auto plus8, float (&out)[kW4Waves][T][256]) __attribute__((always_inline)) {
+    f32x4 acc[T];
 #pragma unroll
-    for (int b = 0; b < kRound; b += kBatch) {
-      if (tile + b >= tile1) break;
+    for (int t = 0; t < T; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int d = b; d < b + kBatch; ++d) {
-        if (tile + d < tile1) {
-        stage_tile(ring_q[d % D], ring_s[d % D]);
-        if (tile + d + D < tile1) load_tile(tile + d + D, ring_q[d % D], ring_s[d % D]);
-        f32x4 acc[T];
+    for (int c = 0; c < C; ++c)
+      if (c < C / 2 || c < nc) {
+        uint32_t u[4];
+        if constexpr (kPer == 1) {
+          __builtin_memcpy(u, &stage.q[r][4 * (4 * c + kq)], 16);
+        } else {
 #pragma unroll
-        for (int t = 0; t < T; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+          for (int j = 0; j < 4; ++j) u[j] = stage.q[r][4 * (4 * c + j) + kq];
+        }
 #pragma unroll
-        for (int c = 0; c < C; ++c)
-          if (c < nc) {
-            uint32_t u[4];
-            if constexpr (kPer == 1) {
-              __builtin_memcpy(u, &stage.q[r][4 * (4 * c + kq)], 16);
-            } else {
+        for (int g = 0; g < kPer; ++g) {
+          constexpr int kSteps = 4 / kPer;
+          f32x4 sum[T];
 #pragma unroll
-              for (int j = 0; j < 4; ++j) u[j] = stage.q[r][4 * (4 * c + j) + kq];
-            }
+          for (int t = 0; t < T; ++t) {
+            sum[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+            if constexpr (plus8 && kKeepStart) {
+              sum[t] = start[c][t];
+            } else if constexpr (plus8) {
 #pragma unroll
-            for (int g = 0; g < kPer; ++g) {
-              constexpr int kSteps = 4 / kPer;
-              Chunk w[kSteps];
-              f32x4 sum[T];
-#pragma unroll
-              for (int t = 0; t < T; ++t) sum[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-              if (kPlus8 && !wild) {
-#pragma unroll
-                for (int j = 0; j < kSteps; ++j) w[j] = Op::weights_plus_8(u[g * kSteps + j]);
-#pragma unroll
-                for (int t = 0; t < T; ++t) {
-                  if constexpr (kKeepStart) {
-                    sum[t] = start[c][t];
-                  } else {
-#pragma unroll
-                    for (int j = 0; j < kSteps; ++j) Op::mma(sum[t], x[c][g * kSteps + j][t], minus8);
-                  }
-                }
-              } else {
-#pragma unroll
-                for (int j = 0; j < kSteps; ++j) w[j] = Op::weights(u[g * kSteps + j]);
-              }
-#pragma unroll
-              for (int j = 0; j < kSteps; ++j)
-#pragma unroll
-                for (int t = 0; t < T; ++t) Op::mma(sum[t], x[c][g * kSteps + j][t], w[j]);
-#pragma unroll
-              for (int t = 0; t < T; ++t)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[t][i] += stage.s[r][c * kPer + g] * sum[t][i];
+              for (int j = 0; j < kSteps; ++j) Op::mma(sum[t], x[c][g * kSteps + j][t], minus8);
             }
           }
 #pragma unroll
-        for (int t = 0; t < T; ++t)
-          if (16 * t + 4 * kq < rows) *reinterpret_cast<f32x4*>(&red[buf][d - b][wave][t][4 * lane]) = acc[t];
+          for (int j = 0; j < kSteps; ++j) {
+            const uint32_t v = u[g * kSteps + j];
+            const Chunk w = plus8 ? Op::weights_plus_8(v) : Op::weights(v);
+#pragma unroll
+            for (int t = 0; t < T; ++t) Op::mma(sum[t], x[c][g * kSteps + j][t], w);
+          }
+#pragma unroll
+          for (int t = 0; t < T; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[t][i] += stage.s[r][c * kPer + g] * sum[t][i];
         }
+        // registers: no more than one or two chunks' reads and expansions at once
+        if (C == 8 && (c & 1 || kPer == 4)) __builtin_amdgcn_sched_barrier(0);
       }
-      // the waves' sums of the batch; the two buffers take turns, so one
-      // barrier a batch keeps a buffer's readers ahead of its next writers
-      __syncthreads();
-      constexpr int kCols = 16 * kBatch;
-      for (int o = tid; o < kCols * rows; o += 64 * p.waves) {
-        const int m = o / kCols, col = o % kCols;
-        const float* part = &red[buf][col >> 4][0][m >> 4][16 * (m & 12) + 4 * (col & 15) + (m & 3)];
-        float v = 0.f;
-        for (int w = 0; w < p.waves; ++w) v += part[w * (T * 256)];
-        const int64_t n = (int64_t)(tile + b) * 16 + col;
-        if (tile + b + (col >> 4) < tile1 && n < N) {
-          if (p.S == 1)
-            store_out(a.y, m * a.ldy + n, v * a.x_scale * (a.row_scale ? a.row_scale[m] : 1.f), a.out_dtype);
-          else
-            __hip_atomic_store(&p.ws[((int64_t)blockIdx.y * rows + m) * N + n], v, __ATOMIC_RELAXED,
-                               __HIP_MEMORY_SCOPE_AGENT);
-        }
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+      if (16 * t + 4 * kq < rows) *reinterpret_cast<f32x4*>(&out[wave][t][4 * lane]) = acc[t];
+  };
+  auto multiply_tile = [&](float (&out)[kW4Waves][T][256]) __attribute__((always_inline)) {
+    if constexpr (kPlus8) {
+      if (!wild) return multiply(std::true_type(), out);
+    }
+    multiply(std::false_type(), out);
+  };
+  // The waves' sums of a batch of tiles.  The two buffers take turns, so one
+  // barrier a batch keeps a buffer's readers ahead of its next writers.
+  int buf = 0;
+  auto join = [&](int tile) __attribute__((always_inline)) {
+    __syncthreads();
+    constexpr int kCols = 16 * kBatch;
+    for (int o = tid; o < kCols * rows; o += 64 * p.waves) {
+      const int m = o / kCols, col = o % kCols;
+      const float* part = &red[buf][col >> 4][0][m >> 4][16 * (m & 12) + 4 * (col & 15) + (m & 3)];
+      float v = 0.f;
+      for (int w = 0; w < p.waves; ++w) v += part[w * (T * 256)];
+      const int64_t n = (int64_t)tile * 16 + col;
+      if (tile + (col >> 4) < tile1 && n < N) {
+        if (p.S == 1)
+          store_out(a.y, m * a.ldy + n, v * a.x_scale * (a.row_scale ? a.row_scale[m] : 1.f), a.out_dtype);
+        else
+          __hip_atomic_store(&p.ws[((int64_t)blockIdx.y * rows + m) * N + n], v, __ATOMIC_RELAXED,
+                             __HIP_MEMORY_SCOPE_AGENT);
       }
-      buf ^= 1;
+    }
+    buf ^= 1;
+  };
+
+  int tile = tile0;
+  for (; tile + kRound <= tile1; tile += kRound) {
+#pragma unroll
+    for (int b = 0; b < kRound; b += kBatch) {
+#pragma unroll
+      for (int d = b; d < b + kBatch; ++d) {
+        stage_tile(ring_q[d % D], ring_s[d % D]);
+        load_tile(tile + d + D, ring_q[d % D], ring_s[d % D]);
+        multiply_tile(red[buf][d - b]);
+      }
+      join(tile + b);
     }
   }
+#pragma unroll
+  for (int b = 0; b < kRound; b += kBatch)
+    if (tile + b < tile1) {
+#pragma unroll
+      for (int d = b; d < b + kBatch; ++d)
+        if (tile + d < tile1) {
+          stage_tile(ring_q[d % D], ring_s[d % D]);
+          if constexpr (D < kRound) load_tile(tile + d + D, ring_q[d % D], ring_s[d % D]);
+          multiply_tile(red[buf][d - b]);
+        }
+      join(tile + b);
+    }
   if (p.S == 1) return;
   unsigned* counter = p.counters + blockIdx.x;
   last_slice_handshake(counter, p.S, tid, is_last);
@@ -470,9 +505,12 @@ int w4_mma_sizes(const W4Params& p, dim3 grid, int T, int C) {
 #define GT_W4_SIZE(T, C, D) \
   case 16 * T + C: hipLaunchKernelGGL((w4_mma_kernel<XT, FMT, G, WIDE, T, C, D>), grid, block, 0, p.a.stream, p); break;
     GT_W4_SIZE(1, 1, 4)
-    GT_W4_SIZE(1, 4, 4)
+    GT_W4_SIZE(1, 2, 4)
+    GT_W4_SIZE(1, 4, 2)
     GT_W4_SIZE(1, 8, 1)
+    GT_W4_SIZE(2, 1, 4)
     GT_W4_SIZE(2, 2, 4)
+    GT_W4_SIZE(4, 1, 2)
     GT_W4_SIZE(4, 2, 2)
 #undef GT_W4_SIZE
     default: return gt::LS_UNSUPPORTED;
