@@ -147,7 +147,7 @@ size_t w4_workspace_bytes(const W4Args& a, int cus) {
   W4Plan p;
   const int64_t rows = a.M < kRowBlock ? a.M : kRowBlock;
   if (!w4_tiled(a.w) || !w4_plan(a, rows, cus, &p) || p.S == 1) return 0;
-  return kCounterRegion + (size_t)p.S * rows * a.w.N * 4;
+  return kCounterRegion + (size_t)p.S * rows * p.tiles * 64;
 }
 
 int launch_w4_matmul(const W4Args& all, void* ws, int cus) {
@@ -169,6 +169,7 @@ int launch_w4_matmul(const W4Args& all, void* ws, int cus) {
     p.a = a;
     p.counters = static_cast<unsigned*>(ws);
     p.ws = ws ? reinterpret_cast<float*>(static_cast<char*>(ws) + kCounterRegion) : nullptr;
+    p.ws_ld = (int64_t)pl.tiles * 16;
     p.S = pl.S;
     p.waves = pl.waves;
     p.tiles = pl.tiles;
