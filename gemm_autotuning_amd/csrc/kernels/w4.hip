@@ -51,6 +51,30 @@ __global__ __launch_bounds__(256) void w4_plain_kernel(gt::W4Args a) {
     }
 }
 
+// The slices' partial sums, four columns to a thread.  A launch of its own:
+// joined by the last workgroup of a column block inside the product's launch,
+// the sums of 61 x 11001 x 4100 were left to 85 CUs and took 10 us.
+__global__ __launch_bounds__(256) void w4_join_kernel(W4Params p) {
+  const gt::W4Args& a = p.a;
+  const int64_t n = 4 * ((int64_t)blockIdx.x * 256 + threadIdx.x), m = blockIdx.y;
+  if (n >= a.w.N) return;
+  const float* at = p.ws + m * p.ws_ld + n;  // columns past N, up to a tile, are in the workspace
+  const int64_t stride = a.M * p.ws_ld;
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+  for (int q0 = 0; q0 < p.S; q0 += 4) {
+    f32x4 part[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) part[j] = *reinterpret_cast<const f32x4*>(at + min(q0 + j, p.S - 1) * stride);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (q0 + j < p.S) v += part[j];
+  }
+  const float f = a.row_scale ? a.row_scale[m] : 1.f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (n + e < a.w.N) store_out(a.y, m * a.ldy + n + e, v[e] * a.x_scale * f, a.out_dtype);
+}
+
 // Expansion: out[n,k] = s[n,k/G] * v(q[n,k]) rounded once.  The stores bound
 // it (four bytes written for one read at 16 bits), so a thread makes whole
 // 16-byte stores, from a piece of E weights; a group is a whole number of
@@ -139,7 +163,7 @@ bool w4_plan(const W4Args& a, int64_t rows, int cus, W4Plan* p) {
   int64_t wgs = (p->C == 1 ? 2 : 1) * (int64_t)cus / p->S;
   if (wgs < 1) wgs = 1;
   p->grid = dim3((unsigned)(tiles < wgs ? tiles : wgs), (unsigned)p->S, 1);
-  return p->S <= 65535 && (p->S == 1 || (int)p->grid.x <= kMaxCounterBlocks);
+  return p->S <= 65535;
 }
 }  // namespace
 
@@ -167,7 +191,6 @@ int launch_w4_matmul(const W4Args& all, void* ws, int cus) {
     if (!w4_plan(a, a.M, cus, &pl)) return LS_UNSUPPORTED;
     gtk::W4Params p;
     p.a = a;
-    p.counters = static_cast<unsigned*>(ws);
     p.ws = ws ? reinterpret_cast<float*>(static_cast<char*>(ws) + kCounterRegion) : nullptr;
     p.ws_ld = (int64_t)pl.tiles * 16;
     p.S = pl.S;
@@ -185,6 +208,10 @@ int launch_w4_matmul(const W4Args& all, void* ws, int cus) {
       default: rc = int4 ? w4_mma_e4m3_int4(p, pl.grid, pl.T, pl.C) : w4_mma_e4m3_e2m1(p, pl.grid, pl.T, pl.C); break;
     }
     if (rc != LS_OK) return rc;
+    if (p.S > 1) {
+      hipLaunchKernelGGL(gtk::w4_join_kernel, dim3((unsigned)((a.w.N + 1023) / 1024), (unsigned)a.M), dim3(256), 0, a.stream, p);
+      if (hipGetLastError() != hipSuccess) return LS_HIP_ERROR;
+    }
   }
   return LS_OK;
 }

@@ -10,8 +10,8 @@
 // consecutive k of a column) D tiles ahead of the arithmetic.  The
 // workgroup's waves hold consecutive slices, so tiles end with a sum over the
 // waves in LDS, several tiles to a barrier; when K is longer than a
-// workgroup's slices, S workgroups share a tile and the last to finish adds
-// their partial sums in order (slices.h).
+// workgroup's slices, S workgroups share a tile and a second launch adds
+// their partial sums in order.
 //
 // The values are expanded exactly, and a group's products are summed in the
 // matrix core's fp32 accumulators before the group's scale multiplies them.
@@ -20,7 +20,6 @@
 #include <type_traits>
 
 #include "elements.h"
-#include "slices.h"
 
 namespace gtk {
 
@@ -35,7 +34,6 @@ struct W4Params {
   gt::W4Args a;
   float* ws;           // S x M x ws_ld partial sums (S > 1)
   int64_t ws_ld;       // N rounded up to whole tiles
-  unsigned* counters;  // one per workgroup of columns, zero between launches (S > 1)
   int S, waves, tiles;
   int chunks_each, chunks_rest;  // of a wave's slice: the first `rest` slices have one more
   int tiles_each, tiles_rest;    // of a workgroup
@@ -189,8 +187,9 @@ struct W4Operand : W4Rows<XT> {
 // of the wave's own, whose columns lie a piece further apart than their
 // length (the reads of 16 columns fall on different banks).  A chunk's scales
 // take the same way, already as floats.
-template <int G, int C>
+template <int G, int C, int WIDE>
 struct W4Stage {
+  typedef typename std::conditional<WIDE, uint32_t, uint16_t>::type Scale;
   static constexpr int kPer = kW4Chunk / G;  // groups of a chunk
   static constexpr int kLanes = C < 4 ? 4 * C : 16, kCols = 64 / kLanes, kRuns = 4 * C / kLanes;
   static constexpr int kScales = C * kPer < 4 ? 1 : C * kPer / 4;  // of a lane: every fourth
@@ -209,9 +208,9 @@ __device__ __forceinline__ void wave_lds_order() {
 template <int XT, int FMT, int G, int WIDE, int T, int C, int D>
 __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
   typedef W4Operand<XT, FMT> Op;
-  typedef W4Stage<G, C> Stage;
+  typedef W4Stage<G, C, WIDE> Stage;
   constexpr int kPer = Stage::kPer;
-  constexpr int kBatch = 4 / T;                     // tiles to a barrier
+  constexpr int kBatch = T == 4 ? 2 : 4;           // tiles to a barrier
   constexpr int kRound = kBatch > D ? kBatch : D;  // tiles that are unrolled
   // Integers under bf16 rows: value + 8, with the accumulators started at -8
   // times the row's sum.  Exact products either way; the sums are about three
@@ -220,9 +219,8 @@ __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
   constexpr bool kPlus8 = XT == DT_BF16 && FMT == W4_INT4 && T <= 2;
   constexpr bool kKeepStart = kPlus8 && kPer == 1 && C < 8;  // else made again where used, for want of registers
   static_assert(kRound % kBatch == 0 && kRound % D == 0, "a round is a whole number of both");
-  __shared__ float red[2][kBatch][kW4Waves][T][256];
+  __shared__ float red[kW4Waves][2][kBatch][T][256];
   __shared__ Stage stages[kW4Waves];
-  __shared__ int is_last;
   const gt::W4Args& a = p.a;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, kq = lane >> 4;
@@ -265,7 +263,7 @@ __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
   }
 
   Stage& stage = stages[wave];
-  constexpr int kScale = WIDE ? 4 : 2;
+  constexpr int kScale = sizeof(typename Stage::Scale);
   const int groups = (int)((K + G - 1) / G), g0 = c0 * kPer;
   const int64_t b0 = min((int64_t)c0 * (kW4Chunk / 2), row_bytes - 16);
   const uint32_t ldq = (uint32_t)a.w.ldq, lds_n = (uint32_t)a.w.lds_n * kScale, lds_g = (uint32_t)a.w.lds_g * kScale;
@@ -281,15 +279,24 @@ __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
     return g < kPer ? (nc - 1) * kPer + g : g - kPer;
   };
   const uint32_t s_most = (uint32_t)min(groups - 1 - g0, 4 * Stage::kScales) * lds_g;
-  auto load_tile = [&](int tile, u32x4 (&wq)[C], uint32_t (&ws)[Stage::kScales]) __attribute__((always_inline)) {
-    const bool some = tile < tile1;
-    const int64_t n = (int64_t)(some ? tile : tile1 - 1) * 16;
-    const uint32_t last = (uint32_t)min(N - 1 - n, (int64_t)15);  // a column past it is computed and not stored
-    const uint8_t* q = a.w.q + n * a.w.ldq + b0;
+  const uint8_t* const q0 = a.w.q + (int64_t)tile0 * 16 * a.w.ldq + b0;
+  const char* const s0 =
+      static_cast<const char*>(a.w.scales) + ((int64_t)tile0 * 16 * a.w.lds_n + g0 * a.w.lds_g) * kScale;
+  const uint8_t* q_next = q0;
+  const char* s_next = s0;
+  // the workgroup's next tile; past its last, the first bytes of its first
+  auto load_tile = [&](int tile, u32x4 (&wq)[C], typename Stage::Scale (&ws)[Stage::kScales]) __attribute__((always_inline)) {
+    const uint32_t some = tile < tile1 ? ~0u : 0u;
+    const uint32_t last = tile == p.tiles - 1 ? (uint32_t)(N - 1) & 15u : 15u;  // a column past it is computed and not stored
+    const uint8_t* q = some ? q_next : q0;
+    const char* s = some ? s_next : s0;
+    q_next += 16 * a.w.ldq;
+    s_next += 16 * a.w.lds_n * kScale;
     uint32_t most[Stage::kRuns];
 #pragma unroll
     for (int i = 0; i < Stage::kRuns; ++i)
-      most[i] = some && i * Stage::kLanes + lane % Stage::kLanes < 4 * nc ? (last - lane / Stage::kLanes) * ldq + q_off[i] : 0;
+      most[i] = ((last - lane / Stage::kLanes) * ldq + q_off[i]) &
+                (i * Stage::kLanes + lane % Stage::kLanes < 4 * nc ? some : 0u);
     uint32_t step = ldq * Stage::kCols;
     if constexpr (C == 8) asm("" : "+s"(step));  // registers: the sums below are not kept from tile to tile
 #pragma unroll
@@ -297,45 +304,51 @@ __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
       const int run = i % Stage::kRuns;
       wq[i] = *reinterpret_cast<const u32x4_any*>(q + min(i / Stage::kRuns * step + q_off[run], most[run]));
     }
-    const char* s = static_cast<const char*>(a.w.scales) + (n * a.w.lds_n + g0 * a.w.lds_g) * kScale;
     const uint32_t col = min((uint32_t)lane >> 2, last) * lds_n;
 #pragma unroll
     for (int i = 0; i < Stage::kScales; ++i) {
-      const char* at = s + (some ? col + min(group(i) * lds_g, s_most) : 0);
-      if constexpr (WIDE)
-        ws[i] = *reinterpret_cast<const uint32_t*>(at);
-      else
-        ws[i] = *reinterpret_cast<const uint16_t*>(at);
+      const uint32_t off = (col + min(group(i) * lds_g, s_most)) & some;
+      ws[i] = *reinterpret_cast<const typename Stage::Scale*>(s + off);
     }
   };
-  const bool bf16_scales = a.w.scale_dtype == DT_BF16;
-  auto stage_tile = [&](const u32x4 (&wq)[C], const uint32_t (&ws)[Stage::kScales]) __attribute__((always_inline)) {
+  const uint32_t bf16_scales = a.w.scale_dtype == DT_BF16 ? ~0u : 0u;
+  auto stage_tile = [&](const u32x4 (&wq)[C], const typename Stage::Scale (&ws)[Stage::kScales]) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < C; ++i)
       *reinterpret_cast<u32x4*>(&stage.q[i / Stage::kRuns * Stage::kCols + lane / Stage::kLanes]
                                         [4 * (i % Stage::kRuns * Stage::kLanes + lane % Stage::kLanes)]) = wq[i];
 #pragma unroll
     for (int i = 0; i < Stage::kScales; ++i) {
-      const float f = WIDE ? __uint_as_float(ws[i])
-                           : (bf16_scales ? bf16_bits_to_f32((uint16_t)ws[i]) : f16_bits_to_f32((uint16_t)ws[i]));
+      typename Stage::Scale b = ws[i];
+      asm volatile("" : "+v"(b));  // converted here and not where it was loaded, which would wait for it there
+      float f;
+      if constexpr (WIDE)
+        f = __uint_as_float(b);
+      else  // both conversions and a selection by bits: a branch here would split the tile's code
+        f = __uint_as_float(((uint32_t)b << 16 & bf16_scales) | (__float_as_uint(f16_bits_to_f32(b)) & ~bf16_scales));
       // past K: nothing times zero, whatever the last group's scale is
       stage.s[lane >> 2][4 * i + (lane & 3)] = g0 + group(i) < groups ? f : 0.f;
     }
     wave_lds_order();
   };
   u32x4 ring_q[D][C];
-  uint32_t ring_s[D][Stage::kScales];
+  typename Stage::Scale ring_s[D][Stage::kScales];
 #pragma unroll
   for (int d = 0; d < D; ++d) load_tile(tile0 + d, ring_q[d], ring_s[d]);
+  // a tile is staged before its turn, so that the load that takes its place
+  // in the ring is under way
+  stage_tile(ring_q[0], ring_s[0]);
+  load_tile(tile0 + D, ring_q[0], ring_s[0]);
 
-  // Into operand layout through LDS (parts of it that are still unused): a
+  // Into operand layout through LDS (the wave's part of the sums, still
+  // unused): a
   // lane has row r, and of a chunk with one group its own 32 k, eight to a
   // step; with more groups a step's 32 k must be of one group.
   Chunk x[C][4][T];
   {
     constexpr int kOwn = 16 * 17;  // a chunk of 16 rows, rows a piece apart
-    static_assert((C < 4 ? sizeof(red) / kW4Waves : sizeof(stage.q)) >= kOwn * 16, "it fits");
-    u32x4* own = C < 4 ? reinterpret_cast<u32x4*>(&red[0][0][0][0][0]) + wave * kOwn : reinterpret_cast<u32x4*>(&stage.q[0][0]);
+    static_assert(sizeof(red[0]) >= kOwn * 16, "it fits");
+    u32x4* own = reinterpret_cast<u32x4*>(&red[wave][0][0][0][0]);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
 #pragma unroll
@@ -356,7 +369,6 @@ __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
       if (C == 8) __builtin_amdgcn_sched_barrier(0);
     }
   }
-  if constexpr (C < 4) __syncthreads();  // every wave's rows are out of the sums' part
   const Chunk minus8 = {{0xc100c100u, 0xc100c100u, 0xc100c100u, 0xc100c100u}};  // bf16
   f32x4 start[kKeepStart ? C : 1][T];
   bool wild = false;  // an element infinite, or so large that eight times it might not be finite
@@ -383,7 +395,7 @@ __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
   }
 
   // the staged tile's sums over this wave's k, into LDS
-  auto multiply = [&](auto plus8, float (&out)[kW4Waves][T][256]) __attribute__((always_inline)) {
+  auto multiply = [&](auto plus8, float (&out)[T][256]) __attribute__((always_inline)) {
     f32x4 acc[T];
 #pragma unroll
     for (int t = 0; t < T; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -428,9 +440,9 @@ __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
       }
 #pragma unroll
     for (int t = 0; t < T; ++t)
-      if (16 * t + 4 * kq < rows) *reinterpret_cast<f32x4*>(&out[wave][t][4 * lane]) = acc[t];
+      if (16 * t + 4 * kq < rows) *reinterpret_cast<f32x4*>(&out[t][4 * lane]) = acc[t];
   };
-  auto multiply_tile = [&](float (&out)[kW4Waves][T][256]) __attribute__((always_inline)) {
+  auto multiply_tile = [&](float (&out)[T][256]) __attribute__((always_inline)) {
     if constexpr (kPlus8) {
       if (!wild) return multiply(std::true_type(), out);
     }
@@ -444,16 +456,18 @@ __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
     constexpr int kCols = 16 * kBatch;
     for (int o = tid; o < kCols * rows; o += 64 * p.waves) {
       const int m = o / kCols, col = o % kCols;
-      const float* part = &red[buf][col >> 4][0][m >> 4][16 * (m & 12) + 4 * (col & 15) + (m & 3)];
-      float v = 0.f;
-      for (int w = 0; w < p.waves; ++w) v += part[w * (T * 256)];
+      const float* part = &red[0][buf][col >> 4][m >> 4][16 * (m & 12) + 4 * (col & 15) + (m & 3)];
+      float v = 0.f, waves[kW4Waves];
+#pragma unroll
+      for (int w = 0; w < kW4Waves; ++w) waves[w] = part[w * (2 * kBatch * T * 256)];
+#pragma unroll
+      for (int w = 0; w < kW4Waves; ++w) v += w < p.waves ? waves[w] : 0.f;
       const int64_t n = (int64_t)tile * 16 + col;
       if (tile + (col >> 4) < tile1 && n < N) {
         if (p.S == 1)
           store_out(a.y, m * a.ldy + n, v * a.x_scale * (a.row_scale ? a.row_scale[m] : 1.f), a.out_dtype);
         else
-          __hip_atomic_store(&p.ws[((int64_t)blockIdx.y * rows + m) * p.ws_ld + n], v, __ATOMIC_RELAXED,
-                             __HIP_MEMORY_SCOPE_AGENT);
+          p.ws[((int64_t)blockIdx.y * rows + m) * p.ws_ld + n] = v;
       }
     }
     buf ^= 1;
@@ -465,9 +479,9 @@ __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
     for (int b = 0; b < kRound; b += kBatch) {
 #pragma unroll
       for (int d = b; d < b + kBatch; ++d) {
-        stage_tile(ring_q[d % D], ring_s[d % D]);
-        load_tile(tile + d + D, ring_q[d % D], ring_s[d % D]);
-        multiply_tile(red[buf][d - b]);
+        multiply_tile(red[wave][buf][d - b]);
+        stage_tile(ring_q[(d + 1) % D], ring_s[(d + 1) % D]);
+        load_tile(tile + d + 1 + D, ring_q[(d + 1) % D], ring_s[(d + 1) % D]);
       }
       join(tile + b);
     }
@@ -478,47 +492,12 @@ __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
 #pragma unroll
       for (int d = b; d < b + kBatch; ++d)
         if (tile + d < tile1) {
-          stage_tile(ring_q[d % D], ring_s[d % D]);
-          if constexpr (D < kRound) load_tile(tile + d + D, ring_q[d % D], ring_s[d % D]);
-          multiply_tile(red[buf][d - b]);
+          multiply_tile(red[wave][buf][d - b]);
+          stage_tile(ring_q[(d + 1) % D], ring_s[(d + 1) % D]);
+          if constexpr (D < kRound) load_tile(tile + d + 1 + D, ring_q[(d + 1) % D], ring_s[(d + 1) % D]);
         }
       join(tile + b);
     }
-  if (p.S == 1) return;
-  unsigned* counter = p.counters + blockIdx.x;
-  last_slice_handshake(counter, p.S, tid, is_last);
-  if (!is_last) return;
-  // Four columns to a thread and four such quads of its in flight, or the sum
-  // is a memory round trip after another (61 x 11001 x 4100: 23 of 43 us).
-  const int64_t n0 = (int64_t)tile0 * 16;
-  const int quads = 4 * (tile1 - tile0), stride = 64 * p.waves;
-  typedef f32x4 f32x4_any __attribute__((aligned(4)));
-  for (int o0 = tid; o0 < rows * quads; o0 += 4 * stride) {
-    f32x4 v[4];
-    const float* at[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      // past the end the last again; a tile's columns past N are in the workspace
-      const int o = min(o0 + i * stride, rows * quads - 1);
-      at[i] = p.ws + (int64_t)(o / quads) * p.ws_ld + n0 + 4 * (o % quads);
-      v[i] = *reinterpret_cast<const f32x4_any*>(at[i]);
-    }
-    for (int q = 1; q < p.S; ++q)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] += *reinterpret_cast<const f32x4_any*>(at[i] + q * (rows * p.ws_ld));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int o = o0 + i * stride;
-      const int64_t m = o / quads, n = n0 + 4 * (o % quads);
-      if (o < rows * quads) {
-        const float f = a.row_scale ? a.row_scale[m] : 1.f;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (n + e < N) store_out(a.y, m * a.ldy + n + e, v[i][e] * a.x_scale * f, a.out_dtype);
-      }
-    }
-  }
-  if (tid == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
 // Launch for rows of type XT; T and C as chosen by the caller.
