@@ -210,17 +210,18 @@ __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
   typedef W4Operand<XT, FMT> Op;
   typedef W4Stage<G, C, WIDE> Stage;
   constexpr int kPer = Stage::kPer;
-  constexpr int kBatch = T == 4 ? 2 : 4;           // tiles to a barrier
+  constexpr int kBatch = T == 4 || C == 8 ? 2 : 4;  // tiles to a barrier
   constexpr int kRound = kBatch > D ? kBatch : D;  // tiles that are unrolled
   // Integers under bf16 rows: value + 8, with the accumulators started at -8
-  // times the row's sum.  Exact products either way; the sums are about three
-  // times as large.  Past two row blocks the matrix cores have no time for
-  // the second product.
-  constexpr bool kPlus8 = XT == DT_BF16 && FMT == W4_INT4 && T <= 2;
-  constexpr bool kKeepStart = kPlus8 && kPer == 1 && C < 8;  // else made again where used, for want of registers
+  // times the row's sum over the group (four row blocks of small groups have
+  // no LDS for those).  Exact products either way; the sums are about three
+  // times as large.
+  constexpr bool kPlus8 = XT == DT_BF16 && FMT == W4_INT4 && (T < 4 || kPer < 4);
+  constexpr bool kKeepStarts = kPlus8 && C * kPer < 32;  // else multiplied again for each tile, for want of registers
   static_assert(kRound % kBatch == 0 && kRound % D == 0, "a round is a whole number of both");
   __shared__ float red[kW4Waves][2][kBatch][T][256];
   __shared__ Stage stages[kW4Waves];
+  __shared__ f32x4 starts[kKeepStarts ? kW4Waves : 1][C * kPer][T][4];  // of the rows 4 kq.. in a group
   const gt::W4Args& a = p.a;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, kq = lane >> 4;
@@ -346,8 +347,8 @@ __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
   // step; with more groups a step's 32 k must be of one group.
   Chunk x[C][4][T];
   {
-    constexpr int kOwn = 16 * 17;  // a chunk of 16 rows, rows a piece apart
-    static_assert(sizeof(red[0]) >= kOwn * 16, "it fits");
+    static_assert(sizeof(red[0]) >= 16 * 16 * sizeof(u32x4), "a chunk of 16 rows fits");
+    auto place = [](int row, int piece) { return 16 * row + (piece ^ row); };  // a piece of all rows on different banks
     u32x4* own = reinterpret_cast<u32x4*>(&red[wave][0][0][0][0]);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -360,17 +361,16 @@ __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
           for (int i = 0; i < 4; ++i) raw[c][t][i] = Op::window(raw[c][t][i], d, lo);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) own[17 * (4 * i + kq) + r] = Op::widen(raw[c][t][i]);
+        for (int i = 0; i < 4; ++i) own[place(4 * i + kq, r)] = Op::widen(raw[c][t][i]);
         wave_lds_order();
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[c][j][t] = Op::order(own[17 * r + (kPer == 1 ? 4 * kq + j : 4 * j + kq)]);
+        for (int j = 0; j < 4; ++j) x[c][j][t] = Op::order(own[place(r, kPer == 1 ? 4 * kq + j : 4 * j + kq)]);
         wave_lds_order();
       }
       if (C == 8) __builtin_amdgcn_sched_barrier(0);
     }
   }
   const Chunk minus8 = {{0xc100c100u, 0xc100c100u, 0xc100c100u, 0xc100c100u}};  // bf16
-  f32x4 start[kKeepStart ? C : 1][T];
   bool wild = false;  // an element infinite, or so large that eight times it might not be finite
   if constexpr (kPlus8) {
     f32x4 total[T];
@@ -379,14 +379,18 @@ __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
 #pragma unroll
     for (int c = 0; c < C; ++c) {
 #pragma unroll
-      for (int t = 0; t < T; ++t) {
-        f32x4 sum = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int g = 0; g < kPer; ++g)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) Op::mma(sum, x[c][j][t], minus8);
-        if constexpr (kKeepStart) start[c][t] = sum;
-        if (c < nc) total[t] += sum;
-      }
+        for (int t = 0; t < T; ++t) {
+          f32x4 sum = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int j = 0; j < 4 / kPer; ++j) Op::mma(sum, x[c][g * (4 / kPer) + j][t], minus8);
+          if (kKeepStarts && r == 0) starts[wave][c * kPer + g][t][kq] = sum;
+          if (c < nc) total[t] += sum;
+        }
+      if (C == 8) __builtin_amdgcn_sched_barrier(0);
     }
+    wave_lds_order();
 #pragma unroll
     for (int t = 0; t < T; ++t)
 #pragma unroll
@@ -416,8 +420,8 @@ __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
 #pragma unroll
           for (int t = 0; t < T; ++t) {
             sum[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-            if constexpr (plus8 && kKeepStart) {
-              sum[t] = start[c][t];
+            if constexpr (plus8 && kKeepStarts) {
+              sum[t] = starts[wave][c * kPer + g][t][kq];
             } else if constexpr (plus8) {
 #pragma unroll
               for (int j = 0; j < kSteps; ++j) Op::mma(sum[t], x[c][g * kSteps + j][t], minus8);
@@ -436,7 +440,7 @@ __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
             for (int i = 0; i < 4; ++i) acc[t][i] += stage.s[r][c * kPer + g] * sum[t][i];
         }
         // registers: no more than one or two chunks' reads and expansions at once
-        if (C == 8 && (c & 1 || kPer == 4)) __builtin_amdgcn_sched_barrier(0);
+        if (C == 8 && kPer == 4) __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
     for (int t = 0; t < T; ++t)
