@@ -51,6 +51,7 @@ struct NormArgs {
   int quant;  // gt_quant
   float eps, offset, scale;
   int cus;
+  bool past_caches;  // set by the launcher: more than the last-level cache passes by
   hipStream_t stream;
 };
 
@@ -69,6 +70,8 @@ struct NormBwdArgs {
   float offset;
   float* ws;
   int cus;
+  int dw_blocks;  // set by the launcher: workgroups that take columns of dw
+  bool past_caches;
   hipStream_t stream;
 };
 
@@ -94,6 +97,7 @@ struct W4ExpandArgs {
   void* y;
   int64_t ldy;
   int out_dtype;
+  bool past_caches;
   hipStream_t stream;
 };
 

@@ -69,6 +69,12 @@ struct Piece {
     for (int i = 0; i < kWords; ++i) w[i] = 0;
   }
   __device__ __forceinline__ void load(const T* p) { __builtin_memcpy(w, p, sizeof(w)); }
+  __device__ __forceinline__ void set(int e, T v) {  // of a cleared piece
+    if constexpr (DT == DT_F32)
+      w[e] = __float_as_uint(v);
+    else
+      w[e / 2] |= (uint32_t)v << (16 * (e & 1));
+  }
   __device__ __forceinline__ float get(int e) const {
     if constexpr (DT == DT_F32) return __uint_as_float(w[e]);
     if constexpr (DT == DT_BF16) return __uint_as_float((e & 1) ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
@@ -76,10 +82,12 @@ struct Piece {
   }
 };
 
-// E floats rounded to DT and stored.
+// E floats rounded to DT and stored; past the caches where the call writes
+// more than they hold for its reader (kPastCaches).
 template <int DT, int E>
-__device__ __forceinline__ void store_piece(typename Elem<DT>::T* p, const float* v) {
-  uint32_t w[E * (int)sizeof(*p) / 4];
+__device__ __forceinline__ void store_piece(typename Elem<DT>::T* p, const float* v, bool past_caches = false) {
+  constexpr int kWords = E * (int)sizeof(*p) / 4;
+  uint32_t w[kWords];
   if constexpr (DT == DT_F32) {
 #pragma unroll
     for (int e = 0; e < E; ++e) w[e] = __float_as_uint(v[e]);
@@ -102,8 +110,24 @@ __device__ __forceinline__ void store_piece(typename Elem<DT>::T* p, const float
       }
     }
   }
-  __builtin_memcpy(p, w, sizeof(w));
+  if (past_caches) {
+    typedef __attribute__((ext_vector_type(kWords))) uint32_t words;
+    typedef words words_any __attribute__((aligned(1)));
+    words t;
+    __builtin_memcpy(&t, w, sizeof(w));
+    __builtin_nontemporal_store(t, reinterpret_cast<words_any*>(p));
+  } else {
+    __builtin_memcpy(p, w, sizeof(w));
+  }
 }
+
+// Bytes that a call reads and writes from which on its results are stored
+// past the caches.  The last-level cache holds 256 MB: below, a reader that
+// follows finds them there (11000 x 8192 expanded to bf16, then a product of
+// 512 rows: 126 us, 137 past the caches); above, they only drive each other
+// out (12000 x 8192: 154 and 145, 14000 x 8192: 187 and 161).
+constexpr double kPastCaches = 240e6;
+
 // E weights from n on, of a type known at run time.
 template <int E>
 __device__ __forceinline__ void load_weights(const void* p, unsigned n, int dtype, float* out) {

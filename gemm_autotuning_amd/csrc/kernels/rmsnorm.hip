@@ -109,7 +109,7 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void rmsnorm_kernel(gt::NormAr
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         const unsigned n = (t + c * NT) * E;
-        if (n < whole) store_piece<IN, E>(s + n, h + c * E);
+        if (n < whole) store_piece<IN, E>(s + n, h + c * E, a.past_caches);
       }
       if (last < N) s[last] = Elem<IN>::put(hl);
     }
@@ -149,7 +149,7 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void rmsnorm_kernel(gt::NormAr
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const unsigned n = (t + c * NT) * E;
-      if (n < whole) store_piece<OUT, E>(y + n, h + c * E);
+      if (n < whole) store_piece<OUT, E>(y + n, h + c * E, a.past_caches);
     }
     if (last < N) y[last] = Elem<OUT>::put(hl);
   }
@@ -213,7 +213,76 @@ __global__ __launch_bounds__(kLongNT) void rmsnorm_long_kernel(gt::NormArgs a) {
 // columns, so dw's partial sums stay in registers and go to the workspace
 // once (blocks x N floats), where rmsnorm_join_kernel adds them in block
 // order.  Where registers allow, a row's successor is loaded while the row's
-// mean is joined.
+// mean is joined.  8192 x 4096 bf16 with dsum: 51.8 us, 5.2 TB/s.
+//
+// That second launch is most of the time of a small gradient (500 x 1000 f16:
+// 7.0 us of both, 4.0 of one launch).  Where a workgroup reads 32 columns of
+// all rows in about the time a launch takes, the first dw_blocks workgroups
+// do that instead, and the others only make dx.
+constexpr unsigned kDwCols = 32;
+template <int IN, int DY, int THREADS>
+__device__ void dw_columns(const gt::NormBwdArgs& a, unsigned block) {
+  constexpr unsigned E = 16 / sizeof(typename Elem<IN>::T), kLanes = kDwCols / E, kAt = THREADS / kLanes, kSegs = THREADS / kDwCols;
+  typedef typename Elem<IN>::T TI;
+  typedef typename Elem<DY>::T TD;
+  __shared__ float part[kAt][kDwCols + 1];
+  __shared__ float segs[kSegs][kDwCols];
+  const unsigned t = threadIdx.x, N = (unsigned)a.N, M = (unsigned)a.M;
+  const unsigned n = block * kDwCols + t % kLanes * E;
+  float s[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) s[e] = 0.f;
+  for (unsigned m0 = t / kLanes; m0 < M; m0 += 4 * kAt) {
+    Piece<IN, E> h[4];
+    Piece<DY, E> dy[4];
+    float rstd[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const unsigned m = min(m0 + i * kAt, M - 1);
+      h[i].clear();
+      dy[i].clear();
+      if (n + E <= N) {
+        h[i].load(reinterpret_cast<const TI*>(a.h) + m * a.ldh + n);
+        dy[i].load(reinterpret_cast<const TD*>(a.dy) + m * a.lddy + n);
+      }
+      rstd[i] = a.rstd[m];
+    }
+    if (N % E && block == N / kDwCols) {  // after every whole piece's load is under way
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (n < N && n + E > N) {
+          const unsigned m = min(m0 + i * kAt, M - 1);
+#pragma unroll
+          for (int e = 0; e < E; ++e)
+            if (n + e < N) {
+              h[i].set(e, reinterpret_cast<const TI*>(a.h)[m * a.ldh + n + e]);
+              dy[i].set(e, reinterpret_cast<const TD*>(a.dy)[m * a.lddy + n + e]);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (m0 + i * kAt < M)
+#pragma unroll
+        for (int e = 0; e < E; ++e) s[e] += dy[i].get(e) * (h[i].get(e) * rstd[i]);
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) part[t / kLanes][t % kLanes * E + e] = s[e];
+  __syncthreads();
+  const unsigned col = t % kDwCols, seg = t / kDwCols;
+  float v = 0.f;
+#pragma unroll
+  for (int i = 0; i < kAt / kSegs; ++i) v += part[seg * (kAt / kSegs) + i][col];
+  segs[seg][col] = v;
+  __syncthreads();
+  if (seg == 0 && block * kDwCols + col < N) {
+    v = 0.f;
+#pragma unroll
+    for (int i = 0; i < kSegs; ++i) v += segs[i][col];
+    store_out(a.dw, block * kDwCols + col, v, a.dw_dtype);
+  }
+}
+
 template <int IN, int DY, int NT, int C>
 __global__ __launch_bounds__(NT < 256 ? 256 : NT) void rmsnorm_bwd_kernel(gt::NormBwdArgs a) {
   constexpr int kRows = NT < 256 ? 256 / NT : 1;
@@ -233,6 +302,8 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void rmsnorm_bwd_kernel(gt::No
     TD dyl;
     float rstd;
   };
+  if (blockIdx.x < (unsigned)a.dw_blocks) return dw_columns<IN, DY, (NT < 256 ? 256 : NT)>(a, blockIdx.x);
+  const unsigned block = blockIdx.x - a.dw_blocks, blocks = gridDim.x - a.dw_blocks;
   auto load = [&](int64_t m, Raw& v) {
     const TI* h = reinterpret_cast<const TI*>(a.h) + m * a.ldh;
     const TD* dy = reinterpret_cast<const TD*>(a.dy) + m * a.lddy;
@@ -264,8 +335,8 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void rmsnorm_bwd_kernel(gt::No
     }
     v.rstd = a.rstd[m];
   };
-  const int64_t step = (int64_t)gridDim.x * kRows;
-  int64_t m = (int64_t)blockIdx.x * kRows + threadIdx.x / NT;
+  const int64_t step = (int64_t)blocks * kRows;
+  int64_t m = (int64_t)block * kRows + threadIdx.x / NT;
   Raw v;
   if (m < a.M) load(m, v);
   float w[C][E], dw[C * E], wl = 1.f, dwl = 0.f;
@@ -311,7 +382,7 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void rmsnorm_bwd_kernel(gt::No
           const float g = v.dy[c].get(e) * w[c][e], n = v.h[c].get(e) * v.rstd;
           o[e] = v.rstd * (g - n * mean) + v.ds[c].get(e);
         }
-        if (i < whole) store_piece<IN, E>(dx + i, o);
+        if (i < whole) store_piece<IN, E>(dx + i, o, a.past_caches);
       }
       if (last < N) dx[last] = Elem<IN>::put(v.rstd * (dyl * wl - nl * mean) + Elem<IN>::get(v.dsl));
     }
@@ -320,7 +391,7 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void rmsnorm_bwd_kernel(gt::No
     else if (m + step < a.M)
       load(m + step, v);
   }
-  if (!a.dw) return;
+  if (!a.dw || a.dw_blocks) return;
   if constexpr (kRows > 1) {  // the workgroup's rows first, in order
     constexpr unsigned kSpan = C * E * NT + E;
     float* mine = joined + (threadIdx.x / NT) * kSpan;
@@ -485,8 +556,6 @@ int norm_in(const NormArgs& a) {
   }
 }
 
-// Workgroups of the backward pass: each leaves N partial sums of dw, so they
-// are as few as keep the memory busy.
 // Longest rows that the one-pass kernel holds: h, dy, dsum, w and dw of a row
 // in the registers of 512 threads (f32 rows have half the elements a piece).
 bool bwd_long(const NormBwdArgs& a) { return a.N > 16384; }
@@ -494,11 +563,23 @@ RowShape bwd_shape(const NormBwdArgs& a) {
   const RowShape s = row_shape(a.N, a.M, elem_bytes(a.in_dtype), 0);
   return s.NT == 1024 ? RowShape{512, 8} : s;
 }
+// Workgroups of the backward pass: each leaves N partial sums of dw, so they
+// are as few as keep the memory busy.
 int bwd_blocks(const NormBwdArgs& a) {
   if (bwd_long(a)) return (int)(a.M < 64 ? a.M : 64);
   const RowShape s = bwd_shape(a);
-  const int64_t b = ceil_div(a.M, s.NT < 256 ? 256 / s.NT : 1), most = (int64_t)a.cus * (s.NT >= 512 ? 2 : 4);
+  // 8192 x 4096 bf16 (C = 2) with one, two, four a CU: 42.6, 44.5, 48.5 us;
+  // 16384 x 2048 (C = 1): 52.1, 41.7, 44.6; 2048 x 16384 (C = 4): 50.6, 59.5
+  const int64_t b = ceil_div(a.M, s.NT < 256 ? 256 / s.NT : 1), most = (int64_t)a.cus * (s.C == 1 ? 2 : 1);
   return (int)(b < most ? b : most);
+}
+// dw by columns beside dx: few rows (four round trips of a workgroup's loads;
+// 1000 x 2000 f16 7.3 us, 9.8 in two launches; 1000 x 1000 f32, twice the
+// bytes a row, 9.4 and 8.1), a second reading that the caches serve, and dx
+// not written over what it reads.
+int bwd_dw_blocks(const NormBwdArgs& a) {
+  const bool small = a.M * elem_bytes(a.in_dtype) <= 2048 && a.M * a.N <= (1 << 21) && !bwd_long(a);
+  return a.dw && small && a.dx != a.dy && a.dx != a.h ? (int)ceil_div(a.N, gtk::kDwCols) : 0;
 }
 
 template <int IN, int DY>
@@ -516,7 +597,7 @@ int bwd_types(const NormBwdArgs& a) {
     }
   } else {
     const RowShape s = bwd_shape(a);
-    const dim3 g((unsigned)blocks), b(s.NT < 256 ? 256 : s.NT);
+    const dim3 g((unsigned)((a.dx || !a.dw_blocks ? blocks : 0) + a.dw_blocks)), b(s.NT < 256 ? 256 : s.NT);
     switch (s.NT * 32 + s.C) {
 #define GT_BWD(NT, C) \
   case NT * 32 + C: hipLaunchKernelGGL((gtk::rmsnorm_bwd_kernel<IN, DY, NT, C>), g, b, 0, a.stream, a); break;
@@ -534,7 +615,7 @@ int bwd_types(const NormBwdArgs& a) {
 #undef GT_BWD
     }
   }
-  if (a.dw) {
+  if (a.dw && !a.dw_blocks) {
     const dim3 g((unsigned)ceil_div(a.N, gtk::kJoinCols));
     hipLaunchKernelGGL(gtk::rmsnorm_join_kernel, g, dim3(gtk::kJoinCols * gtk::kJoinSlices), 0, a.stream, a.ws, a.dw, blocks,
                        (int)a.N, a.dw_dtype);
@@ -543,7 +624,10 @@ int bwd_types(const NormBwdArgs& a) {
 }
 }  // namespace
 
-int launch_rmsnorm(const NormArgs& a) {
+int launch_rmsnorm(const NormArgs& args) {
+  NormArgs a = args;
+  const int e = elem_bytes(a.in_dtype);
+  a.past_caches = (double)a.M * a.N * (e * (1 + !!a.r + !!a.sum) + elem_bytes(a.out_dtype)) > gtk::kPastCaches;
   switch (a.in_dtype) {
     case DT_F32: return norm_in<DT_F32>(a);
     case DT_F16: return norm_in<DT_F16>(a);
@@ -551,9 +635,15 @@ int launch_rmsnorm(const NormArgs& a) {
   }
 }
 
-size_t rmsnorm_bwd_workspace_bytes(const NormBwdArgs& a) { return a.dw ? (size_t)bwd_blocks(a) * a.N * 4 : 0; }
+size_t rmsnorm_bwd_workspace_bytes(const NormBwdArgs& a) {
+  return a.dw && !bwd_dw_blocks(a) ? (size_t)bwd_blocks(a) * a.N * 4 : 0;
+}
 
-int launch_rmsnorm_bwd(const NormBwdArgs& a) {
+int launch_rmsnorm_bwd(const NormBwdArgs& args) {
+  NormBwdArgs a = args;
+  a.dw_blocks = bwd_dw_blocks(a);
+  const int e = elem_bytes(a.in_dtype);
+  a.past_caches = (double)a.M * a.N * (e * (1 + !!a.dsum + !!a.dx) + elem_bytes(a.dy_dtype)) > gtk::kPastCaches;
   const bool wide = a.dy_dtype == DT_F32;
   switch (a.in_dtype) {
     case DT_F32: return bwd_types<DT_F32, DT_F32>(a);
