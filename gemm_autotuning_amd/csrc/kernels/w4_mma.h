@@ -477,31 +477,18 @@ __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
     buf ^= 1;
   };
 
-  int tile = tile0;
-  for (; tile + kRound <= tile1; tile += kRound) {
+  for (int tile = tile0; tile < tile1; tile += kRound) {
 #pragma unroll
     for (int b = 0; b < kRound; b += kBatch) {
 #pragma unroll
       for (int d = b; d < b + kBatch; ++d) {
-        multiply_tile(red[wave][buf][d - b]);
+        if (tile + d < tile1) multiply_tile(red[wave][buf][d - b]);
         stage_tile(ring_q[(d + 1) % D], ring_s[(d + 1) % D]);
         load_tile(tile + d + 1 + D, ring_q[(d + 1) % D], ring_s[(d + 1) % D]);
       }
-      join(tile + b);
+      if (tile + b < tile1) join(tile + b);
     }
   }
-#pragma unroll
-  for (int b = 0; b < kRound; b += kBatch)
-    if (tile + b < tile1) {
-#pragma unroll
-      for (int d = b; d < b + kBatch; ++d)
-        if (tile + d < tile1) {
-          multiply_tile(red[wave][buf][d - b]);
-          stage_tile(ring_q[(d + 1) % D], ring_s[(d + 1) % D]);
-          if constexpr (D < kRound) load_tile(tile + d + 1 + D, ring_q[(d + 1) % D], ring_s[(d + 1) % D]);
-        }
-      join(tile + b);
-    }
 }
 
 // Launch for rows of type XT; T and C as chosen by the caller.
