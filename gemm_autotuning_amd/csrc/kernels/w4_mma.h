@@ -336,10 +336,6 @@ __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
   typename Stage::Scale ring_s[D][Stage::kScales];
 #pragma unroll
   for (int d = 0; d < D; ++d) load_tile(tile0 + d, ring_q[d], ring_s[d]);
-  // a tile is staged before its turn, so that the load that takes its place
-  // in the ring is under way
-  stage_tile(ring_q[0], ring_s[0]);
-  load_tile(tile0 + D, ring_q[0], ring_s[0]);
 
   // Into operand layout through LDS (the wave's part of the sums, still
   // unused): a
@@ -370,6 +366,11 @@ __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
       if (C == 8) __builtin_amdgcn_sched_barrier(0);
     }
   }
+  // a tile is staged before its turn, so that the load that takes its place
+  // in the ring is under way
+  stage_tile(ring_q[0], ring_s[0]);
+  load_tile(tile0 + D, ring_q[0], ring_s[0]);
+
   const Chunk minus8 = {{0xc100c100u, 0xc100c100u, 0xc100c100u, 0xc100c100u}};  // bf16
   bool wild = false;  // an element infinite, or so large that eight times it might not be finite
   if constexpr (kPlus8) {
