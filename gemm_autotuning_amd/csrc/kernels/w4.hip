@@ -197,8 +197,8 @@ int launch_w4_matmul(const W4Args& all, void* ws, int cus) {
     p.S = pl.S;
     p.waves = pl.waves;
     p.tiles = pl.tiles;
-    p.chunks_each = pl.chunks / (pl.S * pl.waves);
-    p.chunks_rest = pl.chunks % (pl.S * pl.waves);
+    p.chunks_each = pl.chunks / pl.S;
+    p.chunks_rest = pl.chunks % pl.S;
     p.tiles_each = pl.tiles / (int)pl.grid.x;
     p.tiles_rest = pl.tiles % (int)pl.grid.x;
     const bool int4 = a.w.format == gtk::W4_INT4;

@@ -35,8 +35,8 @@ struct W4Params {
   float* ws;           // S x M x ws_ld partial sums (S > 1)
   int64_t ws_ld;       // N rounded up to whole tiles
   int S, waves, tiles;
-  int chunks_each, chunks_rest;  // of a wave's slice: the first `rest` slices have one more
-  int tiles_each, tiles_rest;    // of a workgroup
+  int chunks_each, chunks_rest;  // of a workgroup's slice: the first `rest` of S have one more
+  int tiles_each, tiles_rest;    // of a workgroup's columns
 };
 
 // The low nibble of each byte, two's complement, as four e4m3 bytes of value
@@ -225,10 +225,12 @@ __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
   const gt::W4Args& a = p.a;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, kq = lane >> 4;
-  const int slice = blockIdx.y * p.waves + wave, wg = blockIdx.x;
-  // the slices' chunks differ by at most one, and so do the workgroups'
-  // tiles; a slice has at least C / 2 chunks and at most C
-  const int c0 = slice * p.chunks_each + min(slice, p.chunks_rest), nc = p.chunks_each + (slice < p.chunks_rest);
+  const int wg = blockIdx.x, part = blockIdx.y;
+  // the workgroups' chunks differ by at most one, and so do their waves' and
+  // the workgroups' tiles; a wave has at least C / 2 chunks and at most C
+  const int chunks = p.chunks_each + (part < p.chunks_rest);
+  const int nc = chunks / p.waves + (wave < chunks % p.waves);
+  const int c0 = part * p.chunks_each + min(part, p.chunks_rest) + wave * (chunks / p.waves) + min(wave, chunks % p.waves);
   const int tile0 = wg * p.tiles_each + min(wg, p.tiles_rest), tile1 = tile0 + p.tiles_each + (wg < p.tiles_rest);
   const int64_t K = a.w.K, N = a.w.N;
   const int rows = (int)a.M;
