@@ -157,10 +157,18 @@ bool w4_plan(const W4Args& a, int64_t rows, int cus, W4Plan* p) {
   p->chunks = (int)chunks;
   p->tiles = (int)tiles;
   p->T = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4);
-  p->C = chunks <= gtk::kW4Waves ? 1 : (p->T > 1 || chunks <= 2 * gtk::kW4Waves ? 2 : (chunks <= 4 * gtk::kW4Waves ? 4 : 8));
+  // Chunks to a wave: as few as hold K, up to four (two with more rows, for
+  // registers), then slices of K.  Eight spare the slices' second launch, but
+  // leave one tile in flight, which pays with many tiles to a workgroup: 4 x
+  // 65536 x 8192 (16 each) 52.7 us, 54.9 in slices; 32768 columns 30.4 and
+  // 30.9; 1 x 16384 x 8192 19.4 and 19.1; 16 x 8192 x 8192 15.5 and 15.2.
+  p->C = chunks <= gtk::kW4Waves ? 1 : (p->T > 1 || chunks <= 2 * gtk::kW4Waves ? 2 : 4);
+  if (p->C == 4 && chunks > 4 * gtk::kW4Waves && chunks <= 8 * gtk::kW4Waves && tiles >= 8 * (int64_t)cus) p->C = 8;
   p->waves = (int)(chunks < gtk::kW4Waves ? chunks : gtk::kW4Waves);
   const int per = p->waves * p->C;
   p->S = (int)((chunks + per - 1) / per);
+  // Workgroups a CU: as many as are there at a time.  Two of one chunk a wave:
+  // 16 x 65536 x 1024 13.5 us, 16.6 with one, 15.9 with four.
   int64_t wgs = (p->C == 1 ? 2 : 1) * (int64_t)cus / p->S;
   if (wgs < 1) wgs = 1;
   p->grid = dim3((unsigned)(tiles < wgs ? tiles : wgs), (unsigned)p->S, 1);

@@ -13,6 +13,13 @@
 // workgroup's slices, S workgroups share a tile and a second launch adds
 // their partial sums in order.
 //
+// 4 x 65536 x 8192 bf16 (group 128) takes 53.7 us, 5.2 TB/s, as a copy does:
+// HBM.  One row of 16384 x 4096 takes 10.0 us, of which 2.4 are a launch and
+// 2.8 the time until the rows are laid out.  61 x 11001 x 4100 takes 23.6 us:
+// with four row blocks a tile's expansion, products, the waves' sums and the
+// barrier follow each other (1.3 us a tile, of which the weights' bytes are a
+// quarter), and two waves a SIMD hide little of it.
+//
 // The values are expanded exactly, and a group's products are summed in the
 // matrix core's fp32 accumulators before the group's scale multiplies them.
 #pragma once
