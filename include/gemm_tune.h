@@ -288,9 +288,9 @@ gt_status gt_rmsnorm(const gt_rmsnorm_desc* d);
  *   dx = rstd * (g - n * mean_n(g * n)) + dsum,  dweight = sum_m dy * n.
  * dx is the gradient of x and of the residual alike; dsum is the gradient
  * that reaches h past the norm (sum_out's other uses).  dweight is summed
- * in fp32 in a fixed order; its partial sums take a workspace of the stream,
- * which the first (largest) call allocates: make that call outside stream
- * capture. */
+ * in fp32 in a fixed order; its partial sums may take a workspace of the
+ * stream, which the first (largest) call allocates: make that call outside
+ * stream capture. */
 typedef struct gt_rmsnorm_bwd_desc {
   const void* dy;       /* M x N, lddy                                       */
   const void* h;        /* M x N, ldh: sum_out, or x without a residual      */
@@ -327,7 +327,9 @@ typedef enum gt_w4_format { GT_W4_INT4 = 0, GT_W4_E2M1 = 1 } gt_w4_format;
  * with a transposed right operand (GT_NT) for a few rows, as one token or a
  * decode batch has.  The nibbles are expanded exactly, the products are
  * summed per group in fp32 and the scales applied to the fp32 sums.  Any M
- * is taken; for a prompt's rows, gt_w4_expand and gemm_tuned are faster. */
+ * is taken, 64 rows at a time; for a prompt's rows, gt_w4_expand and
+ * gemm_tuned are faster.  A long K may take a workspace of the stream, as
+ * above. */
 typedef struct gt_w4_desc {
   const void* x;          /* M x K, ldx                                      */
   const float* row_scale; /* M, or NULL                                      */
