@@ -137,7 +137,7 @@ __global__ __launch_bounds__(256) void w4_expand_kernel(gt::W4ExpandArgs a, int 
 namespace gt {
 
 namespace {
-constexpr int kRowBlock = 64;  // rows of one launch: four blocks of 16
+constexpr int kRowBlock = 256;  // rows of one launch, which bounds the workspace
 
 // Whether the tiles can take these weights: 16 bytes to a row at least, and
 // 16 rows (and a wave's groups of their scales) within 31-bit byte offsets.
@@ -147,7 +147,7 @@ bool w4_tiled(const W4Weights& w) {
 }
 
 struct W4Plan {
-  int T, C, waves, S, tiles, chunks;
+  int T, C, waves, groups, S, tiles, chunks;
   dim3 grid;
 };
 
@@ -156,7 +156,12 @@ bool w4_plan(const W4Args& a, int64_t rows, int cus, W4Plan* p) {
   if (chunks > 0x7fffffff / 16 || tiles > 0x7fffffff / 2) return false;
   p->chunks = (int)chunks;
   p->tiles = (int)tiles;
+  // Blocks of 16 rows to a workgroup.  More read the weights less often, but
+  // take longer to begin; where one to a workgroup fits the CUs, that: 53 x 118
+  // x 244 takes 5.6 us and with four 8.7, 64 x 2048 x 4096 (512 workgroups of
+  // one block) 14.5 and 12.4.
   p->T = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4);
+  if (tiles * ((rows + 15) / 16) <= cus) p->T = 1;
   // Chunks to a wave: as few as hold K, up to four (two with more rows, for
   // registers), then slices of K.  Eight spare the slices' second launch, but
   // leave one tile in flight, which pays with many tiles to a workgroup: 4 x
@@ -167,20 +172,28 @@ bool w4_plan(const W4Args& a, int64_t rows, int cus, W4Plan* p) {
   p->waves = (int)(chunks < gtk::kW4Waves ? chunks : gtk::kW4Waves);
   const int per = p->waves * p->C;
   p->S = (int)((chunks + per - 1) / per);
-  // Workgroups a CU: as many as are there at a time.  Two of one chunk a wave:
-  // 16 x 65536 x 1024 13.5 us, 16.6 with one, 15.9 with four.
-  int64_t wgs = (p->C == 1 ? 2 : 1) * (int64_t)cus / p->S;
-  if (wgs < 1) wgs = 1;
-  p->grid = dim3((unsigned)(tiles < wgs ? tiles : wgs), (unsigned)p->S, 1);
+  // Short K leaves waves over, which take other columns.  Workgroups a CU: as
+  // many as are there at a time.  Two of one chunk a wave: 16 x 65536 x 1024
+  // 13.5 us, 16.6 with one, 15.9 with four.
+  p->groups = gtk::kW4Waves / p->waves;
+  const int64_t most = (p->C == 1 && p->T == 1 ? 2 : 1) * (int64_t)cus / p->S, wgs = (tiles + p->groups - 1) / p->groups;
+  p->grid = dim3((unsigned)(wgs < most ? wgs : (most > 1 ? most : 1)), (unsigned)p->S,
+                 (unsigned)((rows + 16 * p->T - 1) / (16 * p->T)));
   return p->S <= 65535;
 }
 }  // namespace
 
 size_t w4_workspace_bytes(const W4Args& a, int cus) {
-  W4Plan p;
-  const int64_t rows = a.M < kRowBlock ? a.M : kRowBlock;
-  if (!w4_tiled(a.w) || !w4_plan(a, rows, cus, &p) || p.S == 1) return 0;
-  return kCounterRegion + (size_t)p.S * rows * p.tiles * 64;
+  size_t most = 0;
+  if (!w4_tiled(a.w)) return 0;
+  // the blocks of rows that there are: whole ones and the last
+  for (const int64_t rows : {a.M < kRowBlock ? a.M : (int64_t)kRowBlock, a.M % kRowBlock}) {
+    W4Plan p;
+    if (rows == 0 || !w4_plan(a, rows, cus, &p) || p.S == 1) continue;
+    const size_t need = kCounterRegion + (size_t)p.S * rows * p.tiles * 64;
+    most = need > most ? need : most;
+  }
+  return most;
 }
 
 int launch_w4_matmul(const W4Args& all, void* ws, int cus) {
@@ -204,11 +217,14 @@ int launch_w4_matmul(const W4Args& all, void* ws, int cus) {
     p.ws_ld = (int64_t)pl.tiles * 16;
     p.S = pl.S;
     p.waves = pl.waves;
+    p.groups = pl.groups;
+    p.waves_inverse = (65536 + pl.waves - 1) / pl.waves;
     p.tiles = pl.tiles;
     p.chunks_each = pl.chunks / pl.S;
     p.chunks_rest = pl.chunks % pl.S;
-    p.tiles_each = pl.tiles / (int)pl.grid.x;
-    p.tiles_rest = pl.tiles % (int)pl.grid.x;
+    const int columns = (int)pl.grid.x * pl.groups;
+    p.tiles_each = pl.tiles / columns;
+    p.tiles_rest = pl.tiles % columns;
     const bool int4 = a.w.format == gtk::W4_INT4;
     int rc;
     switch (a.x_dtype) {

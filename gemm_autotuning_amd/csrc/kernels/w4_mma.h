@@ -41,9 +41,10 @@ struct W4Params {
   gt::W4Args a;
   float* ws;           // S x M x ws_ld partial sums (S > 1)
   int64_t ws_ld;       // N rounded up to whole tiles
-  int S, waves, tiles;
+  int S, waves, groups, tiles;  // waves side by side along K, groups of them side by side along N
+  int waves_inverse;            // 2^16 / waves, rounded up: exact for what is divided (at most 64)
   int chunks_each, chunks_rest;  // of a workgroup's slice: the first `rest` of S have one more
-  int tiles_each, tiles_rest;    // of a workgroup's columns
+  int tiles_each, tiles_rest;    // of a group's columns
 };
 
 // The low nibble of each byte, two's complement, as four e4m3 bytes of value
@@ -232,15 +233,20 @@ __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
   const gt::W4Args& a = p.a;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, kq = lane >> 4;
-  const int wg = blockIdx.x, part = blockIdx.y;
-  // the workgroups' chunks differ by at most one, and so do their waves' and
-  // the workgroups' tiles; a wave has at least C / 2 chunks and at most C
+  // With fewer chunks than waves, groups of waves have columns of their own.
+  // The slices' chunks differ by at most one, and so do their waves' and the
+  // groups' tiles; a wave has at least C / 2 chunks and at most C.
+  const int group = (wave * p.waves_inverse) >> 16, turn = wave - group * p.waves, part = blockIdx.y;
+  const int cols = blockIdx.x * p.groups + group;
   const int chunks = p.chunks_each + (part < p.chunks_rest);
-  const int nc = chunks / p.waves + (wave < chunks % p.waves);
-  const int c0 = part * p.chunks_each + min(part, p.chunks_rest) + wave * (chunks / p.waves) + min(wave, chunks % p.waves);
-  const int tile0 = wg * p.tiles_each + min(wg, p.tiles_rest), tile1 = tile0 + p.tiles_each + (wg < p.tiles_rest);
+  const int each = (chunks * p.waves_inverse) >> 16, rest = chunks - each * p.waves;
+  const int nc = each + (turn < rest);
+  const int c0 = part * p.chunks_each + min(part, p.chunks_rest) + turn * each + min(turn, rest);
+  const int tile0 = cols * p.tiles_each + min(cols, p.tiles_rest), tile1 = tile0 + p.tiles_each + (cols < p.tiles_rest);
+  const int most_tiles = p.groups == 1 ? tile1 - tile0 : p.tiles_each + (p.tiles_rest > 0);  // of the workgroup's groups
   const int64_t K = a.w.K, N = a.w.N;
-  const int rows = (int)a.M;
+  const int64_t row0 = (int64_t)blockIdx.z * (16 * T);
+  const int rows = (int)min(a.M - row0, (int64_t)(16 * T));
 
   // The rows.  A chunk's k come in pieces of eight, and weight bytes in 16: a
   // column's last 16 bytes end with the row, so in the last chunk they reach
@@ -268,7 +274,7 @@ __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
     for (int t = 0; t < T; ++t)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        raw[c][t][i] = Op::load(a.x, min(16 * t + 4 * i + kq, rows - 1) * a.ldx + (k < K - 8 ? k : K - 8));
+        raw[c][t][i] = Op::load(a.x, (row0 + min(16 * t + 4 * i + kq, rows - 1)) * a.ldx + (k < K - 8 ? k : K - 8));
     if (C == 8) __builtin_amdgcn_sched_barrier(0);  // registers: no addresses of later chunks yet
   }
 
@@ -284,17 +290,17 @@ __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
     q_off[i] = (uint32_t)(min((int64_t)chunk(piece >> 2) * (kW4Chunk / 2) + 16 * (piece & 3), row_bytes - 16) - b0) +
                lane / Stage::kLanes * ldq;
   }
-  auto group = [&](int i) {  // of the slice's: that of the lane's i-th scale
+  auto scale_of = [&](int i) {  // of the slice's groups of k: that of the lane's i-th scale
     const int g = 4 * i + (lane & 3);
     return g < kPer ? (nc - 1) * kPer + g : g - kPer;
   };
   const uint32_t s_most = (uint32_t)min(groups - 1 - g0, 4 * Stage::kScales) * lds_g;
-  const uint8_t* const q0 = a.w.q + (int64_t)tile0 * 16 * a.w.ldq + b0;
-  const char* const s0 =
-      static_cast<const char*>(a.w.scales) + ((int64_t)tile0 * 16 * a.w.lds_n + g0 * a.w.lds_g) * kScale;
+  const int64_t n0 = (int64_t)min(tile0, p.tiles - 1) * 16;  // a group may have no tile
+  const uint8_t* const q0 = a.w.q + n0 * a.w.ldq + b0;
+  const char* const s0 = static_cast<const char*>(a.w.scales) + (n0 * a.w.lds_n + g0 * a.w.lds_g) * kScale;
   const uint8_t* q_next = q0;
   const char* s_next = s0;
-  // the workgroup's next tile; past its last, the first bytes of its first
+  // the group's next tile; past its last, the first bytes of its first
   auto load_tile = [&](int tile, u32x4 (&wq)[C], typename Stage::Scale (&ws)[Stage::kScales]) __attribute__((always_inline)) {
     const uint32_t some = tile < tile1 ? ~0u : 0u;
     const uint32_t last = tile == p.tiles - 1 ? (uint32_t)(N - 1) & 15u : 15u;  // a column past it is computed and not stored
@@ -317,7 +323,7 @@ __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
     const uint32_t col = min((uint32_t)lane >> 2, last) * lds_n;
 #pragma unroll
     for (int i = 0; i < Stage::kScales; ++i) {
-      const uint32_t off = (col + min(group(i) * lds_g, s_most)) & some;
+      const uint32_t off = (col + min(scale_of(i) * lds_g, s_most)) & some;
       ws[i] = *reinterpret_cast<const typename Stage::Scale*>(s + off);
     }
   };
@@ -337,7 +343,7 @@ __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
       else  // both conversions and a selection by bits: a branch here would split the tile's code
         f = __uint_as_float(((uint32_t)b << 16 & bf16_scales) | (__float_as_uint(f16_bits_to_f32(b)) & ~bf16_scales));
       // past K: nothing times zero, whatever the last group's scale is
-      stage.s[lane >> 2][4 * i + (lane & 3)] = g0 + group(i) < groups ? f : 0.f;
+      stage.s[lane >> 2][4 * i + (lane & 3)] = g0 + scale_of(i) < groups ? f : 0.f;
     }
     wave_lds_order();
   };
@@ -467,36 +473,39 @@ __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
   int buf = 0;
   auto join = [&](int tile) __attribute__((always_inline)) {
     __syncthreads();
+    const int first = group * p.waves * 64;
+    auto wave_of = [&](int w) { return (group * p.waves + w) & (kW4Waves - 1); };  // past the group's, any that is there
     auto put = [&](int m, int64_t n, float v) __attribute__((always_inline)) {
+      const int64_t at = row0 + m;
       if (p.S == 1)
-        store_out(a.y, m * a.ldy + n, v * a.x_scale * (a.row_scale ? a.row_scale[m] : 1.f), a.out_dtype);
+        store_out(a.y, at * a.ldy + n, v * a.x_scale * (a.row_scale ? a.row_scale[at] : 1.f), a.out_dtype);
       else
-        p.ws[((int64_t)blockIdx.y * rows + m) * p.ws_ld + n] = v;
+        p.ws[(part * a.M + at) * p.ws_ld + n] = v;
     };
     // Up to four rows an output to a thread, else four rows of a column: 4 x
     // 65536 x 8192 takes 53.7 and 57.1 us, 61 x 11001 x 4100 28.0 and 25.5.
     if (T == 1 && rows <= 4) {
       constexpr int kCols = 16 * kBatch;
-      for (int o = tid; o < kCols * rows; o += 64 * p.waves) {
+      for (int o = tid - first; o < kCols * rows; o += 64 * p.waves) {
         const int m = o / kCols, i = o / 16 % kBatch, l = o & 15;
         const int64_t n = (int64_t)(tile + i) * 16 + l;
         float v = 0.f, waves[kW4Waves];
 #pragma unroll
-        for (int w = 0; w < kW4Waves; ++w) waves[w] = red[w][buf][i][0][4 * l + m];
+        for (int w = 0; w < kW4Waves; ++w) waves[w] = red[wave_of(w)][buf][i][0][4 * l + m];
 #pragma unroll
         for (int w = 0; w < kW4Waves; ++w) v += w < p.waves ? waves[w] : 0.f;
         if (tile + i < tile1 && n < N) put(m, n, v);
       }
     } else {
       constexpr int kItems = kBatch * T * 64;
-      for (int o = tid; o < kItems; o += 64 * p.waves) {
+      for (int o = tid - first; o < kItems; o += 64 * p.waves) {
         const int l = o & 63, t = o / 64 % T, i = o / (64 * T);
         const int m = 16 * t + 4 * (l >> 4);
         const int64_t n = (int64_t)(tile + i) * 16 + (l & 15);
         if (tile + i < tile1 && m < rows && n < N) {
           f32x4 v = {0.f, 0.f, 0.f, 0.f}, waves[kW4Waves];
 #pragma unroll
-          for (int w = 0; w < kW4Waves; ++w) waves[w] = *reinterpret_cast<const f32x4*>(&red[w][buf][i][t][4 * l]);
+          for (int w = 0; w < kW4Waves; ++w) waves[w] = *reinterpret_cast<const f32x4*>(&red[wave_of(w)][buf][i][t][4 * l]);
 #pragma unroll
           for (int w = 0; w < kW4Waves; ++w)
             if (w < p.waves) v += waves[w];
@@ -509,7 +518,8 @@ __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
     buf ^= 1;
   };
 
-  for (int tile = tile0; tile < tile1; tile += kRound) {
+  for (int done = 0; done < most_tiles; done += kRound) {
+    const int tile = tile0 + done;
 #pragma unroll
     for (int b = 0; b < kRound; b += kBatch) {
 #pragma unroll
@@ -518,7 +528,7 @@ __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
         stage_tile(ring_q[(d + 1) % D], ring_s[(d + 1) % D]);
         load_tile(tile + d + 1 + D, ring_q[(d + 1) % D], ring_s[(d + 1) % D]);
       }
-      if (tile + b < tile1) join(tile + b);
+      if (done + b < most_tiles) join(tile + b);
     }
   }
 }
@@ -526,7 +536,7 @@ __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
 // Launch for rows of type XT; T and C as chosen by the caller.
 template <int XT, int FMT, int G, int WIDE>
 int w4_mma_sizes(const W4Params& p, dim3 grid, int T, int C) {
-  const dim3 block(64 * p.waves);
+  const dim3 block(64 * p.waves * p.groups);
   switch (16 * T + C) {
 #define GT_W4_SIZE(T, C, D) \
   case 16 * T + C: hipLaunchKernelGGL((w4_mma_kernel<XT, FMT, G, WIDE, T, C, D>), grid, block, 0, p.a.stream, p); break;
