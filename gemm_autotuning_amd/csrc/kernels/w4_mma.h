@@ -471,16 +471,17 @@ __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
   // The waves' sums of a batch of tiles.  The two buffers take turns, so one
   // barrier a batch keeps a buffer's readers ahead of its next writers.
   int buf = 0;
+  const int64_t y0 = row0 * a.ldy;
+  float* const ws0 = p.ws + (part * a.M + row0) * p.ws_ld;
   auto join = [&](int tile) __attribute__((always_inline)) {
     __syncthreads();
     const int first = group * p.waves * 64;
     auto wave_of = [&](int w) { return (group * p.waves + w) & (kW4Waves - 1); };  // past the group's, any that is there
     auto put = [&](int m, int64_t n, float v) __attribute__((always_inline)) {
-      const int64_t at = row0 + m;
       if (p.S == 1)
-        store_out(a.y, at * a.ldy + n, v * a.x_scale * (a.row_scale ? a.row_scale[at] : 1.f), a.out_dtype);
+        store_out(a.y, y0 + m * a.ldy + n, v * a.x_scale * (a.row_scale ? a.row_scale[row0 + m] : 1.f), a.out_dtype);
       else
-        p.ws[(part * a.M + at) * p.ws_ld + n] = v;
+        ws0[m * p.ws_ld + n] = v;
     };
     // Up to four rows an output to a thread, else four rows of a column: 4 x
     // 65536 x 8192 takes 53.7 and 57.1 us, 61 x 11001 x 4100 28.0 and 25.5.
