@@ -36,7 +36,7 @@ size_t rmsnorm_bwd_workspace_bytes(const NormBwdArgs& a);
 // ws: w4_workspace_bytes of the stream's workspace, or null when that is 0
 int launch_w4_matmul(const W4Args& a, void* ws, int cus);
 size_t w4_workspace_bytes(const W4Args& a, int cus);
-int launch_w4_expand(const W4ExpandArgs& a);
+int launch_w4_expand(const W4ExpandArgs& a, int cus);
 
 // Workspace layout shared by every candidate: a fixed region of counters
 // first (GEMV slice counters; zero between launches, each launch leaves them

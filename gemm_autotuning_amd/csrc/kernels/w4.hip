@@ -78,36 +78,50 @@ __global__ __launch_bounds__(256) void w4_join_kernel(W4Params p) {
 // Expansion: out[n,k] = s[n,k/G] * v(q[n,k]) rounded once.  The stores bound
 // it (four bytes written for one read at 16 bits), so a thread makes whole
 // 16-byte stores, from a piece of E weights; a group is a whole number of
-// pieces.  A thread takes kExpandPer pieces, all loaded before the first is
-// stored: 256 pieces apart along a long row, or those of rows below each
-// other where a row has no more than 256 (1 << lg threads to a row).
+// pieces.  A thread takes PER pieces, all loaded before the first is stored:
+// 256 pieces apart along a long row, or those of rows below each other where
+// a row has no more than 256 (1 << lg threads to a row).  The last K % E
+// weights of a row go one to a thread beside them.
 // 16384 x 8192 to bf16: 58 us, 5.8 TB/s (73 with its stores through the
-// caches; two or eight pieces a thread 76 and 84).
-constexpr int kExpandPer = 4;
-template <int FMT, int OUT, bool LONG>
+// caches, and then two or eight pieces a thread 76 and 84).
+template <int FMT, int OUT, bool LONG, int PER>
 __global__ __launch_bounds__(256) void w4_expand_kernel(gt::W4ExpandArgs a, int lg, int group_lg) {
   typedef typename Elem<OUT>::T TO;
   constexpr int E = 16 / (int)sizeof(TO);
   const int64_t whole = a.w.K / E * E;
   const int tx = threadIdx.x & ((1 << lg) - 1), ty = threadIdx.x >> lg, per_block = 256 >> lg;
-  const int64_t block_rows = LONG ? 1 : (int64_t)per_block * kExpandPer;
+  const int64_t block_rows = LONG ? 1 : (int64_t)per_block * PER;
+  const bool ends = whole < a.w.K && (!LONG || blockIdx.y == 0);
+  constexpr int kEnds = LONG ? 1 : PER;  // rows of a thread
   for (int64_t n0 = blockIdx.x * block_rows; n0 < a.w.N; n0 += gridDim.x * block_rows) {
     auto row = [&](int j) { return LONG ? n0 : n0 + j * per_block + ty; };
-    auto col = [&](int j) { return E * (LONG ? ((int64_t)blockIdx.y * kExpandPer + j) * 256 + tx : (int64_t)tx); };
-    uint32_t q[kExpandPer];
-    float s[kExpandPer];
+    auto col = [&](int j) { return E * (LONG ? ((int64_t)blockIdx.y * PER + j) * 256 + tx : (int64_t)tx); };
+    auto scale = [&](int64_t n, int64_t k) {
+      return load_any(a.w.scales, n * a.w.lds_n + (k >> group_lg) * a.w.lds_g, a.w.scale_dtype);
+    };
+    uint32_t q[PER], q_end[kEnds];
+    float s[PER], s_end[kEnds];
 #pragma unroll
-    for (int j = 0; j < kExpandPer; ++j) {
+    for (int j = 0; j < PER; ++j) {
       const int64_t n = row(j), k = col(j);
       q[j] = 0;
       s[j] = 0.f;
       if (n < a.w.N && k < whole) {
         __builtin_memcpy(&q[j], a.w.q + n * a.w.ldq + (k >> 1), E / 2);
-        s[j] = load_any(a.w.scales, n * a.w.lds_n + (k >> group_lg) * a.w.lds_g, a.w.scale_dtype);
+        s[j] = scale(n, k);
       }
     }
+    const int64_t k_end = whole + tx;
+    if (ends) {
 #pragma unroll
-    for (int j = 0; j < kExpandPer; ++j) {
+      for (int j = 0; j < kEnds; ++j)
+        if (row(j) < a.w.N && k_end < a.w.K) {
+          q_end[j] = a.w.q[row(j) * a.w.ldq + (k_end >> 1)];
+          s_end[j] = scale(row(j), k_end);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
       const int64_t n = row(j), k = col(j);
       float v[E];
 #pragma unroll
@@ -116,18 +130,12 @@ __global__ __launch_bounds__(256) void w4_expand_kernel(gt::W4ExpandArgs a, int 
       for (int e = 0; e < E; ++e) v[e] *= s[j];
       if (n < a.w.N && k < whole) store_piece<OUT, E>(reinterpret_cast<TO*>(a.y) + n * a.ldy + k, v, a.past_caches);
     }
-    // the row's last K % E weights, one to a thread
-    if (whole < a.w.K && (!LONG || blockIdx.y == 0)) {
-      const int64_t k = whole + tx;
-      const uint32_t e = (uint32_t)k & 1u;
+    if (ends) {
 #pragma unroll
-      for (int j = 0; j < (LONG ? 1 : kExpandPer); ++j) {
-        const int64_t n = row(j);
-        if (n < a.w.N && k < a.w.K)
-          reinterpret_cast<TO*>(a.y)[n * a.ldy + k] =
-              Elem<OUT>::put(load_any(a.w.scales, n * a.w.lds_n + (k >> group_lg) * a.w.lds_g, a.w.scale_dtype) *
-                             nibble_value<FMT>(a.w.q[n * a.w.ldq + (k >> 1)], e));
-      }
+      for (int j = 0; j < kEnds; ++j)
+        if (row(j) < a.w.N && k_end < a.w.K)
+          reinterpret_cast<TO*>(a.y)[row(j) * a.ldy + k_end] =
+              Elem<OUT>::put(s_end[j] * nibble_value<FMT>(q_end[j], (int)(k_end & 1)));
     }
   }
 }
@@ -243,37 +251,52 @@ int launch_w4_matmul(const W4Args& all, void* ws, int cus) {
 
 namespace {
 template <int FMT, int OUT>
-int expand_launch(const W4ExpandArgs& a) {
+int expand_launch(const W4ExpandArgs& a, int cus) {
   const int64_t pieces = a.w.K / (16 / elem_bytes(OUT)) + 1;  // and a thread for the rest of the row
   const int group_lg = a.w.group == 32 ? 5 : (a.w.group == 64 ? 6 : 7);
   // a row's rest of up to seven weights needs as many threads
   int lg = 3;
   while (lg < 8 && (1 << lg) < pieces) ++lg;
   const bool wide = pieces > 256;
-  const int64_t rows = wide ? 1 : (int64_t)(256 >> lg) * gtk::kExpandPer, wgs = (a.w.N + rows - 1) / rows;
-  const int64_t parts = wide ? (pieces + 256 * gtk::kExpandPer - 1) / (256 * gtk::kExpandPer) : 1;
+  // Four pieces a thread, or one where that leaves CUs without a workgroup
+  // (500 x 2000 to bf16 in a graph: 2.3 us, 3.4 with four).
+  auto blocks = [&](int per, int64_t* parts) {
+    const int64_t rows = wide ? 1 : (int64_t)(256 >> lg) * per;
+    *parts = wide ? (pieces + 256 * per - 1) / (256 * per) : 1;
+    return (a.w.N + rows - 1) / rows;
+  };
+  int64_t parts = 1, wgs = blocks(4, &parts);
+  const bool one = wgs * parts < 2 * (int64_t)cus;
+  if (one) wgs = blocks(1, &parts);
   if (parts > 65535) return LS_UNSUPPORTED;
   const dim3 g((unsigned)(wgs < (1 << 22) ? wgs : 1 << 22), (unsigned)parts);
-  if (wide)
-    hipLaunchKernelGGL((gtk::w4_expand_kernel<FMT, OUT, true>), g, dim3(256), 0, a.stream, a, lg, group_lg);
+#define GT_EXPAND(LONG, PER) \
+  hipLaunchKernelGGL((gtk::w4_expand_kernel<FMT, OUT, LONG, PER>), g, dim3(256), 0, a.stream, a, lg, group_lg)
+  if (wide && one)
+    GT_EXPAND(true, 1);
+  else if (wide)
+    GT_EXPAND(true, 4);
+  else if (one)
+    GT_EXPAND(false, 1);
   else
-    hipLaunchKernelGGL((gtk::w4_expand_kernel<FMT, OUT, false>), g, dim3(256), 0, a.stream, a, lg, group_lg);
+    GT_EXPAND(false, 4);
+#undef GT_EXPAND
   return hipGetLastError() == hipSuccess ? LS_OK : LS_HIP_ERROR;
 }
 template <int FMT>
-int expand_format(const W4ExpandArgs& a) {
+int expand_format(const W4ExpandArgs& a, int cus) {
   switch (a.out_dtype) {
-    case DT_F32: return expand_launch<FMT, DT_F32>(a);
-    case DT_F16: return expand_launch<FMT, DT_F16>(a);
-    default: return expand_launch<FMT, DT_BF16>(a);
+    case DT_F32: return expand_launch<FMT, DT_F32>(a, cus);
+    case DT_F16: return expand_launch<FMT, DT_F16>(a, cus);
+    default: return expand_launch<FMT, DT_BF16>(a, cus);
   }
 }
 }  // namespace
 
-int launch_w4_expand(const W4ExpandArgs& args) {
+int launch_w4_expand(const W4ExpandArgs& args, int cus) {
   W4ExpandArgs a = args;
   a.past_caches = (double)a.w.N * a.w.K * (0.5 + elem_bytes(a.out_dtype)) > gtk::kPastCaches;
-  return a.w.format == gtk::W4_INT4 ? expand_format<gtk::W4_INT4>(a) : expand_format<gtk::W4_E2M1>(a);
+  return a.w.format == gtk::W4_INT4 ? expand_format<gtk::W4_INT4>(a, cus) : expand_format<gtk::W4_E2M1>(a, cus);
 }
 
 }  // namespace gt

@@ -248,7 +248,7 @@ gt_status w4_expand(const gt_w4_expand_desc* d) {
   DeviceState* dev = nullptr;
   GT_CHECK(current_device(&dev));
   if (dev->fake) return GT_OK;
-  return launched(launch_w4_expand(a), "gt_w4_expand");
+  return launched(launch_w4_expand(a, dev->cus), "gt_w4_expand");
 }
 
 // Nothing throws across the C boundary: an allocation that fails while a
