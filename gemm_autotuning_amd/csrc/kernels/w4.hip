@@ -172,9 +172,10 @@ bool w4_plan(const W4Args& a, int64_t rows, int cus, W4Plan* p) {
   if (tiles * ((rows + 15) / 16) <= cus) p->T = 1;
   // Chunks to a wave: as few as hold K, up to four (two with more rows, for
   // registers), then slices of K.  Eight spare the slices' second launch, but
-  // leave one tile in flight, which pays with many tiles to a workgroup: 4 x
-  // 65536 x 8192 (16 each) 52.7 us, 54.9 in slices; 32768 columns 30.4 and
-  // 30.9; 1 x 16384 x 8192 19.4 and 19.1; 16 x 8192 x 8192 15.5 and 15.2.
+  // leave one tile in flight, which pays with many tiles to a workgroup
+  // (through the caches: 4 x 65536 x 8192, 16 tiles each, 52.7 us, 54.9 in
+  // slices; 32768 columns 30.4 and 30.9; 1 x 16384 x 8192 19.4 and 19.1; 16 x
+  // 8192 x 8192 15.5 and 15.2).
   p->C = chunks <= gtk::kW4Waves ? 1 : (p->T > 1 || chunks <= 2 * gtk::kW4Waves ? 2 : 4);
   if (p->C == 4 && chunks > 4 * gtk::kW4Waves && chunks <= 8 * gtk::kW4Waves && tiles >= 8 * (int64_t)cus) p->C = 8;
   p->waves = (int)(chunks < gtk::kW4Waves ? chunks : gtk::kW4Waves);

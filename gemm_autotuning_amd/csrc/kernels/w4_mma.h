@@ -13,9 +13,9 @@
 // workgroup's slices, S workgroups share a tile and a second launch adds
 // their partial sums in order.
 //
-// 4 x 65536 x 8192 bf16 (group 128) takes 53.7 us, 5.2 TB/s, as a copy does:
-// HBM.  One row of 16384 x 4096 takes 10.0 us, of which 2.4 are a launch and
-// 2.8 the time until the rows are laid out.  61 x 11001 x 4100 takes 23.6 us:
+// 4 x 65536 x 8192 bf16 (group 128) takes 52 us, 5.3 TB/s, more than a copy:
+// HBM.  One row of 16384 x 4096 takes 10.1 us, of which 2.4 are a launch and
+// 2.8 the time until the rows are laid out.  61 x 11001 x 4100 takes 24.3 us:
 // with four row blocks a tile's expansion, products, the waves' sums and the
 // barrier follow each other (1.3 us a tile, of which the weights' bytes are a
 // quarter), and two waves a SIMD hide little of it.
@@ -213,7 +213,12 @@ __device__ __forceinline__ void wave_lds_order() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-template <int XT, int FMT, int G, int WIDE, int T, int C, int D>
+// ONCE: the weights pass by the caches.  It pays where each row of them starts
+// a cache line and a wave reads whole ones, so that no line is read by two
+// loads far apart (4 x 65536 x 8192: 51.9 us, 54.5 through the caches; 16 x
+// 32768 x 2048 11.8 and 12.8; rows of 2050 bytes lose, 27.1 and 24.3), and
+// with one row block (64 x 32768 x 4096 39.1 and 37.2).
+template <int XT, int FMT, int G, int WIDE, int T, int C, int D, int ONCE>
 __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
   typedef W4Operand<XT, FMT> Op;
   typedef W4Stage<G, C, WIDE> Stage;
@@ -318,7 +323,11 @@ __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
 #pragma unroll
     for (int i = 0; i < C; ++i) {
       const int run = i % Stage::kRuns;
-      wq[i] = *reinterpret_cast<const u32x4_any*>(q + min(i / Stage::kRuns * step + q_off[run], most[run]));
+      const u32x4_any* at = reinterpret_cast<const u32x4_any*>(q + min(i / Stage::kRuns * step + q_off[run], most[run]));
+      if constexpr (ONCE)
+        wq[i] = __builtin_nontemporal_load(at);
+      else
+        wq[i] = *at;
     }
     const uint32_t col = min((uint32_t)lane >> 2, last) * lds_n;
 #pragma unroll
@@ -538,18 +547,30 @@ __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
 template <int XT, int FMT, int G, int WIDE>
 int w4_mma_sizes(const W4Params& p, dim3 grid, int T, int C) {
   const dim3 block(64 * p.waves * p.groups);
+  const bool lines = p.a.w.ldq % 128 == 0 && (uintptr_t)p.a.w.q % 128 == 0;
   switch (16 * T + C) {
+#define GT_W4_RUN(T, C, D, ONCE) \
+  hipLaunchKernelGGL((w4_mma_kernel<XT, FMT, G, WIDE, T, C, D, ONCE>), grid, block, 0, p.a.stream, p)
 #define GT_W4_SIZE(T, C, D) \
-  case 16 * T + C: hipLaunchKernelGGL((w4_mma_kernel<XT, FMT, G, WIDE, T, C, D>), grid, block, 0, p.a.stream, p); break;
+  case 16 * T + C: GT_W4_RUN(T, C, D, 0); break;
+#define GT_W4_LINES(T, C, D)   \
+  case 16 * T + C:             \
+    if (lines)                 \
+      GT_W4_RUN(T, C, D, 1);   \
+    else                       \
+      GT_W4_RUN(T, C, D, 0);   \
+    break;
     GT_W4_SIZE(1, 1, 4)
-    GT_W4_SIZE(1, 2, 4)
-    GT_W4_SIZE(1, 4, 2)
-    GT_W4_SIZE(1, 8, 1)
+    GT_W4_LINES(1, 2, 4)
+    GT_W4_LINES(1, 4, 2)
+    GT_W4_LINES(1, 8, 1)
     GT_W4_SIZE(2, 1, 4)
     GT_W4_SIZE(2, 2, 4)
     GT_W4_SIZE(4, 1, 2)
     GT_W4_SIZE(4, 2, 2)
+#undef GT_W4_LINES
 #undef GT_W4_SIZE
+#undef GT_W4_RUN
     default: return gt::LS_UNSUPPORTED;
   }
   return hipGetLastError() == hipSuccess ? gt::LS_OK : gt::LS_HIP_ERROR;
