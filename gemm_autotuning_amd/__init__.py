@@ -273,13 +273,17 @@ def _type_of(t, what):
 
 
 def _matrix(t, shape, what, dtype=None):
-    """Leading dimension of a matrix of this shape (and type) whose rows are contiguous."""
+    """Leading dimension of a matrix of this shape (and type) whose rows are
+    contiguous and apart from each other: a broadcast row's stride of 0 would
+    reach the library as "dense", and it would run past the row's end."""
     if tuple(t.shape) != tuple(shape):
         raise ValueError("%s has shape %s, not %s" % (what, tuple(t.shape), tuple(shape)))
     if dtype is not None and _type_of(t, what) != dtype:
         raise ValueError("%s is %s" % (what, t.dtype))
     if t.shape[1] > 1 and t.stride(1) != 1:
         raise ValueError("%s: the elements of a row must be contiguous" % what)
+    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError("%s: broadcast or overlapping rows are not taken" % what)
     return t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
 
