@@ -37,28 +37,44 @@ class Desc(ctypes.Structure):
                 ("scale_a", ctypes.c_float), ("scale_b", ctypes.c_float), ("stream", ctypes.c_void_p)]
 
 
-class RmsNormDesc(ctypes.Structure):
+class OperatorDesc(ctypes.Structure):
+    """A descriptor that, made from tensors, keeps them alive and knows
+    whether they are where a kernel can reach them."""
+    tensors = ()
+    elsewhere = None  # the device of tensors that are not on a GPU
+
+    def keep(self, *tensors):
+        for t in tensors[1:]:
+            if t is not None and t.device != tensors[0].device:
+                raise ValueError("tensors on %s and %s" % (tensors[0].device, t.device))
+        self.tensors = tensors
+        if not tensors[0].is_cuda:
+            self.elsewhere = str(tensors[0].device)
+        return self
+
+
+class RmsNormDesc(OperatorDesc):
     _fields_ = [(n, ctypes.c_void_p) for n in ("x", "residual", "weight", "sum_out", "y", "rstd", "row_scale")] + [
         (n, ctypes.c_int64) for n in ("M", "N", "ldx", "ldr", "lds", "ldy")] + [
         (n, ctypes.c_int32) for n in ("in_dtype", "weight_dtype", "out_dtype", "quant")] + [
         (n, ctypes.c_float) for n in ("eps", "weight_offset", "scale")] + [("stream", ctypes.c_void_p)]
 
 
-class RmsNormBwdDesc(ctypes.Structure):
+class RmsNormBwdDesc(OperatorDesc):
     _fields_ = [(n, ctypes.c_void_p) for n in ("dy", "h", "weight", "rstd", "dsum", "dx", "dweight")] + [
         (n, ctypes.c_int64) for n in ("M", "N", "lddy", "ldh", "ldds", "lddx")] + [
         (n, ctypes.c_int32) for n in ("in_dtype", "dy_dtype", "weight_dtype", "dweight_dtype")] + [
         ("weight_offset", ctypes.c_float), ("stream", ctypes.c_void_p)]
 
 
-class W4Desc(ctypes.Structure):
+class W4Desc(OperatorDesc):
     _fields_ = [(n, ctypes.c_void_p) for n in ("x", "row_scale", "qweight", "scales", "y")] + [
         (n, ctypes.c_int64) for n in ("M", "N", "K", "ldx", "ldq", "ldy", "scale_ldn", "scale_ldg")] + [
         (n, ctypes.c_int32) for n in ("x_dtype", "out_dtype", "format", "scale_dtype", "group")] + [
         ("x_scale", ctypes.c_float), ("stream", ctypes.c_void_p)]
 
 
-class W4ExpandDesc(ctypes.Structure):
+class W4ExpandDesc(OperatorDesc):
     _fields_ = [(n, ctypes.c_void_p) for n in ("qweight", "scales", "out")] + [
         (n, ctypes.c_int64) for n in ("N", "K", "ldq", "ldo", "scale_ldn", "scale_ldg")] + [
         (n, ctypes.c_int32) for n in ("out_dtype", "format", "scale_dtype", "group")] + [("stream", ctypes.c_void_p)]
@@ -296,12 +312,6 @@ def _vector(t, n, what, dtype=None):
         raise ValueError("%s is %s" % (what, t.dtype))
 
 
-def _same_device(first, *others):
-    for t in others:
-        if t is not None and t.device != first.device:
-            raise ValueError("tensors on %s and %s" % (first.device, t.device))
-
-
 def make_rmsnorm_desc(x, weight, y, residual=None, sum_out=None, rstd=None, row_scale=None, quant="none", eps=1e-6,
                       scale=1.0, weight_offset=0.0, stream=None):
     """Descriptor of gt_rmsnorm from tensors (M x N; strides and types are
@@ -316,9 +326,7 @@ def make_rmsnorm_desc(x, weight, y, residual=None, sum_out=None, rstd=None, row_
     _vector(weight, N, "weight")
     _vector(rstd, M, "rstd", F32)
     _vector(row_scale, M, "row_scale", F32)
-    _same_device(x, weight, y, residual, sum_out, rstd, row_scale)
-    d.tensors = (x, weight, y, residual, sum_out, rstd, row_scale)
-    return d
+    return d.keep(x, weight, y, residual, sum_out, rstd, row_scale)
 
 
 def make_rmsnorm_bwd_desc(dy, h, weight, rstd, dx, dweight=None, dsum=None, weight_offset=0.0, stream=None):
@@ -334,9 +342,7 @@ def make_rmsnorm_bwd_desc(dy, h, weight, rstd, dx, dweight=None, dsum=None, weig
     _vector(weight, N, "weight")
     _vector(rstd, M, "rstd", F32)
     _vector(dweight, N, "dweight")
-    _same_device(dy, h, weight, rstd, dsum, dx, dweight)
-    d.tensors = (dy, h, weight, rstd, dsum, dx, dweight)
-    return d
+    return d.keep(dy, h, weight, rstd, dsum, dx, dweight)
 
 
 def _w4_weights(qweight, scales, K, group, format):
@@ -365,9 +371,7 @@ def make_w4_desc(x, qweight, scales, y, format="int4", group=128, row_scale=None
                _matrix(y, (M, N), "y"), sn, sg, _type_of(x, "x"), _type_of(y, "y"), _code(format, W4_FORMATS), sdt,
                group, x_scale, _ptr(stream))
     _vector(row_scale, M, "row_scale", F32)
-    _same_device(x, qweight, scales, y, row_scale)
-    d.tensors = (x, qweight, scales, y, row_scale)
-    return d
+    return d.keep(x, qweight, scales, y, row_scale)
 
 
 def make_w4_expand_desc(qweight, scales, out, format="int4", group=128, stream=None):
@@ -376,25 +380,29 @@ def make_w4_expand_desc(qweight, scales, out, format="int4", group=128, stream=N
     n, ldq, sn, sg, sdt = _w4_weights(qweight, scales, K, group, format)
     d = W4ExpandDesc(_ptr(qweight), _ptr(scales), _ptr(out), N, K, ldq, _matrix(out, (n, K), "out"), sn, sg,
                      _type_of(out, "out"), _code(format, W4_FORMATS), sdt, group, _ptr(stream))
-    _same_device(qweight, scales, out)
-    d.tensors = (qweight, scales, out)
-    return d
+    return d.keep(qweight, scales, out)
+
+
+def _run_operator(call, desc):
+    if desc.elsewhere:
+        raise ValueError("tensors on %s: the operators run on a GPU" % desc.elsewhere)
+    _check(call(ctypes.byref(desc)))
 
 
 def gt_rmsnorm(desc):
-    _check(lib().gt_rmsnorm(ctypes.byref(desc)))
+    _run_operator(lib().gt_rmsnorm, desc)
 
 
 def gt_rmsnorm_backward(desc):
-    _check(lib().gt_rmsnorm_backward(ctypes.byref(desc)))
+    _run_operator(lib().gt_rmsnorm_backward, desc)
 
 
 def gt_w4_matmul(desc):
-    _check(lib().gt_w4_matmul(ctypes.byref(desc)))
+    _run_operator(lib().gt_w4_matmul, desc)
 
 
 def gt_w4_expand(desc):
-    _check(lib().gt_w4_expand(ctypes.byref(desc)))
+    _run_operator(lib().gt_w4_expand, desc)
 
 
 # ---- control

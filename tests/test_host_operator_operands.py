@@ -89,3 +89,21 @@ def test_vectors_must_not_be_broadcast():
     with pytest.raises(ValueError, match="row_scale"):
         gt.make_w4_desc(torch.zeros(M, K, dtype=BF), torch.zeros(N, K // 2, dtype=torch.uint8), torch.zeros(N, 1),
                         torch.zeros(M, N), group=64, row_scale=torch.zeros(1).expand(M))
+
+
+@pytest.mark.parametrize("op", ["norm", "bwd", "w4", "expand"])
+def test_host_tensors_are_refused_before_a_launch(op):
+    # the stand-in device takes every call that reaches the library
+    make, call = {"norm": (norm, gt.gt_rmsnorm), "bwd": (bwd, gt.gt_rmsnorm_backward), "w4": (w4, gt.gt_w4_matmul),
+                  "expand": (expand, gt.gt_w4_expand)}[op]
+    gt.gt_test_fake_device(True, "f32", [1.0])
+    try:
+        with pytest.raises(ValueError, match="cpu"):
+            call(make())
+    finally:
+        gt.gt_test_fake_device(False)
+
+
+def test_tensors_of_two_devices_are_refused():
+    with pytest.raises(ValueError, match="meta"):
+        norm(residual=torch.zeros(M, N, dtype=BF, device="meta"))
