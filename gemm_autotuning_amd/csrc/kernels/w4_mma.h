@@ -47,13 +47,18 @@ struct W4Params {
   int tiles_each, tiles_rest;    // of a group's columns
 };
 
-// The low nibble of each byte, two's complement, as four e4m3 bytes of value
-// nibble / 512: e4m3 is linear below 2^-5 (magnitudes 0..15 in steps of 2^-9
-// are the bytes 0..15), so the magnitude itself is the code.  A negative c in
-// -8..-1 has the bits 8 + j and the magnitude 8 - j = (j ^ 7) + 1.
-__device__ __forceinline__ uint32_t int4_to_e4m3(uint32_t u) {
-  const uint32_t t = u & 0x08080808u, one = t >> 3;
-  return (((u & 0x07070707u) ^ (t - one)) + one) | (t << 4);
+// Eight two's complement nibbles as e4m3 bytes of value nibble / 512, those of
+// the bytes' low nibbles and those of the high ones: e4m3 is linear below 2^-5
+// (magnitudes 0..15 in steps of 2^-9 are the bytes 0..15), so the magnitude
+// itself is the code.  A negative c in -8..-1 has the bits 8 + j and the
+// magnitude 8 - j = (j ^ 7) + 1.
+__device__ __forceinline__ void int4_to_e4m3(uint32_t u, uint32_t* lo, uint32_t* hi) {
+  uint32_t sign = u & 0x88888888u;
+  const uint32_t one = sign >> 3;
+  asm("" : "+v"(sign));  // else its known bits make two instructions of each selection below
+  const uint32_t mag = ((u & 0x77777777u) ^ (sign - one)) + one;
+  *lo = (mag & 0x0f0f0f0fu) | (sign << 4 & 0xf0f0f0f0u);
+  *hi = (mag >> 4 & 0x0f0f0f0fu) | (sign & 0xf0f0f0f0u);
 }
 template <class V>
 __device__ __forceinline__ uint32_t bits_of(V v) {
@@ -107,12 +112,13 @@ struct W4Rows {
 
 // Eight weights from a dword of nibbles, and the rows' elements in the order
 // of k they come in.  Instructions per dword, which the arithmetic of one row
-// block hardly hides: e2m1 four (conversions); integers with f16 rows nine;
-// with bf16 rows seven for value + 8, seventeen for the value.
+// block hardly hides: e2m1 four (conversions); integers nine with f16 rows,
+// thirteen with bf16 ones (value + 8 would take seven there, but its sums hold
+// eight times the row's elements, and a large one at a weight of zero costs
+// the others their last bits).
 template <int XT, int FMT>
 struct W4Operand : W4Rows<XT> {
   typedef W4Rows<XT> R;
-  // the value itself
   static __device__ __forceinline__ Chunk weights(uint32_t u) {
     Chunk f;
     if constexpr (FMT == W4_E2M1) {
@@ -137,7 +143,8 @@ struct W4Operand : W4Rows<XT> {
       f.w[2] = low(h & 0x000f000fu);
       f.w[3] = high(h & 0x00f000f0u);
     } else {
-      const uint32_t lo = int4_to_e4m3(u), hi = int4_to_e4m3(u >> 4);
+      uint32_t lo, hi;
+      int4_to_e4m3(u, &lo, &hi);
       f.w[0] = bits_of(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.f, false));
       f.w[1] = bits_of(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.f, true));
       f.w[2] = bits_of(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.f, false));
@@ -157,16 +164,6 @@ struct W4Operand : W4Rows<XT> {
     __builtin_memcpy(&f, &b, 4);
     return bits_of(__builtin_elementwise_fma(f, f16x2v{(_Float16)0.0625f, (_Float16)0.0625f},
                                              f16x2v{(_Float16)-72.f, (_Float16)-72.f}));
-  }
-  // integers with bf16 rows: value + 8
-  static __device__ __forceinline__ Chunk weights_plus_8(uint32_t u) {
-    const uint32_t lo = (u & 0x0f0f0f0fu) ^ 0x08080808u, hi = (u >> 4 & 0x0f0f0f0fu) ^ 0x08080808u;
-    Chunk f;
-    f.w[0] = bits_of(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.f, false));
-    f.w[1] = bits_of(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.f, true));
-    f.w[2] = bits_of(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.f, false));
-    f.w[3] = bits_of(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.f, true));
-    return f;
   }
   // e2m1: as stored.  Integers: f16 pairs k with k + 4; bf16 takes the even
   // k (the bytes' low nibbles), then the odd ones.
@@ -225,16 +222,9 @@ __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
   constexpr int kPer = Stage::kPer;
   constexpr int kBatch = T == 4 || C == 8 ? 2 : 4;  // tiles to a barrier
   constexpr int kRound = kBatch > D ? kBatch : D;  // tiles that are unrolled
-  // Integers under bf16 rows: value + 8, with the accumulators started at -8
-  // times the row's sum over the group (four row blocks of small groups have
-  // no LDS for those).  Exact products either way; the sums are about three
-  // times as large.
-  constexpr bool kPlus8 = XT == DT_BF16 && FMT == W4_INT4 && (T < 4 || kPer < 4);
-  constexpr bool kKeepStarts = kPlus8 && C * kPer < 32;  // else multiplied again for each tile, for want of registers
   static_assert(kRound % kBatch == 0 && kRound % D == 0, "a round is a whole number of both");
   __shared__ float red[kW4Waves][2][kBatch][T][256];
   __shared__ Stage stages[kW4Waves];
-  __shared__ f32x4 starts[kKeepStarts ? kW4Waves : 1][C * kPer][T][4];  // of the rows 4 kq.. in a group
   const gt::W4Args& a = p.a;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, kq = lane >> 4;
@@ -395,36 +385,8 @@ __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
   stage_tile(ring_q[0], ring_s[0]);
   load_tile(tile0 + D, ring_q[0], ring_s[0]);
 
-  const Chunk minus8 = {{0xc100c100u, 0xc100c100u, 0xc100c100u, 0xc100c100u}};  // bf16
-  bool wild = false;  // an element infinite, or so large that eight times it might not be finite
-  if constexpr (kPlus8) {
-    f32x4 total[T];
-#pragma unroll
-    for (int t = 0; t < T; ++t) total[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-#pragma unroll
-      for (int g = 0; g < kPer; ++g)
-#pragma unroll
-        for (int t = 0; t < T; ++t) {
-          f32x4 sum = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int j = 0; j < 4 / kPer; ++j) Op::mma(sum, x[c][g * (4 / kPer) + j][t], minus8);
-          if (kKeepStarts && r == 0) starts[wave][c * kPer + g][t][kq] = sum;
-          if (c < nc) total[t] += sum;
-        }
-      if (C == 8) __builtin_amdgcn_sched_barrier(0);
-    }
-    wave_lds_order();
-#pragma unroll
-    for (int t = 0; t < T; ++t)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) wild |= !(fabsf(total[t][i]) < 0x1p120f);
-    wild = __any(wild);
-  }
-
   // the staged tile's sums over this wave's k, into LDS
-  auto multiply = [&](auto plus8, float (&out)[T][256]) __attribute__((always_inline)) {
+  auto multiply_tile = [&](float (&out)[T][256]) __attribute__((always_inline)) {
     f32x4 acc[T];
 #pragma unroll
     for (int t = 0; t < T; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -443,19 +405,11 @@ __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
           constexpr int kSteps = 4 / kPer;
           f32x4 sum[T];
 #pragma unroll
-          for (int t = 0; t < T; ++t) {
-            sum[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-            if constexpr (plus8 && kKeepStarts) {
-              sum[t] = starts[wave][c * kPer + g][t][kq];
-            } else if constexpr (plus8) {
-#pragma unroll
-              for (int j = 0; j < kSteps; ++j) Op::mma(sum[t], x[c][g * kSteps + j][t], minus8);
-            }
-          }
+          for (int t = 0; t < T; ++t) sum[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int j = 0; j < kSteps; ++j) {
             const uint32_t v = u[g * kSteps + j];
-            const Chunk w = plus8 ? Op::weights_plus_8(v) : Op::weights(v);
+            const Chunk w = Op::weights(v);
 #pragma unroll
             for (int t = 0; t < T; ++t) Op::mma(sum[t], x[c][g * kSteps + j][t], w);
           }
@@ -470,12 +424,6 @@ __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
 #pragma unroll
     for (int t = 0; t < T; ++t)
       if (16 * t + 4 * kq < rows) *reinterpret_cast<f32x4*>(&out[t][4 * lane]) = acc[t];
-  };
-  auto multiply_tile = [&](float (&out)[T][256]) __attribute__((always_inline)) {
-    if constexpr (kPlus8) {
-      if (!wild) return multiply(std::true_type(), out);
-    }
-    multiply(std::false_type(), out);
   };
   // The waves' sums of a batch of tiles.  The two buffers take turns, so one
   // barrier a batch keeps a buffer's readers ahead of its next writers.
