@@ -171,13 +171,12 @@ bool w4_plan(const W4Args& a, int64_t rows, int cus, W4Plan* p) {
   p->T = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4);
   if (tiles * ((rows + 15) / 16) <= cus) p->T = 1;
   // Chunks to a wave: as few as hold K, up to four (two with more rows, for
-  // registers), then slices of K.  Eight spare the slices' second launch, but
-  // leave one tile in flight, which pays with many tiles to a workgroup
-  // (through the caches: 4 x 65536 x 8192, 16 tiles each, 52.7 us, 54.9 in
-  // slices; 32768 columns 30.4 and 30.9; 1 x 16384 x 8192 19.4 and 19.1; 16 x
-  // 8192 x 8192 15.5 and 15.2).
+  // registers), then slices of K.  Eight would spare the slices' second
+  // launch, but leave one tile in flight: 4 x 65536 x 8192 bf16 and int4 56.6
+  // us, 63.6 with eight, f16 56.4 and 57.7, 1 x 32768 x 8192 30.6 and 34.5
+  // (rows of 3000 bytes through the caches, 4 x 65536 x 6000: bf16 48.2 and
+  // 48.7, f16 52.0 and 49.2).
   p->C = chunks <= gtk::kW4Waves ? 1 : (p->T > 1 || chunks <= 2 * gtk::kW4Waves ? 2 : 4);
-  if (p->C == 4 && chunks > 4 * gtk::kW4Waves && chunks <= 8 * gtk::kW4Waves && tiles >= 8 * (int64_t)cus) p->C = 8;
   p->waves = (int)(chunks < gtk::kW4Waves ? chunks : gtk::kW4Waves);
   const int per = p->waves * p->C;
   p->S = (int)((chunks + per - 1) / per);

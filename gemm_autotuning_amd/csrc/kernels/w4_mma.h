@@ -13,8 +13,8 @@
 // workgroup's slices, S workgroups share a tile and a second launch adds
 // their partial sums in order.
 //
-// 4 x 65536 x 8192 bf16 (group 128) takes 52 us, 5.3 TB/s, more than a copy:
-// HBM.  One row of 16384 x 4096 takes 10.1 us, of which 2.4 are a launch and
+// 4 x 65536 x 8192 bf16 (group 128) takes 56 us, 5.0 TB/s, a copy's rate:
+// HBM.  One row of 16384 x 4096 takes 10.8 us, of which 2.4 are a launch and
 // 2.8 the time until the rows are laid out.  61 x 11001 x 4100 takes 24.3 us:
 // with four row blocks a tile's expansion, products, the waves' sums and the
 // barrier follow each other (1.3 us a tile, of which the weights' bytes are a
@@ -212,15 +212,15 @@ __device__ __forceinline__ void wave_lds_order() {
 
 // ONCE: the weights pass by the caches.  It pays where each row of them starts
 // a cache line and a wave reads whole ones, so that no line is read by two
-// loads far apart (4 x 65536 x 8192: 51.9 us, 54.5 through the caches; 16 x
-// 32768 x 2048 11.8 and 12.8; rows of 2050 bytes lose, 27.1 and 24.3), and
+// loads far apart (4 x 65536 x 8192 f16: 55.4 us, 62.0 through the caches; 16 x
+// 32768 x 2048 12.4 and 13.5; rows of 2050 bytes lose, 27.1 and 24.3), and
 // with one row block (64 x 32768 x 4096 39.1 and 37.2).
 template <int XT, int FMT, int G, int WIDE, int T, int C, int D, int ONCE>
 __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
   typedef W4Operand<XT, FMT> Op;
   typedef W4Stage<G, C, WIDE> Stage;
   constexpr int kPer = Stage::kPer;
-  constexpr int kBatch = T == 4 || C == 8 ? 2 : 4;  // tiles to a barrier
+  constexpr int kBatch = T == 4 ? 2 : 4;  // tiles to a barrier
   constexpr int kRound = kBatch > D ? kBatch : D;  // tiles that are unrolled
   static_assert(kRound % kBatch == 0 && kRound % D == 0, "a round is a whole number of both");
   __shared__ float red[kW4Waves][2][kBatch][T][256];
@@ -270,7 +270,6 @@ __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         raw[c][t][i] = Op::load(a.x, (row0 + min(16 * t + 4 * i + kq, rows - 1)) * a.ldx + (k < K - 8 ? k : K - 8));
-    if (C == 8) __builtin_amdgcn_sched_barrier(0);  // registers: no addresses of later chunks yet
   }
 
   Stage& stage = stages[wave];
@@ -308,8 +307,7 @@ __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
     for (int i = 0; i < Stage::kRuns; ++i)
       most[i] = ((last - lane / Stage::kLanes) * ldq + q_off[i]) &
                 (i * Stage::kLanes + lane % Stage::kLanes < 4 * nc ? some : 0u);
-    uint32_t step = ldq * Stage::kCols;
-    if constexpr (C == 8) asm("" : "+s"(step));  // registers: the sums below are not kept from tile to tile
+    const uint32_t step = ldq * Stage::kCols;
 #pragma unroll
     for (int i = 0; i < C; ++i) {
       const int run = i % Stage::kRuns;
@@ -377,7 +375,6 @@ __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
         for (int j = 0; j < 4; ++j) x[c][j][t] = Op::order(own[place(r, kPer == 1 ? 4 * kq + j : 4 * j + kq)]);
         wave_lds_order();
       }
-      if (C == 8) __builtin_amdgcn_sched_barrier(0);
     }
   }
   // a tile is staged before its turn, so that the load that takes its place
@@ -418,8 +415,6 @@ __global__ __launch_bounds__(64 * kW4Waves) void w4_mma_kernel(W4Params p) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[t][i] += stage.s[r][c * kPer + g] * sum[t][i];
         }
-        // registers: no more than one or two chunks' reads and expansions at once
-        if (C == 8 && kPer == 4) __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
     for (int t = 0; t < T; ++t)
@@ -511,7 +506,6 @@ int w4_mma_sizes(const W4Params& p, dim3 grid, int T, int C) {
     GT_W4_SIZE(1, 1, 4)
     GT_W4_LINES(1, 2, 4)
     GT_W4_LINES(1, 4, 2)
-    GT_W4_LINES(1, 8, 1)
     GT_W4_SIZE(2, 1, 4)
     GT_W4_SIZE(2, 2, 4)
     GT_W4_SIZE(4, 1, 2)
