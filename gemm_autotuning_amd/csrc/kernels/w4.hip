@@ -145,7 +145,8 @@ __global__ __launch_bounds__(256) void w4_expand_kernel(gt::W4ExpandArgs a, int 
 namespace gt {
 
 namespace {
-constexpr int kRowBlock = 256;  // rows of one launch, which bounds the workspace
+constexpr int64_t kRowBlock = 256;         // most rows of one launch
+constexpr int64_t kPartials = 64ll << 20;  // most bytes of the slices' partial sums of one launch
 
 // Whether the tiles can take these weights: 16 bytes to a row at least, and
 // 16 rows (and a wave's groups of their scales) within 31-bit byte offsets.
@@ -189,20 +190,98 @@ bool w4_plan(const W4Args& a, int64_t rows, int cus, W4Plan* p) {
                  (unsigned)((rows + 16 * p->T - 1) / (16 * p->T)));
   return p->S <= 65535;
 }
+
+// Rows and columns of one launch: all columns of up to 256 rows, unless the
+// slices' partial sums would pass kPartials (S x rows x columns floats; S
+// grows with K).  Then fewer rows, in blocks of 64 as a workgroup takes them
+// (256 x 65536 x 8192 524 us, 520 in one launch; in ranges of columns 567);
+// where not even 64 fit, ranges of columns of equal numbers of tiles, and 16
+// rows where not even one tile fits (with S at most 65535 one always does).
+// A part's own plan takes no more slices than the whole's: only T falls with
+// its size, and a smaller T has as many chunks to a wave or more.
+struct W4Ranges {
+  int64_t rows, cols;
+};
+bool w4_ranges(const W4Args& a, int cus, W4Ranges* r) {
+  r->rows = a.M < kRowBlock ? a.M : kRowBlock;
+  r->cols = a.w.N;
+  W4Plan p;
+  if (!w4_plan(a, r->rows, cus, &p)) return false;
+  auto fits = [&] { return kPartials / (64 * (int64_t)p.S * p.tiles); };  // rows of all columns
+  if (p.S == 1 || fits() >= r->rows) return true;
+  r->rows = fits() >= 64 ? fits() / 64 * 64 : (r->rows < 64 ? r->rows : 64);
+  while (w4_plan(a, r->rows, cus, &p)) {
+    if (p.S == 1 || fits() >= r->rows) return true;
+    const int64_t most = kPartials / (64 * p.S * r->rows);  // tiles
+    if (most > 0) {
+      const int64_t parts = (p.tiles + most - 1) / most;
+      r->cols = 16 * ((p.tiles + parts - 1) / parts);
+      return true;
+    }
+    r->rows = 16;
+  }
+  return false;
+}
+// The part of the problem at rows m0.. and columns n0...
+W4Args w4_part(const W4Args& all, const W4Ranges& r, int64_t m0, int64_t n0) {
+  W4Args a = all;
+  a.M = all.M - m0 < r.rows ? all.M - m0 : r.rows;
+  a.w.N = all.w.N - n0 < r.cols ? all.w.N - n0 : r.cols;
+  a.w.q = all.w.q + n0 * all.w.ldq;
+  a.w.scales = static_cast<const char*>(all.w.scales) + n0 * all.w.lds_n * elem_bytes(all.w.scale_dtype);
+  a.x = static_cast<const char*>(all.x) + m0 * all.ldx * elem_bytes(all.x_dtype);
+  a.y = static_cast<char*>(all.y) + (m0 * all.ldy + n0) * elem_bytes(all.out_dtype);
+  if (all.row_scale) a.row_scale = all.row_scale + m0;
+  return a;
+}
 }  // namespace
 
 size_t w4_workspace_bytes(const W4Args& a, int cus) {
   size_t most = 0;
-  if (!w4_tiled(a.w)) return 0;
-  // the blocks of rows that there are: whole ones and the last
-  for (const int64_t rows : {a.M < kRowBlock ? a.M : (int64_t)kRowBlock, a.M % kRowBlock}) {
-    W4Plan p;
-    if (rows == 0 || !w4_plan(a, rows, cus, &p) || p.S == 1) continue;
-    const size_t need = kCounterRegion + (size_t)p.S * rows * p.tiles * 64;
-    most = need > most ? need : most;
-  }
+  W4Ranges r;
+  if (!w4_tiled(a.w) || !w4_ranges(a, cus, &r)) return 0;
+  // the parts that there are: whole ones and the last of either direction
+  for (const int64_t m0 : {(int64_t)0, (a.M - 1) / r.rows * r.rows})
+    for (const int64_t n0 : {(int64_t)0, (a.w.N - 1) / r.cols * r.cols}) {
+      const W4Args part = w4_part(a, r, m0, n0);
+      W4Plan p;
+      if (!w4_plan(part, part.M, cus, &p) || p.S == 1) continue;
+      const size_t need = kCounterRegion + (size_t)p.S * part.M * p.tiles * 64;
+      most = need > most ? need : most;
+    }
   return most;
 }
+
+namespace {
+int w4_launch(const W4Args& a, void* ws, int cus) {
+  W4Plan pl;
+  if (!w4_plan(a, a.M, cus, &pl)) return LS_UNSUPPORTED;
+  gtk::W4Params p;
+  p.a = a;
+  p.ws = ws ? reinterpret_cast<float*>(static_cast<char*>(ws) + kCounterRegion) : nullptr;
+  p.ws_ld = (int64_t)pl.tiles * 16;
+  p.S = pl.S;
+  p.waves = pl.waves;
+  p.groups = pl.groups;
+  p.waves_inverse = (65536 + pl.waves - 1) / pl.waves;
+  p.tiles = pl.tiles;
+  p.chunks_each = pl.chunks / pl.S;
+  p.chunks_rest = pl.chunks % pl.S;
+  const int columns = (int)pl.grid.x * pl.groups;
+  p.tiles_each = pl.tiles / columns;
+  p.tiles_rest = pl.tiles % columns;
+  const bool int4 = a.w.format == gtk::W4_INT4;
+  int rc;
+  switch (a.x_dtype) {
+    case DT_BF16: rc = int4 ? w4_mma_bf16_int4(p, pl.grid, pl.T, pl.C) : w4_mma_bf16_e2m1(p, pl.grid, pl.T, pl.C); break;
+    case DT_F16: rc = int4 ? w4_mma_f16_int4(p, pl.grid, pl.T, pl.C) : w4_mma_f16_e2m1(p, pl.grid, pl.T, pl.C); break;
+    default: rc = int4 ? w4_mma_e4m3_int4(p, pl.grid, pl.T, pl.C) : w4_mma_e4m3_e2m1(p, pl.grid, pl.T, pl.C); break;
+  }
+  if (rc != LS_OK || p.S == 1) return rc;
+  hipLaunchKernelGGL(gtk::w4_join_kernel, dim3((unsigned)((a.w.N + 1023) / 1024), (unsigned)a.M), dim3(256), 0, a.stream, p);
+  return hipGetLastError() == hipSuccess ? LS_OK : LS_HIP_ERROR;
+}
+}  // namespace
 
 int launch_w4_matmul(const W4Args& all, void* ws, int cus) {
   if (!w4_tiled(all.w)) {
@@ -211,41 +290,13 @@ int launch_w4_matmul(const W4Args& all, void* ws, int cus) {
     hipLaunchKernelGGL(gtk::w4_plain_kernel, g, dim3(256), 0, all.stream, all);
     return hipGetLastError() == hipSuccess ? LS_OK : LS_HIP_ERROR;
   }
-  for (int64_t m0 = 0; m0 < all.M; m0 += kRowBlock) {
-    W4Args a = all;
-    a.M = all.M - m0 < kRowBlock ? all.M - m0 : kRowBlock;
-    a.x = static_cast<const char*>(all.x) + m0 * all.ldx * elem_bytes(all.x_dtype);
-    a.y = static_cast<char*>(all.y) + m0 * all.ldy * elem_bytes(all.out_dtype);
-    if (all.row_scale) a.row_scale = all.row_scale + m0;
-    W4Plan pl;
-    if (!w4_plan(a, a.M, cus, &pl)) return LS_UNSUPPORTED;
-    gtk::W4Params p;
-    p.a = a;
-    p.ws = ws ? reinterpret_cast<float*>(static_cast<char*>(ws) + kCounterRegion) : nullptr;
-    p.ws_ld = (int64_t)pl.tiles * 16;
-    p.S = pl.S;
-    p.waves = pl.waves;
-    p.groups = pl.groups;
-    p.waves_inverse = (65536 + pl.waves - 1) / pl.waves;
-    p.tiles = pl.tiles;
-    p.chunks_each = pl.chunks / pl.S;
-    p.chunks_rest = pl.chunks % pl.S;
-    const int columns = (int)pl.grid.x * pl.groups;
-    p.tiles_each = pl.tiles / columns;
-    p.tiles_rest = pl.tiles % columns;
-    const bool int4 = a.w.format == gtk::W4_INT4;
-    int rc;
-    switch (a.x_dtype) {
-      case DT_BF16: rc = int4 ? w4_mma_bf16_int4(p, pl.grid, pl.T, pl.C) : w4_mma_bf16_e2m1(p, pl.grid, pl.T, pl.C); break;
-      case DT_F16: rc = int4 ? w4_mma_f16_int4(p, pl.grid, pl.T, pl.C) : w4_mma_f16_e2m1(p, pl.grid, pl.T, pl.C); break;
-      default: rc = int4 ? w4_mma_e4m3_int4(p, pl.grid, pl.T, pl.C) : w4_mma_e4m3_e2m1(p, pl.grid, pl.T, pl.C); break;
+  W4Ranges r;
+  if (!w4_ranges(all, cus, &r)) return LS_UNSUPPORTED;
+  for (int64_t n0 = 0; n0 < all.w.N; n0 += r.cols)
+    for (int64_t m0 = 0; m0 < all.M; m0 += r.rows) {
+      const int rc = w4_launch(w4_part(all, r, m0, n0), ws, cus);
+      if (rc != LS_OK) return rc;
     }
-    if (rc != LS_OK) return rc;
-    if (p.S > 1) {
-      hipLaunchKernelGGL(gtk::w4_join_kernel, dim3((unsigned)((a.w.N + 1023) / 1024), (unsigned)a.M), dim3(256), 0, a.stream, p);
-      if (hipGetLastError() != hipSuccess) return LS_HIP_ERROR;
-    }
-  }
   return LS_OK;
 }
 

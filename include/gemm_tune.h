@@ -327,9 +327,10 @@ typedef enum gt_w4_format { GT_W4_INT4 = 0, GT_W4_E2M1 = 1 } gt_w4_format;
  * with a transposed right operand (GT_NT) for a few rows, as one token or a
  * decode batch has.  The nibbles are expanded exactly, the products are
  * summed per group in fp32 and the scales applied to the fp32 sums.  Any M
- * is taken, 64 rows at a time; for a prompt's rows, gt_w4_expand and
+ * is taken, up to 256 rows at a time; for a prompt's rows, gt_w4_expand and
  * gemm_tuned are faster.  A long K may take a workspace of the stream, as
- * above. */
+ * above, for at most 64 MiB of partial sums: a call that has more runs over
+ * fewer rows or columns at a time. */
 typedef struct gt_w4_desc {
   const void* x;          /* M x K, ldx                                      */
   const float* row_scale; /* M, or NULL                                      */
