@@ -50,6 +50,7 @@ struct NormArgs {
   int in_dtype, w_dtype, out_dtype;
   int quant;  // gt_quant
   float eps, offset, scale;
+  float near;  // set by the launcher: the power of two that brings scale nearer to 1
   int cus;
   bool past_caches;  // set by the launcher: more than the last-level cache passes by
   hipStream_t stream;

@@ -115,7 +115,8 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void rmsnorm_kernel(gt::NormAr
     }
     const float rstd = 1.0f / sqrtf(row.sum(q) / (float)N + a.eps);
     if (t == 0 && a.rstd) a.rstd[m] = rstd;
-    hl = hl * rstd * wl;
+    const float near = OUT == DT_E4M3 ? a.near : 1.f;
+    hl = hl * rstd * near * wl;
     uint32_t big = last < N ? __float_as_uint(hl) & 0x7fffffffu : 0u;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -126,6 +127,7 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void rmsnorm_kernel(gt::NormAr
       for (int e = 0; e < E; ++e) {
         float& v = h[c * E + e];
         v *= rstd;
+        if constexpr (OUT == DT_E4M3) v *= near;
         if (a.w) v *= g[e] + a.offset;
         if constexpr (OUT == DT_E4M3) most = max(most, __float_as_uint(v) & 0x7fffffffu);
       }
@@ -139,7 +141,7 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void rmsnorm_kernel(gt::NormAr
         if (t == 0) a.row_scale[m] = scale;
         inv = 1.0f / scale;
       } else {
-        inv = 1.0f / a.scale;
+        inv = 1.0f / (a.scale * near);
       }
       hl *= inv;
 #pragma unroll
@@ -183,7 +185,7 @@ __global__ __launch_bounds__(kLongNT) void rmsnorm_long_kernel(gt::NormArgs a) {
     if (threadIdx.x == 0 && a.rstd) a.rstd[m] = rstd;
     float inv = 1.0f;
     if constexpr (OUT == DT_E4M3) {
-      inv = 1.0f / a.scale;
+      inv = 1.0f / (a.scale * a.near);
       if (a.row_scale) {
         uint32_t big = 0;
 #pragma unroll 8
@@ -197,7 +199,7 @@ __global__ __launch_bounds__(kLongNT) void rmsnorm_long_kernel(gt::NormArgs a) {
     }
     for (unsigned n = threadIdx.x; n < N; n += kLongNT) {
       const float h = h_of(n);
-      const float v = h * rstd * w_of(n);
+      const float v = h * rstd * (OUT == DT_E4M3 ? a.near : 1.f) * w_of(n);
       if (s) s[n] = Elem<IN>::put(h);
       y[n] = Elem<OUT>::put(OUT == DT_E4M3 ? v * inv : v);
     }
@@ -629,6 +631,11 @@ int launch_rmsnorm(const NormArgs& args) {
   NormArgs a = args;
   const int e = elem_bytes(a.in_dtype);
   a.past_caches = (double)a.M * a.N * (e * (1 + !!a.r + !!a.sum) + elem_bytes(a.out_dtype)) > gtk::kPastCaches;
+  // The quotient by a given scale is a product with its reciprocal, which
+  // leaves fp32's normal numbers for scales near the ends of its range, as the
+  // weighted value may; a power of two keeps both inside.
+  const bool given = !a.row_scale && a.out_dtype == DT_E4M3;
+  a.near = given && a.scale < 0x1p-64f ? 0x1p64f : (given && a.scale > 0x1p64f ? 0x1p-64f : 1.f);
   switch (a.in_dtype) {
     case DT_F32: return norm_in<DT_F32>(a);
     case DT_F16: return norm_in<DT_F16>(a);
