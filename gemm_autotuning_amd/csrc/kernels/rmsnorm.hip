@@ -522,18 +522,22 @@ RowShape row_shape(int64_t N, int64_t M, int elem, int cus) {
   return {1024, 4};
 }
 
+// Workgroups of a launch, whose threads must be fewer than 2^32: those of up to
+// 1024 threads walk the rows past them.
+constexpr int64_t kMostGroups = 1 << 21;
+
 template <int IN, int OUT, int NT, int C>
 int norm_launch(const NormArgs& a) {
   constexpr int kRows = NT < 256 ? 256 / NT : 1;
   const int64_t wgs = ceil_div(a.M, kRows);
-  const dim3 g((unsigned)(wgs < (1 << 22) ? wgs : 1 << 22)), b(NT < 256 ? 256 : NT);
+  const dim3 g((unsigned)(wgs < kMostGroups ? wgs : kMostGroups)), b(NT < 256 ? 256 : NT);
   hipLaunchKernelGGL((gtk::rmsnorm_kernel<IN, OUT, NT, C>), g, b, 0, a.stream, a);
   return status();
 }
 template <int IN, int OUT>
 int norm_shape(const NormArgs& a) {
   if (long_rows(a.N, elem_bytes(IN))) {
-    const dim3 g((unsigned)(a.M < (1 << 22) ? a.M : 1 << 22));
+    const dim3 g((unsigned)(a.M < kMostGroups ? a.M : kMostGroups));
     hipLaunchKernelGGL((gtk::rmsnorm_long_kernel<IN, OUT>), g, dim3(gtk::kLongNT), 0, a.stream, a);
     return status();
   }
