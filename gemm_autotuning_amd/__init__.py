@@ -138,6 +138,7 @@ def lib():
             "gt_w4_matmul": [P(W4Desc)],
             "gt_w4_expand": [P(W4ExpandDesc)],
             "gt_test_alloc_count": [P(ctypes.c_uint64), P(ctypes.c_uint64)],
+            "gt_test_fail_allocs": [i32],
             "gt_make_key": [P(Desc), p, ctypes.c_char_p, ctypes.c_size_t],
             "gt_key_display": [P(Desc), ctypes.c_char_p, ctypes.c_size_t],
             "tune_lookup": [P(Desc), P(ctypes.c_int), ctypes.c_char_p, ctypes.c_size_t, P(d)],
@@ -228,6 +229,11 @@ def gt_test_alloc_count():
     a, f = ctypes.c_uint64(), ctypes.c_uint64()
     _check(lib().gt_test_alloc_count(ctypes.byref(a), ctypes.byref(f)))
     return a.value, f.value
+
+
+def gt_test_fail_allocs(n):
+    """Make the library's next n device allocations fail."""
+    _check(lib().gt_test_fail_allocs(n))
 
 
 def gt_make_key(desc):

@@ -1325,6 +1325,11 @@ gt_status gt_test_alloc_count(uint64_t* allocs, uint64_t* frees) {
   return GT_OK;
 }
 
+gt_status gt_test_fail_allocs(int n) {
+  fail_allocs(n);
+  return GT_OK;
+}
+
 gt_status gt_set_peaks(gt_dtype dtype, double peak_ops_per_s, double peak_bytes_per_s, double launch_s) {
   if ((int)dtype < 0 || (int)dtype > 3 || !(peak_ops_per_s > 0) || !(peak_bytes_per_s > 0) || launch_s < 0)
     return GT_ERR_INVALID_ARG;

@@ -182,6 +182,7 @@ int launch_candidate(DeviceState& d, const Candidate& c, const Problem& p, void*
 hipError_t dev_malloc(void** p, size_t bytes);
 void dev_free(void* p);
 void alloc_counts(uint64_t* allocs, uint64_t* frees);
+void fail_allocs(int n);  // the next n allocations fail
 
 // cache.cpp
 gt_status save_file(DeviceState& d, const std::string& path);

@@ -20,12 +20,20 @@ static std::string hip_msg(hipError_t e, const char* what) {
 }
 
 // Every device allocation and free the library makes goes through these two
-// (counted, so tests can check that an entry point allocates nothing).
+// (counted, so tests can check that an entry point allocates nothing).  A
+// failure goes to the caller and is taken back from the runtime, where the
+// next check after a launch, the program's own or another library's, would
+// find it.
 static std::atomic<uint64_t> g_allocs{0}, g_frees{0};
+static std::atomic<int> g_fail_allocs{0};
 hipError_t dev_malloc(void** p, size_t bytes) {
   g_allocs.fetch_add(1, std::memory_order_relaxed);
-  return hipMalloc(p, bytes);
+  if (g_fail_allocs.load(std::memory_order_relaxed) > 0 && g_fail_allocs.fetch_sub(1) > 0) bytes = (size_t)1 << 60;
+  const hipError_t e = hipMalloc(p, bytes);
+  if (e != hipSuccess) hipGetLastError();
+  return e;
 }
+void fail_allocs(int n) { g_fail_allocs.store(n); }
 void dev_free(void* p) {
   g_frees.fetch_add(1, std::memory_order_relaxed);
   hipFree(p);

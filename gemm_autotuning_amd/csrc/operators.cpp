@@ -61,7 +61,9 @@ gt_status launched(int rc, const char* what) {
 gt_status operator_workspace(DeviceState& d, hipStream_t stream, size_t bytes, void** ws, std::mutex** mu) {
   if (!d.fake && !workspace_ready(d, (void*)stream, bytes)) {
     hipStreamCaptureStatus cs = hipStreamCaptureStatusNone;
-    if (hipStreamIsCapturing(stream, &cs) != hipSuccess || cs != hipStreamCaptureStatusNone)
+    const bool asked = hipStreamIsCapturing(stream, &cs) == hipSuccess;
+    if (!asked) hipGetLastError();  // the status says it; no later check should find it
+    if (!asked || cs != hipStreamCaptureStatusNone)
       return invalid("the workspace would have to grow under stream capture: make this call once before capturing");
   }
   size_t have = 0;

@@ -129,6 +129,10 @@ gt_status gt_test_write_floor(void* const* bufs, int n_bufs, uint64_t bytes, int
  * since it was loaded. */
 gt_status gt_test_alloc_count(uint64_t* allocs, uint64_t* frees);
 
+/* The library's next n device allocations ask for 2^60 bytes, so that they
+ * fail as they do where memory has run out. */
+gt_status gt_test_fail_allocs(int n);
+
 /* Set the measured peaks of the current device for one input type, as if the
  * probes had run: ops/s, bytes/s (every working-set size) and the launch
  * overhead in seconds. */
