@@ -162,6 +162,9 @@ gt_status throughput_limit(DeviceState& d, const Problem& p, void* stream, doubl
 // that use the buffer).
 gt_status get_workspace(DeviceState& d, void* stream, size_t bytes, void** ptr, size_t* have,
                         std::mutex** launch_mu);
+// The same without a lock, for a buffer that is there and big enough; false
+// where get_workspace has more to do.
+bool find_workspace(DeviceState& d, void* stream, size_t bytes, void** ptr, size_t* have, std::mutex** launch_mu);
 // Whether the stream's workspace already holds `bytes` (get_workspace would
 // allocate nothing).
 bool workspace_ready(DeviceState& d, void* stream, size_t bytes);

@@ -113,6 +113,22 @@ std::string validator_arch(const DeviceState& d) {
 // Per stream: the GEMV slice counters (the first 64 KiB, zero between
 // launches) and the fp32 partial sums of split-K tiles and split GEMVs.  A
 // buffer big enough is found without a lock; growing one takes ws_mu.
+bool find_workspace(DeviceState& d, void* stream, size_t bytes, void** ptr, size_t* have, std::mutex** launch_mu) {
+  const uintptr_t key = (uintptr_t)stream + 1;
+  for (int i = 0; i < kWsSlots; ++i) {
+    const uintptr_t k = d.ws_slots[i].key.load(std::memory_order_acquire);
+    if (k == 0) break;
+    if (k != key) continue;
+    const WsBuf* b = d.ws_slots[i].buf.load(std::memory_order_acquire);
+    if (!b || b->bytes < bytes) break;
+    *ptr = b->ptr;
+    *have = b->bytes;
+    *launch_mu = &d.ws_slots[i].launch_mu;
+    return true;
+  }
+  return false;
+}
+
 gt_status get_workspace(DeviceState& d, void* stream, size_t bytes, void** ptr, size_t* have,
                         std::mutex** launch_mu) {
   *ptr = nullptr;
@@ -127,20 +143,8 @@ gt_status get_workspace(DeviceState& d, void* stream, size_t bytes, void** ptr, 
     *launch_mu = &dummy_mu;
     return GT_OK;
   }
+  if (find_workspace(d, stream, bytes, ptr, have, launch_mu)) return GT_OK;
   const uintptr_t key = (uintptr_t)stream + 1;
-  for (int i = 0; i < kWsSlots; ++i) {
-    const uintptr_t k = d.ws_slots[i].key.load(std::memory_order_acquire);
-    if (k == 0) break;
-    if (k != key) continue;
-    const WsBuf* b = d.ws_slots[i].buf.load(std::memory_order_acquire);
-    if (b && b->bytes >= bytes) {
-      *ptr = b->ptr;
-      *have = b->bytes;
-      *launch_mu = &d.ws_slots[i].launch_mu;
-      return GT_OK;
-    }
-    break;
-  }
   std::lock_guard<std::mutex> g(d.ws_mu);
   WsSlot* slot = nullptr;
   for (int i = 0; i < kWsSlots && !slot; ++i) {

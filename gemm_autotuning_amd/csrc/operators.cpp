@@ -59,14 +59,15 @@ gt_status launched(int rc, const char* what) {
 // The stream's workspace for an operator.  Growing it allocates and clears
 // memory, which a captured graph must not hold, so that is refused.
 gt_status operator_workspace(DeviceState& d, hipStream_t stream, size_t bytes, void** ws, std::mutex** mu) {
-  if (!d.fake && !workspace_ready(d, (void*)stream, bytes)) {
+  size_t have = 0;
+  if (!d.fake) {
+    if (find_workspace(d, (void*)stream, bytes, ws, &have, mu)) return GT_OK;
     hipStreamCaptureStatus cs = hipStreamCaptureStatusNone;
     const bool asked = hipStreamIsCapturing(stream, &cs) == hipSuccess;
     if (!asked) hipGetLastError();  // the status says it; no later check should find it
-    if (!asked || cs != hipStreamCaptureStatusNone)
+    if ((!asked || cs != hipStreamCaptureStatusNone) && !workspace_ready(d, (void*)stream, bytes))
       return invalid("the workspace would have to grow under stream capture: make this call once before capturing");
   }
-  size_t have = 0;
   return get_workspace(d, (void*)stream, bytes, ws, &have, mu);
 }
 
