@@ -48,7 +48,6 @@ struct NormArgs {
   float* row_scale;
   int64_t M, N, ldx, ldr, lds, ldy;
   int in_dtype, w_dtype, out_dtype;
-  int quant;  // gt_quant
   float eps, offset, scale;
   float near;  // set by the launcher: the power of two that brings scale nearer to 1
   int cus;

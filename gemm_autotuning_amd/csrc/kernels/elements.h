@@ -1,6 +1,6 @@
 // elements.h -- element types of the operators around the product: loads and
 // stores of one element or of a piece of a row, converted from and to fp32,
-// and sums over a wave.
+// and joins over a wave.
 #pragma once
 
 #include "common.h"
@@ -165,15 +165,6 @@ __device__ __forceinline__ uint32_t wave_join(uint32_t v, F f) {
   v = f(r[0], r[1]);
   const auto h = __builtin_amdgcn_permlane32_swap(v, v, false, false);
   return f(h[0], h[1]);
-}
-__device__ __forceinline__ float wave_sum(float v) {
-  return __uint_as_float(wave_join(__float_as_uint(v), [](uint32_t a, uint32_t b) {
-    return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
-  }));
-}
-// largest of bit patterns
-__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-  return wave_join(v, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
 }
 
 }  // namespace gtk

@@ -111,7 +111,6 @@ gt_status rmsnorm(const gt_rmsnorm_desc* d) {
   a.row_scale = d->quant == GT_QUANT_ROW ? d->row_scale : nullptr;
   a.M = d->M;
   a.N = d->N;
-  a.quant = d->quant;
   a.eps = d->eps;
   a.offset = d->weight_offset;
   a.scale = d->scale;
