@@ -82,8 +82,9 @@ __global__ __launch_bounds__(256) void w4_join_kernel(W4Params p) {
 // 256 pieces apart along a long row, or those of rows below each other where
 // a row has no more than 256 (1 << lg threads to a row).  The last K % E
 // weights of a row go one to a thread beside them.
-// 16384 x 8192 to bf16: 48.4 us, 7.0 TB/s, the rate of a fill.  Stores through
-// the caches take a quarter more, and two or eight pieces a thread more again.
+// 16384 x 8192 to bf16: 47.9 us, 7.1 TB/s, the rate of a fill (73 with its
+// stores through the caches; four and eight pieces a thread 48.4 and 51.3, and
+// 32768 x 1024 with two, four and eight 14.8, 17.4 and 25.2).
 template <int FMT, int OUT, bool LONG, int PER>
 __global__ __launch_bounds__(256) void w4_expand_kernel(gt::W4ExpandArgs a, int lg, int group_lg) {
   typedef typename Elem<OUT>::T TO;
@@ -309,14 +310,14 @@ int expand_launch(const W4ExpandArgs& a, int cus) {
   int lg = 3;
   while (lg < 8 && (1 << lg) < pieces) ++lg;
   const bool wide = pieces > 256;
-  // Four pieces a thread, or one where that leaves CUs without a workgroup
+  // Two pieces a thread, or one where that leaves CUs without a workgroup
   // (500 x 2000 to bf16 in a graph: 2.3 us, 3.4 with four).
   auto blocks = [&](int per, int64_t* parts) {
     const int64_t rows = wide ? 1 : (int64_t)(256 >> lg) * per;
     *parts = wide ? (pieces + 256 * per - 1) / (256 * per) : 1;
     return (a.w.N + rows - 1) / rows;
   };
-  int64_t parts = 1, wgs = blocks(4, &parts);
+  int64_t parts = 1, wgs = blocks(2, &parts);
   const bool one = wgs * parts < 2 * (int64_t)cus;
   if (one) wgs = blocks(1, &parts);
   if (parts > 65535) return LS_UNSUPPORTED;
@@ -326,11 +327,11 @@ int expand_launch(const W4ExpandArgs& a, int cus) {
   if (wide && one)
     GT_EXPAND(true, 1);
   else if (wide)
-    GT_EXPAND(true, 4);
+    GT_EXPAND(true, 2);
   else if (one)
     GT_EXPAND(false, 1);
   else
-    GT_EXPAND(false, 4);
+    GT_EXPAND(false, 2);
 #undef GT_EXPAND
   return hipGetLastError() == hipSuccess ? LS_OK : LS_HIP_ERROR;
 }
