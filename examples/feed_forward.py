@@ -76,7 +76,8 @@ class FeedForward:
 
 
 class RmsNorm(torch.autograd.Function):
-    """(norm(x + residual), x + residual) with the library's backward pass."""
+    """(norm(x + residual), x + residual) with the library's backward pass,
+    which has no derivative of its own."""
 
     @staticmethod
     def forward(ctx, x, residual, weight):
@@ -88,6 +89,7 @@ class RmsNorm(torch.autograd.Function):
         return y, h
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, dy, dh):
         h, weight, rstd = ctx.saved_tensors
         dx, dw = torch.empty_like(h), torch.empty_like(weight)
