@@ -251,9 +251,10 @@ typedef enum gt_quant { GT_QUANT_NONE = 0, GT_QUANT_TENSOR = 1, GT_QUANT_ROW = 2
 /* h = x + residual, rstd[m] = 1 / sqrt(mean_n h[m,n]^2 + eps),
  * y = h * rstd * (weight + weight_offset), all in fp32 and rounded once.
  * sum_out receives h rounded to in_dtype (the norm itself uses the unrounded
- * h).  A product of the stored e4m3 rows takes the scale back as scale_a
+ * h).  Elements whose squares sum past fp32's range (about 1e19 each) give
+ * rstd 0.  A product of the stored e4m3 rows takes the scale back as scale_a
  * (GT_QUANT_TENSOR, gemm_tuned_ex) or row_scale (GT_QUANT_ROW,
- * gt_w4_matmul). */
+ * gt_w4_matmul); gemm_tuned_ex takes no scale per row. */
 typedef struct gt_rmsnorm_desc {
   const void* x;        /* M x N, ldx                                        */
   const void* residual; /* M x N, ldr, or NULL                               */
@@ -320,13 +321,16 @@ gt_status gt_rmsnorm_backward(const gt_rmsnorm_bwd_desc* d);
  * low nibble; (K + 1) / 2 bytes a row, rows ldq bytes apart.  A nibble is a
  * two's complement integer (-8..7), or an e2m1 float (sign, then 0, 0.5, 1,
  * 1.5, 2, 3, 4, 6).  Every `group` of consecutive k in a row shares a scale:
- * weight = scale * value. */
+ * weight = scale * value, so integers are symmetric (there are no zero
+ * points), and groups are of 32, 64 or 128 (neither 16 nor a whole row, nor k
+ * in another order). */
 typedef enum gt_w4_format { GT_W4_INT4 = 0, GT_W4_E2M1 = 1 } gt_w4_format;
 
 /* y[m,n] = x_scale * row_scale[m] * sum_k x[m,k] * weight[n,k]: a product
  * with a transposed right operand (GT_NT) for a few rows, as one token or a
  * decode batch has.  The nibbles are expanded exactly, the products are
- * summed per group in fp32 and the scales applied to the fp32 sums.  Any M
+ * summed per group in fp32 and the scales applied to the fp32 sums (so a sum
+ * of x * value past 2^128 is infinite, whatever its scale).  Any M
  * is taken, up to 256 rows at a time; for a prompt's rows, gt_w4_expand and
  * gemm_tuned are faster.  A long K may take a workspace of the stream, as
  * above, for at most 64 MiB of partial sums: a call that has more runs over
@@ -357,8 +361,9 @@ typedef struct gt_w4_desc {
  * N == 0 is a no-op; K == 0 writes zeros. */
 gt_status gt_w4_matmul(const gt_w4_desc* d);
 
-/* out[n,k] = weight (n, k), rounded once to out_dtype: N x K row-major, the
- * right operand of a GT_NT product. */
+/* out[n,k] = weight (n, k) as an fp32 product (exact unless the scales are
+ * fp32), rounded to out_dtype: N x K row-major, the right operand of a GT_NT
+ * product.  There is no e4m3 output. */
 typedef struct gt_w4_expand_desc {
   const void* qweight;
   const void* scales;
