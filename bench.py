@@ -36,7 +36,9 @@ data and config fields), plus
                 of the next 20 calls), then the same in a second process that
                 reads the first one's results file
 
-    python bench.py [--gpus 1] [--steps K] [--warmup W] [--workload NAME]
+The line holds these parts in short; --record writes them whole.
+
+    python bench.py [--gpus 1] [--steps K] [--warmup W] [--workload NAME] [--record FILE]
 """
 import argparse
 import json
@@ -82,6 +84,8 @@ def main():
     ap.add_argument("--gpus", type=int, default=1)
     ap.add_argument("--steps", type=int, default=20)
     ap.add_argument("--warmup", type=int, default=3)
+    ap.add_argument("--record", default="", metavar="FILE",
+                    help="write the whole record as JSON: every candidate's median of the exhaustive sweeps, unrounded")
     ap.add_argument("--workload", default="bf16_m_sweep", choices=sorted(WORKLOAD_TEXT))
     ap.add_argument("--no-cpu-baseline", action="store_true")
     ap.add_argument("--no-configs", action="store_true", help="skip the other workloads of the metric")
@@ -301,7 +305,48 @@ def main():
         "untuned_default": untuned, "offline": offline, "rt_tune": rt,
         "configs": configs["workloads"] if configs else None,
     }
-    print(json.dumps(out))
+    if args.record:
+        with open(args.record, "w") as f:
+            json.dump(out, f)
+    print(json.dumps(line_of(out), separators=(",", ":")))
+
+
+# What the printed line leaves to --record.  Programs that keep the last few
+# KB of a run's output must find the line whole, so it holds what the metric's
+# parts are judged by, with five digits outside the contract's own fields.
+ROW_LEFT_OUT = ("rotated_copies", "batched_reps", "plan_candidates", "candidates_measured", "lda", "ldb", "warm_call_s",
+                "roofline_frac_resident")
+
+
+def rounded(v):
+    if isinstance(v, float):
+        return float("%.5g" % v)
+    if isinstance(v, dict):
+        return {k: rounded(x) for k, x in v.items()}
+    return [rounded(x) for x in v] if isinstance(v, (list, tuple)) else v
+
+
+def line_of(record):
+    def row(r):
+        r = {k: v for k, v in r.items() if k not in ROW_LEFT_OUT}
+        if "exhaustive" in r:
+            r["exhaustive"] = {k: v for k, v in r["exhaustive"].items() if k != "medians_us"}
+        return r
+
+    out = dict(record)
+    out["per_problem"] = [row(r) for r in out["per_problem"]]
+    if out["configs"]:
+        out["configs"] = {n: [row(r) for r in c["per_problem"]] for n, c in out["configs"].items()}
+    for k in ("untuned_default", "offline"):
+        if out[k]:
+            out[k] = {**out[k], "per_problem": [[r["candidate"], r["batched_us"]] for r in out[k]["per_problem"]]}
+    if out["warm_dispatch"]:
+        out["warm_dispatch"] = {k: v for k, v in out["warm_dispatch"].items() if k != "method"}
+    if out["rt_tune"]:
+        out["rt_tune"] = {k: [[r["size"], r["first_call_ms"], r["next20_min_ms"], r["first_call"]["tunes"]] for r in v["rows"]]
+                          if isinstance(v, dict) and "rows" in v else v for k, v in out["rt_tune"].items()}
+    exact = ("value", "ms_per_step")
+    return {k: v if k in exact else rounded(v) for k, v in out.items()}
 
 
 def make_problems(gt, torch, wl, workload, problems, stream):
