@@ -313,7 +313,7 @@ def main():
 
 # What the printed line leaves to --record.  Programs that keep the last few
 # KB of a run's output must find the line whole, so it holds what the metric's
-# parts are judged by, with five digits outside the contract's own fields.
+# parts are read from, with five digits outside its value and step time.
 ROW_LEFT_OUT = ("rotated_copies", "batched_reps", "plan_candidates", "candidates_measured", "lda", "ldb", "warm_call_s",
                 "roofline_frac_resident")
 

@@ -1,5 +1,5 @@
 """The benchmark's printed line: whole and short enough for programs that keep
-the last few KB of a run's output, with the contract's fields as measured.
+the last few KB of a run's output, with the metric's fields as measured.
 """
 import json
 
