@@ -19,6 +19,9 @@ DTYPES = {"f32": F32, "f16": F16, "bf16": BF16, "e4m3": FP8_E4M3}
 LAYOUTS = {"NN": NN, "NT": NT, "TN": TN, "TT": TT}
 QUANT = {"none": 0, "tensor": 1, "row": 2}
 W4_FORMATS = {"int4": 0, "e2m1": 1}
+SCORES = {"softmax": 0, "sigmoid": 1}
+EXPERT_FORMATS = dict(W4_FORMATS, none=-1)
+ACTIVATIONS = {"silu": 0, "gelu": 1}
 STATUS = {0: "GT_OK", 1: "GT_ERR_INVALID_ARG", 2: "GT_ERR_UNSUPPORTED", 3: "GT_ERR_HIP", 4: "GT_ERR_NOT_FOUND",
           5: "GT_ERR_IO", 6: "GT_ERR_VALIDATION", 7: "GT_ERR_OOM", 8: "GT_ERR_NO_DEVICE"}
 
@@ -80,6 +83,43 @@ class W4ExpandDesc(OperatorDesc):
         (n, ctypes.c_int32) for n in ("out_dtype", "format", "scale_dtype", "group")] + [("stream", ctypes.c_void_p)]
 
 
+class BesideDesc(OperatorDesc):
+    """A descriptor that also knows its tensors' GPU, which has to be the
+    current one when it runs."""
+    gpu = None
+
+    def keep(self, *tensors):
+        OperatorDesc.keep(self, *tensors)
+        if tensors[0].is_cuda:
+            self.gpu = tensors[0].device.index
+        return self
+
+
+class RouteDesc(BesideDesc):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("logits", "index", "weight")] + [
+        (n, ctypes.c_int64) for n in ("M", "E", "topk", "ldl", "ldi", "ldw")] + [
+        (n, ctypes.c_int32) for n in ("dtype", "score", "normalise")] + [
+        ("scale", ctypes.c_float), ("stream", ctypes.c_void_p)]
+
+
+class MoeDesc(BesideDesc):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("x", "index", "weight", "gate_up", "gate_up_scales", "down", "down_scales", "base",
+                                               "y", "workspace")] + [
+        (n, ctypes.c_int64) for n in ("workspace_bytes", "M", "K", "H", "E", "topk", "ldx", "ldi", "ldw", "ldb", "ldy",
+                                      "gate_up_ld", "gate_up_stride", "down_ld", "down_stride", "gate_up_scale_lde",
+                                      "gate_up_scale_ldn", "gate_up_scale_ldg", "down_scale_lde", "down_scale_ldn",
+                                      "down_scale_ldg")] + [
+        (n, ctypes.c_int32) for n in ("x_dtype", "out_dtype", "format", "scale_dtype", "group", "activation")] + [
+        ("stream", ctypes.c_void_p)]
+
+
+class LoraDesc(BesideDesc):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("x", "index", "a", "b", "scale", "base", "y", "workspace")] + [
+        (n, ctypes.c_int64) for n in ("workspace_bytes", "M", "K", "N", "adapters", "rank", "ldx", "ldb", "ldy", "a_ld",
+                                      "a_stride", "b_ld", "b_stride")] + [
+        (n, ctypes.c_int32) for n in ("x_dtype", "out_dtype")] + [("stream", ctypes.c_void_p)]
+
+
 class TuneFileReport(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int64) for n in ("rows", "tuned", "present", "skipped")]
 
@@ -137,6 +177,11 @@ def lib():
             "gt_rmsnorm_backward": [P(RmsNormBwdDesc)],
             "gt_w4_matmul": [P(W4Desc)],
             "gt_w4_expand": [P(W4ExpandDesc)],
+            "gt_route": [P(RouteDesc)],
+            "gt_moe": [P(MoeDesc)],
+            "gt_lora": [P(LoraDesc)],
+            "gt_moe_workspace": [P(MoeDesc), P(i64)],
+            "gt_lora_workspace": [P(LoraDesc), P(i64)],
             "gt_test_alloc_count": [P(ctypes.c_uint64), P(ctypes.c_uint64)],
             "gt_test_fail_allocs": [i32],
             "gt_make_key": [P(Desc), p, ctypes.c_char_p, ctypes.c_size_t],
@@ -389,6 +434,125 @@ def make_w4_expand_desc(qweight, scales, out, format="int4", group=128, stream=N
     return d.keep(qweight, scales, out)
 
 
+# ---- experts and adapters beside the product
+def _indices(t, shape, what):
+    """Leading dimension of int32 indices of this shape, a row's contiguous."""
+    if str(t.dtype) != "torch.int32":
+        raise ValueError("%s is %s, not torch.int32" % (what, t.dtype))
+    if len(shape) == 1:
+        if tuple(t.shape) != shape or (shape[0] > 1 and t.stride(0) != 1):
+            raise ValueError("%s must be %d contiguous elements" % (what, shape[0]))
+        return 0
+    return _matrix(t, shape, what)
+
+
+def _matrices(t, shape, what):
+    """(row stride, matrix stride) of matrices whose rows are contiguous, and
+    neither rows nor matrices broadcast.  A dimension of one says nothing."""
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s has shape %s, not %s" % (what, tuple(t.shape), tuple(shape)))
+    E, N, K = shape
+    if K > 1 and t.stride(2) != 1:
+        raise ValueError("%s: the elements of a row must be contiguous" % what)
+    ld = t.stride(1) if N > 1 else max(K, 1)
+    stride = t.stride(0) if E > 1 else max(N, 1) * ld
+    if ld < K or stride < K or ld < 1 or stride < 1:
+        raise ValueError("%s: broadcast or overlapping rows are not taken" % what)
+    return ld, stride
+
+
+def _expert_weights(w, scales, shape, format, group, dtype, what):
+    """(row stride, matrix stride, the scales' three strides and type) of E x N
+    x K weights: of the rows' type, or bytes of 4-bit codes with scales."""
+    E, N, K = shape
+    if format == EXPERT_FORMATS["none"]:
+        if _type_of(w, what) != dtype:
+            raise ValueError("%s is %s" % (what, w.dtype))
+        if scales is not None:
+            raise ValueError("scales belong to 4-bit weights")
+        return _matrices(w, shape, what) + (0, 0, 0, F32)
+    if str(w.dtype) != "torch.uint8":
+        raise ValueError("%s must be bytes (torch.uint8)" % what)
+    if group not in (32, 64, 128):
+        raise ValueError("group must be 32, 64 or 128")
+    if scales is None:
+        raise ValueError("%s: 4-bit weights come with scales" % what)
+    G = -(-K // group)
+    if tuple(scales.shape) != (E, N, G):
+        raise ValueError("scales of %s have shape %s, not %s" % (what, tuple(scales.shape), (E, N, G)))
+    sn = scales.stride(1) if N > 1 else max(1, G)
+    strides = (scales.stride(0) if E > 1 else max(1, N * sn), sn, scales.stride(2) if G > 1 else 1)
+    if E and N and G and min(strides) < 1:
+        raise ValueError("scales of %s: broadcast strides are not taken" % what)
+    return _matrices(w, (E, N, -(-K // 2)), what) + tuple(max(1, v) for v in strides) + (_type_of(scales, "scales of " + what),)
+
+
+def _workspace(t):
+    """(address, bytes) of a workspace tensor, or none."""
+    if t is None:
+        return None, 0
+    if not t.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return _ptr(t), t.numel() * t.element_size()
+
+
+def make_route_desc(logits, index, weight, score="softmax", normalise=True, scale=1.0, stream=None):
+    """Descriptor of gt_route from tensors: logits M x E, index (int32) and
+    weight (float32) M x topk."""
+    M, E = logits.shape
+    k = index.shape[1]
+    d = RouteDesc(_ptr(logits), _ptr(index), _ptr(weight), M, E, k, _matrix(logits, (M, E), "logits"),
+                  _indices(index, (M, k), "index"), _matrix(weight, (M, k), "weight", F32), _type_of(logits, "logits"),
+                  _code(score, SCORES), int(bool(normalise)), scale, _ptr(stream))
+    return d.keep(logits, index, weight)
+
+
+def make_moe_desc(x, index, weight, gate_up, down, y, base=None, gate_up_scales=None, down_scales=None, format="none", group=128,
+                  activation="silu", workspace=None, stream=None):
+    """Descriptor of gt_moe from tensors: x and y M x K, index (int32) and
+    weight (float32) M x topk, gate_up E x 2H x K and down E x K x H (of x's
+    type, or bytes with two codes each for the formats of 4 bits, whose scales
+    are E x 2H x ceil(K/group) and E x K x ceil(H/group))."""
+    M, K = x.shape
+    k, E, fmt, dt = index.shape[1], gate_up.shape[0], _code(format, EXPERT_FORMATS), _type_of(x, "x")
+    if gate_up.shape[1] % 2:
+        raise ValueError("gate_up has an odd number of rows")
+    H = gate_up.shape[1] // 2
+    gl, gs, ge, gn, gg, gdt = _expert_weights(gate_up, gate_up_scales, (E, 2 * H, K), fmt, group, dt, "gate_up")
+    dl, ds, de, dn, dg, ddt = _expert_weights(down, down_scales, (E, K, H), fmt, group, dt, "down")
+    if gdt != ddt:
+        raise ValueError("scales of two types")
+    odt = _type_of(y, "y")
+    ws, nbytes = _workspace(workspace)
+    d = MoeDesc(_ptr(x), _ptr(index), _ptr(weight), _ptr(gate_up), _ptr(gate_up_scales), _ptr(down), _ptr(down_scales), _ptr(base),
+                _ptr(y), ws, nbytes, M, K, H, E, k, _matrix(x, (M, K), "x"), _indices(index, (M, k), "index"),
+                _matrix(weight, (M, k), "weight", F32), 0 if base is None else _matrix(base, (M, K), "base", odt),
+                _matrix(y, (M, K), "y"), gl, gs, dl, ds, ge, gn, gg, de, dn, dg, dt, odt, fmt, gdt, group,
+                _code(activation, ACTIVATIONS), _ptr(stream))
+    return d.keep(x, index, weight, gate_up, down, y, base, gate_up_scales, down_scales, workspace)
+
+
+def make_lora_desc(x, index, a, b, y, base=None, scale=None, workspace=None, stream=None):
+    """Descriptor of gt_lora from tensors: x M x K, index (int32) M, a adapters
+    x rank x K, b adapters x N x rank, scale (float32) adapters, y and base M x
+    N (base may be y itself)."""
+    M, K = x.shape
+    L, r, _ = a.shape
+    N, dt, odt = b.shape[1], _type_of(x, "x"), _type_of(y, "y")
+    for t, what in ((a, "a"), (b, "b")):
+        if _type_of(t, what) != dt:
+            raise ValueError("%s is %s" % (what, t.dtype))
+    _indices(index, (M,), "index")
+    _vector(scale, L, "scale", F32)
+    al, as_ = _matrices(a, (L, r, K), "a")
+    bl, bs = _matrices(b, (L, N, r), "b")
+    ws, nbytes = _workspace(workspace)
+    d = LoraDesc(_ptr(x), _ptr(index), _ptr(a), _ptr(b), _ptr(scale), _ptr(base), _ptr(y), ws, nbytes, M, K, N, L, r,
+                 _matrix(x, (M, K), "x"), 0 if base is None else _matrix(base, (M, N), "base", odt), _matrix(y, (M, N), "y"), al,
+                 as_, bl, bs, dt, odt, _ptr(stream))
+    return d.keep(x, index, a, b, y, base, scale, workspace)
+
+
 def _run_operator(call, desc):
     if desc.elsewhere:
         raise ValueError("tensors on %s: the operators run on a GPU" % desc.elsewhere)
@@ -409,6 +573,41 @@ def gt_w4_matmul(desc):
 
 def gt_w4_expand(desc):
     _run_operator(lib().gt_w4_expand, desc)
+
+
+def _run_beside(call, desc):
+    if desc.gpu is not None:
+        import torch
+
+        if torch.cuda.current_device() != desc.gpu:
+            raise ValueError("tensors on GPU %d, which is not the current device" % desc.gpu)
+    _run_operator(call, desc)
+
+
+def gt_route(desc):
+    _run_beside(lib().gt_route, desc)
+
+
+def gt_moe(desc):
+    _run_beside(lib().gt_moe, desc)
+
+
+def gt_lora(desc):
+    _run_beside(lib().gt_lora, desc)
+
+
+def gt_moe_workspace(desc):
+    """Bytes of workspace that the call takes (make_moe_desc's workspace)."""
+    n = ctypes.c_int64(0)
+    _check(lib().gt_moe_workspace(ctypes.byref(desc), ctypes.byref(n)))
+    return n.value
+
+
+def gt_lora_workspace(desc):
+    """Bytes of workspace that the call takes (make_lora_desc's workspace)."""
+    n = ctypes.c_int64(0)
+    _check(lib().gt_lora_workspace(ctypes.byref(desc), ctypes.byref(n)))
+    return n.value
 
 
 # ---- control

@@ -32,9 +32,10 @@ HIP_FLAGS = ["--offload-arch=" + ARCH, "-O3", "-std=c++17", "-fPIC", "-Wno-unuse
 HOST_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-function", "-D__HIP_PLATFORM_AMD__",
               "-I", os.path.join(ROCM, "include"), "-I", CSRC, "-I", GEN]
 HOST_SOURCES = ["key.cpp", "candidates.cpp", "tuner.cpp", "cache.cpp", "device.cpp", "heuristic.cpp", "offline.cpp", "api.cpp",
-                "operators.cpp"]
+                "operators.cpp", "experts.cpp"]
 # the kernels written out by hand; the tile kernels are generated beside them
-HIP_SOURCES = ["small_kernels.hip", "gemv.hip", "scratch.hip", "rmsnorm.hip", "w4.hip"] + [
+HIP_SOURCES = ["small_kernels.hip", "gemv.hip", "scratch.hip", "rmsnorm.hip", "w4.hip", "route.hip",
+               "experts.hip", "lora.hip"] + [
     "w4_%s_%s.hip" % (x, f) for x in ("bf16", "f16", "e4m3") for f in ("int4", "e2m1")]
 
 

@@ -101,6 +101,60 @@ struct W4ExpandArgs {
   hipStream_t stream;
 };
 
+// The experts of each row by its logits (route.hip).
+struct RouteArgs {
+  const void* logits;
+  int32_t* index;
+  float* weight;
+  int64_t M, ldl, ldi, ldw;
+  int E, topk, dtype;
+  bool sigmoid, normalise;
+  float scale;
+  int cus;
+  hipStream_t stream;
+};
+
+// E matrices of weights, row-major: 16-bit elements or 4-bit codes.  Strides
+// in bytes; a scale (e, n, g) is at e * s_lde + n * s_ldn + g * s_ldg.
+struct ExpertWeights {
+  const char* p;
+  const void* scales;
+  int64_t ld, stride, s_lde, s_ldn, s_ldg;
+};
+
+// A layer of gated experts (experts.hip) for a range of tokens, whose
+// (token, slot) pairs are numbered token * topk + slot.
+struct MoeArgs {
+  const void* x;
+  const int32_t* index;
+  const float* weight;
+  ExpertWeights gate_up, down;
+  const void* base;
+  void* y;
+  int64_t M, K, H, ldx, ldi, ldw, ldb, ldy;
+  int E, topk;
+  int x_dtype, out_dtype, format, scale_dtype, group_lg, activation;
+  char* ws;
+  int cus;
+  hipStream_t stream;
+};
+
+// Rows' adapters (lora.hip).
+struct LoraArgs {
+  const void* x;
+  const int32_t* index;
+  ExpertWeights a, b;
+  const float* scale;
+  const void* base;
+  void* y;
+  int64_t M, K, N, ldx, ldb, ldy;
+  int adapters, rank;
+  int x_dtype, out_dtype;
+  char* ws;
+  int cus;
+  hipStream_t stream;
+};
+
 // Launcher status codes (0 = launched).
 enum LaunchStatus { LS_OK = 0, LS_UNSUPPORTED = 1, LS_HIP_ERROR = 2 };
 

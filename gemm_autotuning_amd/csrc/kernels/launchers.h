@@ -38,6 +38,19 @@ int launch_w4_matmul(const W4Args& a, void* ws, int cus);
 size_t w4_workspace_bytes(const W4Args& a, int cus);
 int launch_w4_expand(const W4ExpandArgs& a, int cus);
 
+// experts and adapters beside the product: route.hip, experts.hip, lora.hip.
+// A launch takes the rows that one range has (all of them where there is no
+// workspace); ws: the bytes for that many, 16-byte aligned.
+int launch_route(const RouteArgs& a);
+int64_t moe_range(const MoeArgs& a);  // tokens that one launch takes at most
+size_t moe_workspace_bytes(const MoeArgs& a, int64_t tokens);
+int launch_moe(const MoeArgs& a);
+int64_t lora_range(const LoraArgs& a);
+size_t lora_workspace_bytes(const LoraArgs& a, int64_t rows);
+int launch_lora(const LoraArgs& a);
+// y = base, or zeros without one; nothing where they are one matrix
+int launch_copy_rows(const void* base, void* y, int64_t M, int64_t N, int64_t ldb, int64_t ldy, int dtype, hipStream_t stream);
+
 // Workspace layout shared by every candidate: a fixed region of counters
 // first (GEMV slice counters; zero between launches, each launch leaves them
 // zero), then the data region (fp32 partial sums).  Nothing but those

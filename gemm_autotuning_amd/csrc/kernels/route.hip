@@ -1,0 +1,124 @@
+// route.hip -- the experts of each row by its logits.
+//
+// A row is held by LANES lanes, PER logits each, as unsigned keys in the
+// order of the floats (a NaN above all of them, -0 as +0); topk times the
+// largest key is joined over the lanes and taken out.  Equal keys go to the
+// lowest index by a second join, which only rows with ties make.
+#include "elements.h"
+#include "launchers.h"
+
+namespace gtk {
+
+__device__ __forceinline__ uint32_t order_key(float f) {
+  const uint32_t u = __float_as_uint(f + 0.f);  // -0 becomes +0
+  if (f != f) return 0xffffffffu;
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float of_key(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
+}
+constexpr uint32_t kMasked = 0x007fffffu;  // the key of -infinity; 0 is below every key
+
+// A value joined over LANES neighbouring lanes, the same in all of them.
+template <int LANES, class F>
+__device__ __forceinline__ uint32_t lanes_join(uint32_t v, F f) {
+  if constexpr (LANES == 64) return wave_join(v, f);
+  v = f(v, dpp<0xB1>(v));
+  v = f(v, dpp<0x4E>(v));
+  v = f(v, dpp<0x141>(v));
+  return f(v, dpp<0x140>(v));
+}
+template <int LANES>
+__device__ __forceinline__ float lanes_sum(float v) {
+  return __uint_as_float(lanes_join<LANES>(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+    return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+  }));
+}
+
+template <int LANES, int PER>
+__global__ __launch_bounds__(256) void route_kernel(gt::RouteArgs a) {
+  constexpr int kRows = 256 / LANES;
+  const int lane = threadIdx.x % LANES;
+  const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / LANES;
+  const int64_t m = row < a.M ? row : a.M - 1;  // every lane takes part in the joins
+  const char* p = static_cast<const char*>(a.logits) + m * a.ldl * (a.dtype == DT_F32 ? 4 : 2);
+  uint32_t key[PER];
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    const int e = j * LANES + lane;
+    key[j] = e < a.E ? order_key(load_any(p, e, a.dtype)) : 0u;
+  }
+  auto largest = [](uint32_t x, uint32_t y) { return x > y ? x : y; };
+  uint32_t mine = 0;
+#pragma unroll
+  for (int j = 0; j < PER; ++j) mine = largest(mine, key[j]);
+  const uint32_t top = lanes_join<LANES>(mine, largest);
+  const float most = top > kMasked ? of_key(top) : 0.f;  // nothing left: no sum is used
+  float all = 0.f;
+  if (!a.sigmoid && !a.normalise) {
+#pragma unroll
+    for (int j = 0; j < PER; ++j) all += key[j] > kMasked ? __expf(of_key(key[j]) - most) : 0.f;
+    all = lanes_sum<LANES>(all);
+  }
+  int chosen = -1;          // of slot `lane`
+  float logit = 0.f;
+  uint32_t best = top;
+  for (int s = 0; s < a.topk; ++s) {
+    if (s > 0) {
+      mine = 0;
+#pragma unroll
+      for (int j = 0; j < PER; ++j) mine = largest(mine, key[j]);
+      best = lanes_join<LANES>(mine, largest);
+    }
+    if (best <= kMasked) best = 0u;  // nothing is left: no key is taken out
+    int at = 0x7fffffff;
+#pragma unroll
+    for (int j = PER - 1; j >= 0; --j) at = best && key[j] == best ? j * LANES + lane : at;
+    at = (int)lanes_join<LANES>((uint32_t)at, [](uint32_t x, uint32_t y) { return x < y ? x : y; });
+#pragma unroll
+    for (int j = 0; j < PER; ++j) key[j] = at == j * LANES + lane ? 0u : key[j];
+    if (lane == s) {
+      chosen = best ? at : -1;
+      logit = of_key(best);
+    }
+  }
+  // With m = min(largest, 0) a sigmoid is exp(m) times what is here, so that
+  // the quotient by the sum stands where all of them are below fp32's range.
+  float w = 0.f;
+  if (chosen >= 0) {
+    if (a.sigmoid) {
+      const float low = a.normalise && most < 0.f ? most : 0.f;
+      w = logit >= 0.f ? 1.f / (1.f + expf(-logit)) : expf(logit - low) / (1.f + expf(logit));
+    } else {
+      w = expf(logit - most);
+    }
+  }
+  if (a.normalise) all = lanes_sum<LANES>(w);
+  if (a.normalise || !a.sigmoid) w = w / all;
+  if (row < a.M && lane < a.topk) {
+    a.index[row * a.ldi + lane] = chosen;
+    a.weight[row * a.ldw + lane] = chosen >= 0 ? w * a.scale : 0.f;
+  }
+}
+
+}  // namespace gtk
+
+namespace gt {
+
+int launch_route(const RouteArgs& a) {
+  const bool few = a.topk > 16 || a.E > 256;
+  const int64_t blocks = few ? (a.M + 3) / 4 : (a.M + 15) / 16;
+  if (blocks > 0x7fffff) return LS_UNSUPPORTED;
+  const dim3 grid((unsigned)blocks), block(256);
+#define GT_ROUTE(LANES, PER) \
+  if (a.E <= LANES * PER) { hipLaunchKernelGGL((gtk::route_kernel<LANES, PER>), grid, block, 0, a.stream, a); }
+  if (few) {
+    GT_ROUTE(64, 4) else GT_ROUTE(64, 8) else GT_ROUTE(64, 16)
+  } else {
+    GT_ROUTE(16, 4) else GT_ROUTE(16, 8) else GT_ROUTE(16, 16)
+  }
+#undef GT_ROUTE
+  return hipGetLastError() == hipSuccess ? LS_OK : LS_HIP_ERROR;
+}
+
+}  // namespace gt

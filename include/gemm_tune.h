@@ -382,6 +382,137 @@ typedef struct gt_w4_expand_desc {
 /* Errors as gt_w4_matmul.  N == 0 or K == 0 is a no-op. */
 gt_status gt_w4_expand(const gt_w4_expand_desc* d);
 
+/* ---- experts and adapters beside the product ---------------------------- */
+
+/* What a batch of requests meets beside the shared products: the choice of
+ * experts from a router's logits (a product of gemm_tuned), a whole layer of
+ * gated experts for a few tokens, and the low-rank adapters that requests
+ * bring to a shared projection.  All are in the manner of the operators
+ * above.  Indices are int32 in device memory, where the host cannot check
+ * them: one outside its range means "none" and is never followed. */
+typedef enum gt_score { GT_SCORE_SOFTMAX = 0, GT_SCORE_SIGMOID = 1 } gt_score;
+
+/* For every row the topk experts of the largest logits, in descending order,
+ * equal logits by ascending index, and their weights:
+ *   softmax: exp(l_i) / sum exp(l), over all experts, or over the chosen ones
+ *            with normalise;
+ *   sigmoid: 1 / (1 + exp(-l_i)), over their sum with normalise;
+ * times scale, in fp32.  A logit of -infinity masks its expert: it is never
+ * chosen, and slots for which none is left get index -1 and weight 0.  A NaN
+ * ranks above every number and its weight, with a softmax or normalise all
+ * weights of its row, are NaN (as +infinity's are with a softmax). */
+typedef struct gt_route_desc {
+  const void* logits; /* M x E, ldl                                          */
+  int32_t* index;     /* M x topk, ldi                                       */
+  float* weight;      /* M x topk, ldw                                       */
+  int64_t M, E, topk; /* topk <= E <= 1024, topk <= 64                       */
+  int64_t ldl, ldi, ldw;
+  int32_t dtype;     /* f32, f16, bf16                                       */
+  int32_t score;     /* gt_score                                             */
+  int32_t normalise; /* 0 or 1                                               */
+  float scale;       /* finite                                               */
+  void* stream;
+} gt_route_desc;
+
+/* GT_ERR_INVALID_ARG: NULL operands, a bad enum, dimension, leading dimension
+ * or scale, topk outside 1..E, a misaligned pointer.  GT_ERR_UNSUPPORTED:
+ * e4m3 logits, E > 1024, topk > 64.  M == 0 is a no-op. */
+gt_status gt_route(const gt_route_desc* d);
+
+/* How weights of experts are stored: 16 bits as the rows, or 4 bits with
+ * group scales as gt_w4_matmul's (gt_w4_format's two). */
+#define GT_WEIGHTS_16BIT (-1)
+typedef enum gt_activation { GT_ACT_SILU = 0, GT_ACT_GELU = 1 /* its tanh form */ } gt_activation;
+
+/* A layer of gated experts: with e = index[t,j],
+ *   y[t] = base[t] + sum_j weight[t,j] * down_e (act(gate_e x[t]) * (up_e x[t]))
+ * Each expert's gate_up holds the H rows of gate, then the H rows of up, K
+ * long; its down holds K rows of H.  Sums, activations and what passes
+ * between the products are fp32; the down product takes them as two 16-bit
+ * parts (at least 16 bits of each value), and y is rounded once.  A token may
+ * name an expert twice; a slot whose index is outside 0..E-1 adds nothing.
+ *
+ * The weights of the experts that are named are read once for up to 16 of
+ * their rows, so this is for the few tokens of a decode batch: any M is
+ * taken, in ranges of tokens whose intermediate values fit 64 MiB, but a
+ * prompt's rows belong in one product per expert.
+ *
+ * The intermediate values take gt_moe_workspace bytes of device memory: the
+ * caller's workspace (16-byte aligned), or, where that is NULL, the stream's,
+ * which the first (largest) call allocates: make that call outside stream
+ * capture.  Calls and graph replays that overlap in time must not share a
+ * workspace: graphs captured on one stream and replayed on several need the
+ * caller's, one each. */
+typedef struct gt_moe_desc {
+  const void* x;              /* M x K, ldx                                  */
+  const int32_t* index;       /* M x topk, ldi                               */
+  const float* weight;        /* M x topk, ldw                               */
+  const void* gate_up;        /* E matrices of 2 H x K, rows gate_up_ld      */
+  const void* gate_up_scales; /* 4 bits: (e, n, g) at e * _lde + n * _ldn + g * _ldg */
+  const void* down;           /* E matrices of K x H, rows down_ld           */
+  const void* down_scales;
+  const void* base;           /* M x K, ldb, of y's type, or NULL; may be y
+                                 itself (same leading dimension)             */
+  void* y;                    /* M x K, ldy                                  */
+  void* workspace;            /* or NULL                                     */
+  int64_t workspace_bytes;
+  int64_t M, K, H, E, topk;   /* E <= 4096, topk <= 64                       */
+  int64_t ldx, ldi, ldw, ldb, ldy;
+  int64_t gate_up_ld, gate_up_stride; /* of rows and of experts, in elements */
+  int64_t down_ld, down_stride;       /* (4 bits: bytes); <= 0: dense        */
+  int64_t gate_up_scale_lde, gate_up_scale_ldn, gate_up_scale_ldg; /* elements; <= 0: dense */
+  int64_t down_scale_lde, down_scale_ldn, down_scale_ldg;
+  int32_t x_dtype;     /* f16, bf16: x, and 16-bit weights                   */
+  int32_t out_dtype;   /* f32, f16, bf16; -1: x_dtype                        */
+  int32_t format;      /* GT_WEIGHTS_16BIT or a gt_w4_format                 */
+  int32_t scale_dtype; /* f32, f16, bf16 (4 bits)                            */
+  int32_t group;       /* 32, 64 or 128 (4 bits)                             */
+  int32_t activation;  /* gt_activation                                      */
+  void* stream;
+} gt_moe_desc;
+
+/* GT_ERR_INVALID_ARG: a NULL operand, a bad enum, dimension, leading
+ * dimension, stride or group, a misaligned pointer, a workspace that is too
+ * small; also when the stream's would have to grow while the stream is being
+ * captured.  GT_ERR_UNSUPPORTED: f32 or e4m3 rows, e4m3 output or scales, E >
+ * 4096, topk > 64.  GT_ERR_OOM: no memory for the workspace.  M == 0 or K ==
+ * 0 is a no-op; H, E or topk == 0 leaves y = base (zeros without one). */
+gt_status gt_moe(const gt_moe_desc* d);
+/* The workspace's bytes (0 for none); pointers are not looked at. */
+gt_status gt_moe_workspace(const gt_moe_desc* d, int64_t* bytes);
+
+/* Adapters of many requests beside a shared projection: with a = index[m],
+ *   y[m] = base[m] + scale[a] * b_a (a_a x[m])
+ * where a_a is rank x K and b_a is N x rank (smaller ranks are padded with
+ * zeros).  base is the projection's own result, y itself to add in place; a
+ * row without an adapter (an index outside 0..adapters-1) is left as base, not
+ * written at all in place.  Sums and what passes between the products are
+ * fp32 (two 16-bit parts of it in the second, as gt_moe); y is rounded once.
+ * An adapter's weights are read once for up to 16 of its rows.  Workspace as
+ * gt_moe. */
+typedef struct gt_lora_desc {
+  const void* x;        /* M x K, ldx                                        */
+  const int32_t* index; /* M                                                 */
+  const void* a;        /* adapters of rank x K, rows a_ld, matrices a_stride */
+  const void* b;        /* adapters of N x rank, rows b_ld, matrices b_stride */
+  const float* scale;   /* adapters, or NULL for 1                           */
+  const void* base;     /* M x N, ldb, of y's type, or NULL; may be y itself */
+  void* y;              /* M x N, ldy                                        */
+  void* workspace;      /* or NULL                                           */
+  int64_t workspace_bytes;
+  int64_t M, K, N, adapters, rank; /* adapters <= 4096, rank <= 256          */
+  int64_t ldx, ldb, ldy;
+  int64_t a_ld, a_stride, b_ld, b_stride; /* elements; <= 0: dense           */
+  int32_t x_dtype;   /* f16, bf16: x, a and b                                */
+  int32_t out_dtype; /* f32, f16, bf16; -1: x_dtype                          */
+  void* stream;
+} gt_lora_desc;
+
+/* Errors as gt_moe (GT_ERR_UNSUPPORTED: adapters > 4096, rank > 256).  M == 0
+ * or N == 0 is a no-op; K, adapters or rank == 0 leaves y = base. */
+gt_status gt_lora(const gt_lora_desc* d);
+gt_status gt_lora_workspace(const gt_lora_desc* d, int64_t* bytes);
+
 /* ---- control ------------------------------------------------------------ */
 
 /* Enable or disable tuning on a miss (the enable-vs-tuning split of the
