@@ -36,7 +36,8 @@ HOST_SOURCES = ["key.cpp", "candidates.cpp", "tuner.cpp", "cache.cpp", "device.c
 # the kernels written out by hand; the tile kernels are generated beside them
 HIP_SOURCES = ["small_kernels.hip", "gemv.hip", "scratch.hip", "rmsnorm.hip", "w4.hip", "route.hip",
                "experts.hip", "lora.hip"] + [
-    "w4_%s_%s.hip" % (x, f) for x in ("bf16", "f16", "e4m3") for f in ("int4", "e2m1")]
+    "w4_%s_%s.hip" % (x, f) for x in ("bf16", "f16", "e4m3") for f in ("int4", "e2m1")] + [
+    "grouped_%s%s.hip" % (x, f) for x in ("bf16", "f16") for f in ("", "_int4", "_e2m1")]
 
 
 def _headers(kernel=False):

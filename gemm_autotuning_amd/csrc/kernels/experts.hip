@@ -1,10 +1,11 @@
-// experts.hip -- a layer of gated experts for a few tokens.
+// experts.hip -- a layer of gated experts for a few tokens: the gated product
+// into fp32 activations per (token, slot) pair, the down product of each pair
+// (grouped.h), and the pairs' weighted sum.
 #include "elements.h"
+#include "grouped.h"
 #include "launchers.h"
 
 namespace gtk {
-
-constexpr int kInt4 = 0, kE2m1 = 1;
 
 __device__ __forceinline__ float wave_sum(float v) {
   return __uint_as_float(wave_join(__float_as_uint(v), [](uint32_t a, uint32_t b) {
@@ -19,7 +20,7 @@ __device__ __forceinline__ float expert_weight(const gt::ExpertWeights& w, int64
   if (format < 0) return load_any(row, k, dtype);
   const uint32_t c = (uint8_t)row[k >> 1] >> (4 * (k & 1)) & 15u;
   float v;
-  if (format == kInt4) {
+  if (format == W4_INT4) {
     v = (float)((int)(c << 28) >> 28);
   } else {
     const uint32_t m = c & 7u;
@@ -29,12 +30,8 @@ __device__ __forceinline__ float expert_weight(const gt::ExpertWeights& w, int64
   return v * load_any(w.scales, e * w.s_lde + n * w.s_ldn + (k >> group_lg) * w.s_ldg, scale_dtype);
 }
 
-__device__ __forceinline__ float activated(float g, float u, int activation) {
-  // GELU's tanh form is g / (1 + exp(-2 z)), z = sqrt(2 / pi) (g + 0.044715 g^3)
-  const float z = activation == 0 ? g : 1.5957691216057308f * (g + 0.044715f * g * g * g);
-  return g / (1.f + expf(-z)) * u;
-}
-
+// Rows of weights too short for a lane's 16 bytes, or so far apart that a
+// tile's offsets pass 32 bits: a wave to an output.
 __global__ __launch_bounds__(256) void moe_up_kernel(gt::MoeArgs a, float* act) {
   const int lane = threadIdx.x & 63;
   const int64_t h = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
@@ -68,21 +65,135 @@ __global__ __launch_bounds__(256) void moe_down_kernel(gt::MoeArgs a, const floa
   if (lane == 0) store_out(a.y, t * a.ldy + n, y, a.out_dtype);
 }
 
+// y[t] = base[t] + sum_j weight[t,j] * part[t,j], four columns to a thread.
+__global__ __launch_bounds__(256) void moe_join_kernel(gt::MoeArgs a, const float* part, int64_t ld) {
+  const int64_t n = 4 * ((int64_t)blockIdx.x * 256 + threadIdx.x), t = blockIdx.y;
+  if (n >= a.K) return;
+  f32x4 y = {0.f, 0.f, 0.f, 0.f};
+  if (a.base) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (n + e < a.K) y[e] = load_any(a.base, t * a.ldb + n + e, a.out_dtype);
+  }
+  for (int j = 0; j < a.topk; ++j) {
+    const int e = a.index[t * a.ldi + j];
+    if (e < 0 || e >= a.E) continue;
+    y += a.weight[t * a.ldw + j] * *reinterpret_cast<const f32x4*>(part + (t * a.topk + j) * ld + n);
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (n + e < a.K) store_out(a.y, t * a.ldy + n + e, y[e], a.out_dtype);
+}
+
 }  // namespace gtk
 
 namespace gt {
+namespace {
+
+constexpr int64_t kMostPairs = 2048;
+
+struct MoeSpace {
+  int64_t act_ld, part_ld;
+  size_t act, part, bytes;  // offsets; the table of tiles comes first
+};
+MoeSpace space(const MoeArgs& a, int64_t tokens) {
+  MoeSpace s;
+  const int64_t pairs = tokens * a.topk;
+  s.act_ld = (a.H + 3) / 4 * 4;
+  s.part_ld = (a.K + 3) / 4 * 4;
+  s.act = ((size_t)pairs * sizeof(gtk::RowTile) + 255) / 256 * 256;
+  s.part = s.act + (size_t)pairs * s.act_ld * 4;
+  s.bytes = s.part + (size_t)pairs * s.part_ld * 4;
+  return s;
+}
+
+GroupedLaunch launcher(const MoeArgs& a) {
+  const bool bf = a.x_dtype == DT_BF16;
+  if (a.format == gtk::W4_INT4) return bf ? grouped_bf16_int4 : grouped_f16_int4;
+  if (a.format == gtk::W4_E2M1) return bf ? grouped_bf16_e2m1 : grouped_f16_e2m1;
+  return bf ? grouped_bf16 : grouped_f16;
+}
+
+// Whether a matrix' rows can be walked in whole units: 16 bytes of a row at
+// least, and a tile's offsets within 32 bits.
+bool in_units(const MoeArgs& a, const ExpertWeights& w, int64_t K) {
+  const int64_t row = a.format < 0 ? 2 * K : (K + 1) / 2;
+  const int64_t most = INT64_C(1) << 31;
+  if (row < 16 || w.ld > most / 16 || row > most / 2) return false;
+  if (a.format < 0) return true;
+  const int e = elem_bytes(a.scale_dtype);
+  return w.s_ldn <= most / 32 / e && w.s_ldg <= most / 2 / e / ((K >> a.group_lg) + 1);
+}
+
+GroupedCut cut(const MoeArgs& a, int units, bool down) {
+  GroupedCut c;
+  const bool k4 = a.format >= 0;
+  const int least = k4 ? 1 : 2, most = k4 ? (down ? 1 : 2) : 4;
+  c.U = least;
+  while (c.U < most && units > 8 * c.U) c.U *= 2;
+  c.wk = std::min(8, (units + c.U - 1) / c.U);
+  c.turns = (units + c.wk * c.U - 1) / (c.wk * c.U);
+  c.cols = 8 / c.wk;
+  return c;
+}
+
+int product(const MoeArgs& a, gtk::GroupedParams& p, int phase, int64_t tiles) {
+  const int unit = a.format < 0 ? 128 : 256;
+  const int units = (p.K + unit - 1) / unit;
+  const GroupedCut c = cut(a, units, phase == gtk::GROUPED_DOWN);
+  fill_cut(p, c, units, 1);
+  p.pairs = phase == gtk::GROUPED_GATE_UP ? (p.N + 15) / 16 : (p.N + 31) / 32;
+  const int64_t groups = (p.pairs + c.cols - 1) / c.cols;
+  p.pairs_each = (int)std::max<int64_t>(1, std::min<int64_t>(8, groups * tiles / (3 * a.cus)));
+  const int64_t wgs = (p.pairs + c.cols * p.pairs_each - 1) / (c.cols * p.pairs_each);
+  return launcher(a)(p, dim3((unsigned)wgs, (unsigned)tiles), 64 * c.wk * c.cols, phase, 1, c.U, a.stream);
+}
+
+}  // namespace
 
 int64_t moe_range(const MoeArgs& a) {
-  const int64_t pairs = ((int64_t)64 << 20) / (4 * a.H);
-  const int64_t t = (pairs < 2048 ? pairs : 2048) / a.topk;
-  return t > 0 ? t : 1;
+  const int64_t pairs = ((int64_t)64 << 20) / (4 * (a.H + a.K + 6));
+  return std::max<int64_t>(1, std::min(pairs, kMostPairs) / a.topk);
 }
-size_t moe_workspace_bytes(const MoeArgs& a, int64_t tokens) { return (size_t)(tokens * a.topk * a.H * 4); }
+size_t moe_workspace_bytes(const MoeArgs& a, int64_t tokens) { return space(a, tokens).bytes; }
 
 int launch_moe(const MoeArgs& a) {
-  float* act = reinterpret_cast<float*>(a.ws);
-  hipLaunchKernelGGL(gtk::moe_up_kernel, dim3((unsigned)((a.H + 3) / 4), (unsigned)(a.M * a.topk)), dim3(256), 0, a.stream, a, act);
-  hipLaunchKernelGGL(gtk::moe_down_kernel, dim3((unsigned)((a.K + 3) / 4), (unsigned)a.M), dim3(256), 0, a.stream, a, act);
+  const MoeSpace s = space(a, a.M);
+  float* act = reinterpret_cast<float*>(a.ws + s.act);
+  float* part = reinterpret_cast<float*>(a.ws + s.part);
+  if (!in_units(a, a.gate_up, a.K) || !in_units(a, a.down, a.H)) {
+    hipLaunchKernelGGL(gtk::moe_up_kernel, dim3((unsigned)((a.H + 3) / 4), (unsigned)(a.M * a.topk)), dim3(256), 0, a.stream, a, act);
+    hipLaunchKernelGGL(gtk::moe_down_kernel, dim3((unsigned)((a.K + 3) / 4), (unsigned)a.M), dim3(256), 0, a.stream, a, act);
+    return hipGetLastError() == hipSuccess ? LS_OK : LS_HIP_ERROR;
+  }
+  const int64_t pairs = a.M * a.topk, tiles = most_tiles(pairs, a.E, 16);
+  gtk::GroupedParams p{};
+  p.ix = gtk::RowIndex{a.index, a.ldi, (int)pairs, a.topk, a.E, 0};
+  p.table = reinterpret_cast<gtk::RowTile*>(a.ws);
+  p.scale_dtype = a.scale_dtype;
+  p.group_lg = a.group_lg;
+  p.activation = a.activation;
+  p.w = a.gate_up;
+  p.x = a.x;
+  p.ldx = a.ldx;
+  p.out = act;
+  p.ld_out = s.act_ld;
+  p.up = a.H;
+  p.N = (int)a.H;
+  p.K = (int)a.K;
+  int rc = product(a, p, gtk::GROUPED_GATE_UP, tiles);
+  if (rc != LS_OK) return rc;
+  p.w = a.down;
+  p.x = act;
+  p.ldx = s.act_ld;
+  p.out = part;
+  p.ld_out = s.part_ld;
+  p.N = (int)a.K;
+  p.K = (int)a.H;
+  rc = product(a, p, gtk::GROUPED_DOWN, tiles);
+  if (rc != LS_OK) return rc;
+  hipLaunchKernelGGL(gtk::moe_join_kernel, dim3((unsigned)((a.K + 1023) / 1024), (unsigned)a.M), dim3(256), 0, a.stream, a, part,
+                     s.part_ld);
   return hipGetLastError() == hipSuccess ? LS_OK : LS_HIP_ERROR;
 }
 

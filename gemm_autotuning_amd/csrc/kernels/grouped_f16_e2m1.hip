@@ -1,0 +1,6 @@
+// grouped_f16_e2m1.hip -- grouped products of f16 rows with e2m1 weights (grouped.h).
+#include "grouped.h"
+
+namespace gt {
+GT_GROUPED_LAUNCHER(grouped_f16_e2m1, DT_F16, gtk::W4_E2M1)
+}  // namespace gt
