@@ -101,6 +101,14 @@ gt_status on_workspace(DeviceState& dev, A& a, size_t need, void* own, int64_t o
   return launch(a);
 }
 
+// Workspace of the largest of a call's ranges: few rows may take more than
+// many (their sums are cut into more slices), so the last one counts too.
+template <class A, class B>
+size_t most_bytes(const A& a, int64_t most, B bytes) {
+  const size_t whole = bytes(a, std::min(a.M, most));
+  return a.M > most && a.M % most ? std::max(whole, bytes(a, a.M % most)) : whole;
+}
+
 // The descriptor's sizes and types.
 gt_status moe_shape(const gt_moe_desc* d, MoeArgs* a) {
   if (d->M < 0 || d->K < 0 || d->H < 0 || d->E < 0 || d->topk < 0) return invalid("negative dimension");
@@ -175,7 +183,7 @@ gt_status moe(const gt_moe_desc* d) {
     return launched(launch_copy_rows(a.base, a.y, a.M, a.K, a.ldb, a.ldy, a.out_dtype, a.stream), "gt_moe");
   }
   const int64_t most = moe_range(a);
-  return on_workspace(*dev, a, moe_workspace_bytes(a, std::min(a.M, most)), d->workspace, d->workspace_bytes, [&](MoeArgs& all) {
+  return on_workspace(*dev, a, most_bytes(a, most, moe_workspace_bytes), d->workspace, d->workspace_bytes, [&](MoeArgs& all) {
     for (int64_t m = 0; m < all.M; m += most) {
       MoeArgs r = all;
       r.M = std::min(most, all.M - m);
@@ -199,7 +207,7 @@ gt_status moe_workspace(const gt_moe_desc* d, int64_t* bytes) {
   DeviceState* dev = nullptr;
   GT_CHECK(current_device(&dev));
   a.cus = dev->cus;
-  *bytes = (int64_t)moe_workspace_bytes(a, std::min(a.M, moe_range(a)));
+  *bytes = (int64_t)most_bytes(a, moe_range(a), moe_workspace_bytes);
   return GT_OK;
 }
 
@@ -253,7 +261,7 @@ gt_status lora(const gt_lora_desc* d) {
     return launched(launch_copy_rows(a.base, a.y, a.M, a.N, a.ldb, a.ldy, a.out_dtype, a.stream), "gt_lora");
   }
   const int64_t most = lora_range(a);
-  return on_workspace(*dev, a, lora_workspace_bytes(a, std::min(a.M, most)), d->workspace, d->workspace_bytes, [&](LoraArgs& all) {
+  return on_workspace(*dev, a, most_bytes(a, most, lora_workspace_bytes), d->workspace, d->workspace_bytes, [&](LoraArgs& all) {
     for (int64_t m = 0; m < all.M; m += most) {
       LoraArgs r = all;
       r.M = std::min(most, all.M - m);
@@ -276,7 +284,7 @@ gt_status lora_workspace(const gt_lora_desc* d, int64_t* bytes) {
   DeviceState* dev = nullptr;
   GT_CHECK(current_device(&dev));
   a.cus = dev->cus;
-  *bytes = (int64_t)lora_workspace_bytes(a, std::min(a.M, lora_range(a)));
+  *bytes = (int64_t)most_bytes(a, lora_range(a), lora_workspace_bytes);
   return GT_OK;
 }
 

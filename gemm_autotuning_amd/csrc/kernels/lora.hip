@@ -1,8 +1,20 @@
-// lora.hip -- adapters of many requests beside a shared projection.
+// lora.hip -- adapters of many requests beside a shared projection: the first
+// product of each row (grouped.h, slices of K to workgroups where the rows are
+// few) into fp32 values, then the second one, which adds the slices, and the
+// base to its results.
 #include "elements.h"
+#include "grouped.h"
 #include "launchers.h"
 
 namespace gtk {
+
+struct ExpandParams {
+  gt::LoraArgs a;
+  const RowTile* table;
+  const float* mid;  // slice s, row m, rank r at (s * M + m) * ld + r
+  int64_t ld, slice;
+  int slices, blocks, blocks_each;  // blocks of 64 columns; of a wave
+};
 
 __device__ __forceinline__ float wave_sum(float v) {
   return __uint_as_float(wave_join(__float_as_uint(v), [](uint32_t a, uint32_t b) {
@@ -10,7 +22,197 @@ __device__ __forceinline__ float wave_sum(float v) {
   }));
 }
 
-__global__ __launch_bounds__(256) void lora_shrink_kernel(gt::LoraArgs a, float* mid) {
+// The second product: a wave holds the tile's 16 rows of up to 32 R values as
+// operands in two 16-bit parts and walks blocks of 64 columns, whose weights
+// (64 rows of the rank) and base it loads a block ahead.  What bounds it is
+// the weights with few rows and base and y with many; the results go through
+// LDS so that a row's 64 columns are read and written by eight lanes.
+template <int XT, int OUT, int R, bool NARROW>
+__global__ __launch_bounds__(256) void lora_expand_kernel(ExpandParams p) {
+  typedef W4Rows<XT> Op;
+  typedef typename Elem<OUT>::T TO;
+  constexpr int kPitch = 68;  // floats of a row of results in LDS
+  __shared__ RowTile tile;
+  __shared__ float h[16][32 * R + 4];
+  __shared__ float out[4][16][kPitch];
+  const gt::LoraArgs& a = p.a;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = lane & 15, kq = lane >> 4;
+  if (tid < 18) reinterpret_cast<int*>(&tile)[tid] = reinterpret_cast<const int*>(p.table + blockIdx.y)[tid];
+  __syncthreads();
+  const int matrix = __builtin_amdgcn_readfirstlane(tile.matrix);
+  if (matrix < 0) return;
+  const int rows = __builtin_amdgcn_readfirstlane(tile.count);
+  const bool some = matrix < a.adapters;
+  const int block0 = (blockIdx.x * 4 + wave) * p.blocks_each, block1 = min(block0 + p.blocks_each, p.blocks);
+
+  const char* const wb = a.b.p + (some ? matrix : 0) * a.b.stride;
+  typedef __attribute__((ext_vector_type(4))) uint32_t Raw;
+  // weights of 16 columns: a column's 8 values of each step of 32
+  auto load_weights = [&](int64_t n0, Raw (&w)[R]) __attribute__((always_inline)) {
+    const int64_t n = min(n0 + r, a.N - 1);
+    const uint16_t* row = reinterpret_cast<const uint16_t*>(wb + n * a.b.ld);
+    if constexpr (NARROW) {
+      uint16_t v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = kq == 0 && e < a.rank ? row[min(e, a.rank - 1)] : 0;
+      __builtin_memcpy(&w[0], v, 16);
+    } else {
+#pragma unroll
+      for (int j = 0; j < R; ++j) w[j] = *reinterpret_cast<const u32x4_any*>(row + min(32 * j + 8 * kq, a.rank - 8));
+    }
+  };
+  auto place_weights = [&](Raw (&w)[R], Chunk (&f)[R]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      Raw v = w[j];
+      if (!NARROW && 32 * (j + 1) > a.rank) v = bytes_from(v, max(0, 2 * (32 * j + 8 * kq - (a.rank - 8))));
+      __builtin_memcpy(&f[j], &v, 16);
+    }
+  };
+  Raw raw[4][R];
+  if (some && block0 < block1)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) load_weights(64 * (int64_t)block0 + 16 * c, raw[c]);
+
+  // the rows' values: the slices' sums, in order
+  Chunk x[R][2];
+  float back[4] = {1.f, 1.f, 1.f, 1.f};  // of this lane's four rows of results
+  if (some) {
+    for (int i = tid; i < 16 * 32 * R; i += 256) {
+      const int m = i / (32 * R), k = i % (32 * R);
+      float v = 0.f;
+      if (m < rows && k < a.rank) {
+        const float* at = p.mid + tile.rows[m] * p.ld + k;
+        for (int s0 = 0; s0 < p.slices; s0 += 4) {
+          float part[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) part[j] = at[min(s0 + j, p.slices - 1) * p.slice];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v += s0 + j < p.slices ? part[j] : 0.f;
+        }
+      }
+      h[m][k] = v;
+    }
+    __syncthreads();
+    float v[R][8];
+    uint32_t most = 0;
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      __builtin_memcpy(v[j], &h[r][32 * j + 8 * kq], 32);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) most = max(most, __float_as_uint(v[j][e]) & 0x7fffffffu);
+    }
+    if constexpr (XT == DT_F16) {
+      // the row's power of two, as in grouped.h
+      const auto half = __builtin_amdgcn_permlane16_swap(most, most, false, false);
+      most = max(half[0], half[1]);
+      const auto both = __builtin_amdgcn_permlane32_swap(most, most, false, false);
+      most = max(both[0], both[1]);
+      const uint32_t ex = most >> 23;
+      const uint32_t to = ex == 255 || ex == 0 ? 127u : min(253u, 268u - ex);
+      const float s = __uint_as_float(to << 23);
+#pragma unroll
+      for (int j = 0; j < R; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[j][e] *= s;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) back[e] = __shfl(__uint_as_float((254u - to) << 23), 4 * kq + e);
+    }
+#pragma unroll
+    for (int j = 0; j < R; ++j)
+#pragma unroll
+      for (int part = 0; part < 2; ++part) {
+        uint16_t b[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          float near;
+          if constexpr (XT == DT_BF16) {
+            const uint32_t top = __float_as_uint(v[j][e]) & 0xffff0000u;
+            b[e] = part == 0 ? (uint16_t)(top >> 16) : f32_to_bf16_bits(v[j][e]);
+            near = __uint_as_float(top);
+          } else {
+            b[e] = f32_to_f16_bits(v[j][e]);
+            near = f16_bits_to_f32(b[e]);
+          }
+          const float left = v[j][e] - near;
+          v[j][e] = left == left ? left : 0.f;
+        }
+        __builtin_memcpy(&x[j][part], b, 16);
+      }
+  }
+  const float scale = some && a.scale ? a.scale[matrix] : 1.f;
+
+  const int pass_row = lane >> 3, col = 8 * (lane & 7);
+  for (int block = block0; block < block1; ++block) {
+    const int64_t n0 = 64 * (int64_t)block;
+    const bool whole = n0 + 64 <= a.N;
+    float v[2][8];  // of rows pass_row and pass_row + 8: the base
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
+      const int m = pass_row + 8 * i;
+      if (a.base && m < rows) {
+        const TO* at = static_cast<const TO*>(a.base) + tile.rows[m] * a.ldb + n0 + col;
+        if (whole) {
+          Piece<OUT, 8> b;
+          b.load(at);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[i][e] = b.get(e);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (n0 + col + e < a.N) v[i][e] = Elem<OUT>::get(at[e]);
+        }
+      }
+    }
+    if (some) {
+      Chunk f[4][R];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) place_weights(raw[c], f[c]);
+      if (block + 1 < block1)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) load_weights(n0 + 64 + 16 * c, raw[c]);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+          Op::mma(acc, x[j][0], f[c][j]);
+          Op::mma(acc, x[j][1], f[c][j]);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) out[wave][4 * kq + e][16 * c + r] = acc[e] * back[e] * scale;
+      }
+      wave_lds_order();
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int m = pass_row + 8 * i;
+      if (m < rows) {
+        if (some) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[i][e] += out[wave][m][col + e];
+        }
+        TO* at = static_cast<TO*>(a.y) + tile.rows[m] * a.ldy + n0 + col;
+        if (whole) {
+          store_piece<OUT, 8>(at, v[i]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (n0 + col + e < a.N) at[e] = Elem<OUT>::put(v[i][e]);
+        }
+      }
+    }
+    wave_lds_order();
+  }
+}
+
+// Rows of x or of the adapters' first matrices too short for a lane's 16
+// bytes, or the latter so far apart that a tile's offsets pass 32 bits: a wave
+// to a value.
+__global__ __launch_bounds__(256) void lora_shrink_kernel(gt::LoraArgs a, float* mid, int64_t ld) {
   const int lane = threadIdx.x & 63, r = blockIdx.y * 4 + (threadIdx.x >> 6);
   for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x) {
     const int e = a.index[m];
@@ -19,26 +221,21 @@ __global__ __launch_bounds__(256) void lora_shrink_kernel(gt::LoraArgs a, float*
     float v = 0.f;
     for (int64_t k = lane; k < a.K; k += 64) v += load_any(a.x, m * a.ldx + k, a.x_dtype) * load_any(row, k, a.x_dtype);
     v = wave_sum(v);
-    if (lane == 0) mid[m * a.rank + r] = v;
+    if (lane == 0) mid[m * ld + r] = v;
   }
 }
 
-__global__ __launch_bounds__(256) void lora_expand_kernel(gt::LoraArgs a, const float* mid) {
-  for (int64_t m = blockIdx.y; m < a.M; m += gridDim.y) {
-    const int e = a.index[m];
-    const bool some = e >= 0 && e < a.adapters;
-    if (!some && a.base == a.y) continue;
-    for (int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x; n < a.N; n += (int64_t)gridDim.x * 256) {
-      float v = 0.f;
-      if (some) {
-        const char* row = a.b.p + e * a.b.stride + n * a.b.ld;
-        for (int r = 0; r < a.rank; ++r) v += mid[m * a.rank + r] * load_any(row, r, a.x_dtype);
-        v *= a.scale ? a.scale[e] : 1.f;
-      }
-      if (a.base) v += load_any(a.base, m * a.ldb + n, a.out_dtype);
-      store_out(a.y, m * a.ldy + n, v, a.out_dtype);
-    }
+// The tiles of those rows.
+__global__ __launch_bounds__(512) void lora_tiles_kernel(RowIndex ix, RowTile* table) {
+  __shared__ TileSearch<16> tile;
+  __shared__ uint32_t count[kMostMatrices + 1];
+  find_tile<16>(ix, blockIdx.x, tile, count);
+  const int tid = threadIdx.x;
+  if (tid == 0) {
+    table[blockIdx.x].matrix = tile.matrix;
+    table[blockIdx.x].count = tile.count;
   }
+  if (tid < 16) table[blockIdx.x].rows[tid] = tile.matrix >= 0 && tid < tile.count ? tile.rows[tid] : 0;
 }
 
 __global__ __launch_bounds__(256) void copy_rows_kernel(const void* base, void* y, int64_t M, int64_t N, int64_t ldb, int64_t ldy,
@@ -51,21 +248,116 @@ __global__ __launch_bounds__(256) void copy_rows_kernel(const void* base, void* 
 }  // namespace gtk
 
 namespace gt {
+namespace {
+
+constexpr int64_t kMostRows = 4096;
+
+bool in_units(const LoraArgs& a) { return a.K >= 8 && a.a.ld <= (INT64_C(1) << 27); }
+
+// The first product's slices: one workgroup's K where the tiles alone fill the
+// CUs, more where they do not.
+struct LoraCut {
+  GroupedCut c;
+  int units, split;
+};
+LoraCut cut(const LoraArgs& a, int64_t rows) {
+  LoraCut l;
+  const int64_t tiles = most_tiles(rows, a.adapters, 16);
+  l.units = (int)((a.K + 127) / 128);
+  const int pairs = (a.rank + 31) / 32;
+  const int64_t want = std::max<int64_t>(1, 2 * a.cus / (tiles * pairs));
+  l.c.wk = std::min(8, l.units);
+  l.split = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, 16), l.units / l.c.wk));
+  const int each = (l.units + l.c.wk * l.split - 1) / (l.c.wk * l.split);  // of a wave
+  l.c.U = each > 2 ? 4 : (each > 1 ? 2 : 1);
+  l.c.turns = (each + l.c.U - 1) / l.c.U;
+  l.c.cols = 8 / l.c.wk;
+  return l;
+}
+struct LoraSpace {
+  int64_t ld;
+  size_t mid, bytes;
+};
+LoraSpace space(const LoraArgs& a, int64_t rows) {
+  LoraSpace s;
+  s.ld = (a.rank + 3) / 4 * 4;
+  s.mid = ((size_t)most_tiles(rows, a.adapters + 1, 16) * sizeof(gtk::RowTile) + 255) / 256 * 256;
+  s.bytes = s.mid + (size_t)cut(a, rows).split * rows * s.ld * 4;
+  return s;
+}
+
+template <int XT, int OUT>
+int expand(const gtk::ExpandParams& p, dim3 grid) {
+  const int rank = p.a.rank;
+  hipStream_t st = p.a.stream;
+  if (rank < 8)
+    hipLaunchKernelGGL((gtk::lora_expand_kernel<XT, OUT, 1, true>), grid, dim3(256), 0, st, p);
+  else if (rank <= 32)
+    hipLaunchKernelGGL((gtk::lora_expand_kernel<XT, OUT, 1, false>), grid, dim3(256), 0, st, p);
+  else if (rank <= 64)
+    hipLaunchKernelGGL((gtk::lora_expand_kernel<XT, OUT, 2, false>), grid, dim3(256), 0, st, p);
+  else if (rank <= 128)
+    hipLaunchKernelGGL((gtk::lora_expand_kernel<XT, OUT, 4, false>), grid, dim3(256), 0, st, p);
+  else
+    hipLaunchKernelGGL((gtk::lora_expand_kernel<XT, OUT, 8, false>), grid, dim3(256), 0, st, p);
+  return hipGetLastError() == hipSuccess ? LS_OK : LS_HIP_ERROR;
+}
+template <int XT>
+int expand(const gtk::ExpandParams& p, dim3 grid) {
+  switch (p.a.out_dtype) {
+    case DT_F32: return expand<XT, DT_F32>(p, grid);
+    case DT_F16: return expand<XT, DT_F16>(p, grid);
+    default: return expand<XT, DT_BF16>(p, grid);
+  }
+}
+
+unsigned at_most(int64_t n, int64_t most) { return (unsigned)(n < most ? n : most); }
+
+}  // namespace
 
 int64_t lora_range(const LoraArgs& a) {
-  const int64_t rows = ((int64_t)64 << 20) / (4 * a.rank);
-  return rows;
+  // a row has up to 16 slices where the rows are few, one where they are many
+  return std::min<int64_t>(kMostRows, ((int64_t)64 << 20) / (16 * (4 * ((a.rank + 3) / 4 * 4) + 6)));
 }
-size_t lora_workspace_bytes(const LoraArgs& a, int64_t rows) { return (size_t)(rows * a.rank * 4); }
-
-static unsigned at_most(int64_t n, int64_t most) { return (unsigned)(n < most ? n : most); }
+size_t lora_workspace_bytes(const LoraArgs& a, int64_t rows) { return space(a, rows).bytes; }
 
 int launch_lora(const LoraArgs& a) {
-  float* mid = reinterpret_cast<float*>(a.ws);
-  hipLaunchKernelGGL(gtk::lora_shrink_kernel, dim3(at_most(a.M, 65536), (a.rank + 3) / 4), dim3(256), 0, a.stream, a, mid);
-  hipLaunchKernelGGL(gtk::lora_expand_kernel, dim3(at_most((a.N + 255) / 256, 1024), at_most(a.M, 32768)), dim3(256), 0, a.stream, a,
-                     mid);
-  return hipGetLastError() == hipSuccess ? LS_OK : LS_HIP_ERROR;
+  const LoraSpace s = space(a, a.M);
+  const int none = a.base != a.y;
+  const int64_t tiles = most_tiles(a.M, a.adapters + none, 16);
+  gtk::RowTile* table = reinterpret_cast<gtk::RowTile*>(a.ws);
+  float* mid = reinterpret_cast<float*>(a.ws + s.mid);
+  const gtk::RowIndex ix{a.index, 1, (int)a.M, 1, a.adapters, none};
+  int split = 1;
+  if (in_units(a)) {
+    const LoraCut l = cut(a, a.M);
+    split = l.split;
+    gtk::GroupedParams p{};
+    p.ix = ix;
+    p.table = table;
+    p.w = a.a;
+    p.x = a.x;
+    p.ldx = a.ldx;
+    p.out = mid;
+    p.ld_out = s.ld;
+    p.out_slice = a.M * s.ld;
+    p.N = a.rank;
+    p.K = (int)a.K;
+    fill_cut(p, l.c, l.units, l.split);
+    p.pairs = (p.N + 31) / 32;
+    p.pairs_each = 1;
+    const int rc = (a.x_dtype == DT_BF16 ? grouped_bf16 : grouped_f16)(
+        p, dim3((p.pairs + l.c.cols - 1) / l.c.cols, (unsigned)tiles, l.split), 64 * l.c.wk * l.c.cols, gtk::GROUPED_SHRINK, 1, l.c.U, a.stream);
+    if (rc != LS_OK) return rc;
+  } else {
+    hipLaunchKernelGGL(gtk::lora_tiles_kernel, dim3((unsigned)tiles), dim3(512), 0, a.stream, ix, table);
+    hipLaunchKernelGGL(gtk::lora_shrink_kernel, dim3(at_most(a.M, 65536), (a.rank + 3) / 4), dim3(256), 0, a.stream, a, mid, s.ld);
+  }
+  gtk::ExpandParams e{a, table, mid, s.ld, a.M * s.ld, split, (int)((a.N + 63) / 64), 1};
+  const int64_t groups = (e.blocks + 3) / 4;
+  e.blocks_each = (int)std::max<int64_t>(1, std::min<int64_t>(16, groups * tiles / (4 * a.cus)));
+  const dim3 grid((unsigned)((e.blocks + 4 * e.blocks_each - 1) / (4 * e.blocks_each)), (unsigned)tiles);
+  return a.x_dtype == DT_BF16 ? expand<DT_BF16>(e, grid) : expand<DT_F16>(e, grid);
 }
 
 int launch_copy_rows(const void* base, void* y, int64_t M, int64_t N, int64_t ldb, int64_t ldy, int dtype, hipStream_t stream) {

@@ -162,3 +162,24 @@ def test_nothing_to_add(none):
     base, index = br.normal((M, N), 1.0, BF, 1), torch.zeros(M, dtype=torch.int32)
     assert torch.equal(run(x, index, a, b, base=base, pad=2), base)
     assert (run(x, index, a, b, pad=2) == 0).all()
+
+
+@pytest.mark.parametrize("M,L,r,K", [(1, 1, 16, 4096), (3, 2, 40, 9000), (500, 1, 8, 5000), (4096, 3, 16, 256), (4097, 1, 16, 4096), (4596, 1, 16, 8192),
+                                     (9000, 9, 12, 2000), (5, 2, 7, 4)])
+def test_the_callers_workspace_is_enough_and_not_left(M, L, r, K):
+    g = ref.rng(M)
+    x = torch.randint(-1, 2, (M, K), generator=g).to(BF)
+    a, b = torch.randint(-1, 2, (L, r, K), generator=g).to(BF), torch.randint(-2, 3, (L, 64, r), generator=g).to(BF)
+    index = torch.randint(-1, L, (M,), generator=g, dtype=torch.int32)
+    y = torch.empty(M, 64, device="cuda")
+    args = (x.cuda(), index.cuda(), a.cuda(), b.cuda(), y)
+    n = gt.gt_lora_workspace(gt.make_lora_desc(*args))
+    buf = torch.full((n + 4096,), 0x5A, dtype=torch.uint8, device="cuda")
+    gt.gt_lora(gt.make_lora_desc(*args, workspace=buf[:n], stream=torch.cuda.current_stream().cuda_stream))
+    torch.cuda.synchronize()
+    assert (buf[n:] == 0x5A).all(), "written past the workspace"
+    want = torch.zeros(M, 64, dtype=torch.float64)
+    for e in range(L):
+        m = index == e
+        want[m] = (x[m].double() @ a[e].double().t()) @ b[e].double().t()
+    assert torch.equal(y.cpu().double(), want)

@@ -219,3 +219,18 @@ def test_nothing_to_add(none):
     w = dict(gate_up=torch.ones(E, 2 * H, K).to(BF), down=torch.ones(E, K, H).to(BF))
     assert torch.equal(run(x, index, weight, w, base=base, pad=2), base)
     assert (run(x, index, weight, w, pad=2) == 0).all()
+
+
+@pytest.mark.parametrize("T,E,k,K,H", [(1, 5, 3, 64, 48), (9, 300, 40, 33, 17), (700, 3, 3, 64, 32), (1400, 2, 2, 16, 8), (3, 2, 2, 4, 4)])
+def test_the_callers_workspace_is_enough_and_not_left(T, E, k, K, H):
+    x = ref.loud(T, K, 1).to(BF)
+    w = layer(E, H, K, BF, "none", 128, "bf16", 2)
+    index, weight = br.choices(T, E, k, 3)
+    y = torch.empty(T, K, device="cuda").bfloat16()
+    args = (x.cuda(), index.cuda(), weight.cuda(), w["gate_up"].cuda(), w["down"].cuda(), y)
+    n = gt.gt_moe_workspace(gt.make_moe_desc(*args))
+    buf = torch.full((n + 4096,), 0x5A, dtype=torch.uint8, device="cuda")
+    gt.gt_moe(gt.make_moe_desc(*args, workspace=buf[:n], stream=torch.cuda.current_stream().cuda_stream))
+    torch.cuda.synchronize()
+    assert (buf[n:] == 0x5A).all(), "written past the workspace"
+    assert torch.equal(y.cpu(), run(x, index, weight, w))
