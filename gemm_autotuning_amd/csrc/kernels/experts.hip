@@ -65,8 +65,9 @@ __global__ __launch_bounds__(256) void moe_down_kernel(gt::MoeArgs a, const floa
   if (lane == 0) store_out(a.y, t * a.ldy + n, y, a.out_dtype);
 }
 
-// y[t] = base[t] + sum_j weight[t,j] * part[t,j], four columns to a thread.
-__global__ __launch_bounds__(256) void moe_join_kernel(gt::MoeArgs a, const float* part, int64_t ld) {
+// y[t] = base[t] + sum_j weight[t,j] * part[t,j], four columns to a thread; a
+// part has `split` slices.
+__global__ __launch_bounds__(256) void moe_join_kernel(gt::MoeArgs a, const float* part, int64_t ld, int split) {
   const int64_t n = 4 * ((int64_t)blockIdx.x * 256 + threadIdx.x), t = blockIdx.y;
   if (n >= a.K) return;
   f32x4 y = {0.f, 0.f, 0.f, 0.f};
@@ -75,10 +76,26 @@ __global__ __launch_bounds__(256) void moe_join_kernel(gt::MoeArgs a, const floa
     for (int e = 0; e < 4; ++e)
       if (n + e < a.K) y[e] = load_any(a.base, t * a.ldb + n + e, a.out_dtype);
   }
-  for (int j = 0; j < a.topk; ++j) {
-    const int e = a.index[t * a.ldi + j];
-    if (e < 0 || e >= a.E) continue;
-    y += a.weight[t * a.ldw + j] * *reinterpret_cast<const f32x4*>(part + (t * a.topk + j) * ld + n);
+  // eight slots at a time, their loads under way together; a slot that adds
+  // nothing reads another's place
+  for (int j0 = 0; j0 < a.topk; j0 += 8) {
+    int of[8];
+    float w[8];
+    f32x4 v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int slot = min(j0 + j, a.topk - 1);
+      of[j] = a.index[t * a.ldi + slot];
+      w[j] = a.weight[t * a.ldw + slot];
+      v[j] = *reinterpret_cast<const f32x4*>(part + (t * a.topk + slot) * ld + n);
+    }
+    for (int s = 1; s < split; ++s)
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        v[j] += *reinterpret_cast<const f32x4*>(part + ((s * a.M + t) * a.topk + min(j0 + j, a.topk - 1)) * ld + n);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j0 + j < a.topk && of[j] >= 0 && of[j] < a.E) y += w[j] * v[j];
   }
 #pragma unroll
   for (int e = 0; e < 4; ++e)
@@ -90,10 +107,12 @@ __global__ __launch_bounds__(256) void moe_join_kernel(gt::MoeArgs a, const floa
 namespace gt {
 namespace {
 
-constexpr int64_t kMostPairs = 2048;
+constexpr int64_t kMostPairs = gtk::kMostRows;
+
+int down_split(const MoeArgs& a);
 
 struct MoeSpace {
-  int64_t act_ld, part_ld;
+  int64_t act_ld, part_ld, split;
   size_t act, part, bytes;  // offsets; the table of tiles comes first
 };
 MoeSpace space(const MoeArgs& a, int64_t tokens) {
@@ -101,9 +120,10 @@ MoeSpace space(const MoeArgs& a, int64_t tokens) {
   const int64_t pairs = tokens * a.topk;
   s.act_ld = (a.H + 3) / 4 * 4;
   s.part_ld = (a.K + 3) / 4 * 4;
-  s.act = ((size_t)pairs * sizeof(gtk::RowTile) + 255) / 256 * 256;
+  s.act = gtk::row_table_bytes(pairs);
   s.part = s.act + (size_t)pairs * s.act_ld * 4;
-  s.bytes = s.part + (size_t)pairs * s.part_ld * 4;
+  s.split = down_split(a);
+  s.bytes = s.part + (size_t)(pairs * s.split * s.part_ld * 4);
   return s;
 }
 
@@ -125,34 +145,47 @@ bool in_units(const MoeArgs& a, const ExpertWeights& w, int64_t K) {
   return w.s_ldn <= most / 32 / e && w.s_ldg <= most / 2 / e / ((K >> a.group_lg) + 1);
 }
 
-GroupedCut cut(const MoeArgs& a, int units, bool down) {
-  GroupedCut c;
-  const bool k4 = a.format >= 0;
-  const int least = k4 ? 1 : 2, most = k4 ? (down ? 1 : 2) : 4;
-  c.U = least;
-  while (c.U < most && units > 8 * c.U) c.U *= 2;
-  c.wk = std::min(8, (units + c.U - 1) / c.U);
-  c.turns = (units + c.wk * c.U - 1) / (c.wk * c.U);
-  c.cols = 8 / c.wk;
+// How a product's K is cut: into units, a wave's slice of them, and where one
+// workgroup's waves do not hold all of them, turns (the gated product) or
+// workgroups whose sums the join adds (the down product).
+struct MoeCut : gtk::GroupedCut {
+  int units, split;
+};
+MoeCut cut(const MoeArgs& a, bool down) {
+  MoeCut c;
+  const int64_t K = down ? a.H : a.K;
+  const int unit = a.format < 0 ? 128 : 256;
+  c.units = (int)((K + unit - 1) / unit);
+  if (a.format >= 0) {
+    c.U = down ? 1 : 2;
+    c.waves = 8;
+  } else {
+    c.waves = c.units > 16 ? 8 : 4;
+    c.U = c.units > 2 * c.waves ? 4 : 2;
+  }
+  const int most = c.U * c.waves;
+  c.split = down ? (c.units + most - 1) / most : 1;
+  const int each = (c.units + c.split - 1) / c.split;  // of a workgroup
+  c.wk = std::min(c.waves, (each + c.U - 1) / c.U);
+  c.turns = (each + c.wk * c.U - 1) / (c.wk * c.U);
+  c.cols = c.waves / c.wk;
   return c;
 }
 
 int product(const MoeArgs& a, gtk::GroupedParams& p, int phase, int64_t tiles) {
-  const int unit = a.format < 0 ? 128 : 256;
-  const int units = (p.K + unit - 1) / unit;
-  const GroupedCut c = cut(a, units, phase == gtk::GROUPED_DOWN);
-  fill_cut(p, c, units, 1);
-  p.pairs = phase == gtk::GROUPED_GATE_UP ? (p.N + 15) / 16 : (p.N + 31) / 32;
-  const int64_t groups = (p.pairs + c.cols - 1) / c.cols;
-  p.pairs_each = (int)std::max<int64_t>(1, std::min<int64_t>(8, groups * tiles / (3 * a.cus)));
-  const int64_t wgs = (p.pairs + c.cols * p.pairs_each - 1) / (c.cols * p.pairs_each);
-  return launcher(a)(p, dim3((unsigned)wgs, (unsigned)tiles), 64 * c.wk * c.cols, phase, 1, c.U, a.stream);
+  const int pairs = phase == gtk::GROUPED_GATE_UP ? (p.N + 15) / 16 : (p.N + 31) / 32;
+  const MoeCut c = cut(a, phase == gtk::GROUPED_DOWN);
+  fill_cut(p, c, c.units, c.split);
+  if (!fill_list(p, tiles, (pairs + c.cols - 1) / c.cols, a.cus)) return LS_UNSUPPORTED;
+  return launcher(a)(p, phase, c, a.stream);
 }
+
+int down_split(const MoeArgs& a) { return cut(a, true).split; }
 
 }  // namespace
 
 int64_t moe_range(const MoeArgs& a) {
-  const int64_t pairs = ((int64_t)64 << 20) / (4 * (a.H + a.K + 6));
+  const int64_t pairs = ((int64_t)64 << 20) / (4 * (a.H + down_split(a) * a.K + 6) + (int64_t)sizeof(gtk::RowTile));
   return std::max<int64_t>(1, std::min(pairs, kMostPairs) / a.topk);
 }
 size_t moe_workspace_bytes(const MoeArgs& a, int64_t tokens) { return space(a, tokens).bytes; }
@@ -166,12 +199,12 @@ int launch_moe(const MoeArgs& a) {
     hipLaunchKernelGGL(gtk::moe_down_kernel, dim3((unsigned)((a.K + 3) / 4), (unsigned)a.M), dim3(256), 0, a.stream, a, act);
     return hipGetLastError() == hipSuccess ? LS_OK : LS_HIP_ERROR;
   }
-  const int64_t pairs = a.M * a.topk, tiles = most_tiles(pairs, a.E, 16);
+  const int64_t pairs = a.M * a.topk, tiles = most_tiles(pairs, a.E);
   gtk::GroupedParams p{};
-  p.ix = gtk::RowIndex{a.index, a.ldi, (int)pairs, a.topk, a.E, 0};
-  p.table = reinterpret_cast<gtk::RowTile*>(a.ws);
+  p.ix = gtk::RowIndex{a.index, a.ldi, (int)pairs, a.topk, a.E, ((1u << 20) + a.topk - 1) / a.topk, 0, bits_of(a.E - 1)};
+  p.table = reinterpret_cast<gtk::RowTable*>(a.ws);
   p.scale_dtype = a.scale_dtype;
-  p.group_lg = a.group_lg;
+  p.group = 1 << a.group_lg;
   p.activation = a.activation;
   p.w = a.gate_up;
   p.x = a.x;
@@ -181,19 +214,22 @@ int launch_moe(const MoeArgs& a) {
   p.up = a.H;
   p.N = (int)a.H;
   p.K = (int)a.K;
-  int rc = product(a, p, gtk::GROUPED_GATE_UP, tiles);
+  int rc = LS_OK;
+  if (pairs > gtk::kFewRows) rc = launch_row_tiles(p.ix, p.table, a.stream);
+  if (rc == LS_OK) rc = product(a, p, gtk::GROUPED_GATE_UP, tiles);
   if (rc != LS_OK) return rc;
   p.w = a.down;
   p.x = act;
   p.ldx = s.act_ld;
   p.out = part;
   p.ld_out = s.part_ld;
+  p.out_slice = pairs * s.part_ld;
   p.N = (int)a.K;
   p.K = (int)a.H;
   rc = product(a, p, gtk::GROUPED_DOWN, tiles);
   if (rc != LS_OK) return rc;
   hipLaunchKernelGGL(gtk::moe_join_kernel, dim3((unsigned)((a.K + 1023) / 1024), (unsigned)a.M), dim3(256), 0, a.stream, a, part,
-                     s.part_ld);
+                     s.part_ld, (int)s.split);
   return hipGetLastError() == hipSuccess ? LS_OK : LS_HIP_ERROR;
 }
 

@@ -10,7 +10,7 @@ namespace gtk {
 
 struct ExpandParams {
   gt::LoraArgs a;
-  const RowTile* table;
+  const RowTable* table;
   const float* mid;  // slice s, row m, rank r at (s * M + m) * ld + r
   int64_t ld, slice;
   int slices, blocks, blocks_each;  // blocks of 64 columns; of a wave
@@ -38,10 +38,10 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(ExpandParams p) {
   const gt::LoraArgs& a = p.a;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, kq = lane >> 4;
-  if (tid < 18) reinterpret_cast<int*>(&tile)[tid] = reinterpret_cast<const int*>(p.table + blockIdx.y)[tid];
+  if ((int)blockIdx.y >= p.table->tiles) return;
+  if (tid < 2 + kTileRows) reinterpret_cast<int*>(&tile)[tid] = reinterpret_cast<const int*>(&p.table->tile[blockIdx.y])[tid];
   __syncthreads();
   const int matrix = __builtin_amdgcn_readfirstlane(tile.matrix);
-  if (matrix < 0) return;
   const int rows = __builtin_amdgcn_readfirstlane(tile.count);
   const bool some = matrix < a.adapters;
   const int block0 = (blockIdx.x * 4 + wave) * p.blocks_each, block1 = min(block0 + p.blocks_each, p.blocks);
@@ -225,19 +225,6 @@ __global__ __launch_bounds__(256) void lora_shrink_kernel(gt::LoraArgs a, float*
   }
 }
 
-// The tiles of those rows.
-__global__ __launch_bounds__(512) void lora_tiles_kernel(RowIndex ix, RowTile* table) {
-  __shared__ TileSearch<16> tile;
-  __shared__ uint32_t count[kMostMatrices + 1];
-  find_tile<16>(ix, blockIdx.x, tile, count);
-  const int tid = threadIdx.x;
-  if (tid == 0) {
-    table[blockIdx.x].matrix = tile.matrix;
-    table[blockIdx.x].count = tile.count;
-  }
-  if (tid < 16) table[blockIdx.x].rows[tid] = tile.matrix >= 0 && tid < tile.count ? tile.rows[tid] : 0;
-}
-
 __global__ __launch_bounds__(256) void copy_rows_kernel(const void* base, void* y, int64_t M, int64_t N, int64_t ldb, int64_t ldy,
                                                         int dtype) {
   for (int64_t m = blockIdx.y; m < M; m += gridDim.y)
@@ -250,19 +237,17 @@ __global__ __launch_bounds__(256) void copy_rows_kernel(const void* base, void* 
 namespace gt {
 namespace {
 
-constexpr int64_t kMostRows = 4096;
-
 bool in_units(const LoraArgs& a) { return a.K >= 8 && a.a.ld <= (INT64_C(1) << 27); }
 
 // The first product's slices: one workgroup's K where the tiles alone fill the
 // CUs, more where they do not.
 struct LoraCut {
-  GroupedCut c;
+  gtk::GroupedCut c;
   int units, split;
 };
 LoraCut cut(const LoraArgs& a, int64_t rows) {
   LoraCut l;
-  const int64_t tiles = most_tiles(rows, a.adapters, 16);
+  const int64_t tiles = most_tiles(rows, a.adapters);
   l.units = (int)((a.K + 127) / 128);
   const int pairs = (a.rank + 31) / 32;
   const int64_t want = std::max<int64_t>(1, 2 * a.cus / (tiles * pairs));
@@ -272,6 +257,7 @@ LoraCut cut(const LoraArgs& a, int64_t rows) {
   l.c.U = each > 2 ? 4 : (each > 1 ? 2 : 1);
   l.c.turns = (each + l.c.U - 1) / l.c.U;
   l.c.cols = 8 / l.c.wk;
+  l.c.waves = 8;
   return l;
 }
 struct LoraSpace {
@@ -281,7 +267,7 @@ struct LoraSpace {
 LoraSpace space(const LoraArgs& a, int64_t rows) {
   LoraSpace s;
   s.ld = (a.rank + 3) / 4 * 4;
-  s.mid = ((size_t)most_tiles(rows, a.adapters + 1, 16) * sizeof(gtk::RowTile) + 255) / 256 * 256;
+  s.mid = gtk::row_table_bytes(most_tiles(rows, a.adapters + 1));
   s.bytes = s.mid + (size_t)cut(a, rows).split * rows * s.ld * 4;
   return s;
 }
@@ -317,19 +303,24 @@ unsigned at_most(int64_t n, int64_t most) { return (unsigned)(n < most ? n : mos
 
 int64_t lora_range(const LoraArgs& a) {
   // a row has up to 16 slices where the rows are few, one where they are many
-  return std::min<int64_t>(kMostRows, ((int64_t)64 << 20) / (16 * (4 * ((a.rank + 3) / 4 * 4) + 6)));
+  return std::min<int64_t>(gtk::kMostRows, ((int64_t)64 << 20) / (16 * (4 * ((a.rank + 3) / 4 * 4) + 6)));
 }
 size_t lora_workspace_bytes(const LoraArgs& a, int64_t rows) { return space(a, rows).bytes; }
 
 int launch_lora(const LoraArgs& a) {
   const LoraSpace s = space(a, a.M);
   const int none = a.base != a.y;
-  const int64_t tiles = most_tiles(a.M, a.adapters + none, 16);
-  gtk::RowTile* table = reinterpret_cast<gtk::RowTile*>(a.ws);
+  const int64_t tiles = most_tiles(a.M, a.adapters + none);
+  gtk::RowTable* table = reinterpret_cast<gtk::RowTable*>(a.ws);
   float* mid = reinterpret_cast<float*>(a.ws + s.mid);
-  const gtk::RowIndex ix{a.index, 1, (int)a.M, 1, a.adapters, none};
+  const gtk::RowIndex ix{a.index, 1, (int)a.M, 1, a.adapters, 1u << 20, none, bits_of(a.adapters - 1 + none)};
   int split = 1;
-  if (in_units(a)) {
+  const bool units = in_units(a);
+  if (!units || a.M > gtk::kFewRows) {
+    const int rc = launch_row_tiles(ix, table, a.stream);
+    if (rc != LS_OK) return rc;
+  }
+  if (units) {
     const LoraCut l = cut(a, a.M);
     split = l.split;
     gtk::GroupedParams p{};
@@ -344,13 +335,12 @@ int launch_lora(const LoraArgs& a) {
     p.N = a.rank;
     p.K = (int)a.K;
     fill_cut(p, l.c, l.units, l.split);
-    p.pairs = (p.N + 31) / 32;
-    p.pairs_each = 1;
+    const int groups = ((p.N + 31) / 32 + l.c.cols - 1) / l.c.cols;
+    if (!fill_list(p, tiles, groups, tiles * l.split * groups)) return LS_UNSUPPORTED;
     const int rc = (a.x_dtype == DT_BF16 ? grouped_bf16 : grouped_f16)(
-        p, dim3((p.pairs + l.c.cols - 1) / l.c.cols, (unsigned)tiles, l.split), 64 * l.c.wk * l.c.cols, gtk::GROUPED_SHRINK, 1, l.c.U, a.stream);
+        p, gtk::GROUPED_SHRINK, l.c, a.stream);
     if (rc != LS_OK) return rc;
   } else {
-    hipLaunchKernelGGL(gtk::lora_tiles_kernel, dim3((unsigned)tiles), dim3(512), 0, a.stream, ix, table);
     hipLaunchKernelGGL(gtk::lora_shrink_kernel, dim3(at_most(a.M, 65536), (a.rank + 3) / 4), dim3(256), 0, a.stream, a, mid, s.ld);
   }
   gtk::ExpandParams e{a, table, mid, s.ld, a.M * s.ld, split, (int)((a.N + 63) / 64), 1};
