@@ -130,12 +130,13 @@ gt_status moe_shape(const gt_moe_desc* d, MoeArgs* a) {
   a->activation = d->activation;
   if (d->E > kMostExperts) return refuse(GT_ERR_UNSUPPORTED, "gt_moe takes at most 4096 experts");
   if (d->topk > kMostSlots) return refuse(GT_ERR_UNSUPPORTED, "gt_moe takes at most 64 experts a token");
-  if (d->H > (INT64_C(1) << 30) || d->K > (INT64_C(1) << 30)) return refuse(GT_ERR_UNSUPPORTED, "gt_moe takes K and H up to 2^30");
+  if (d->H > (INT64_C(1) << 24) || d->K > (INT64_C(1) << 24)) return refuse(GT_ERR_UNSUPPORTED, "gt_moe takes K and H up to 2^24");
   a->M = d->M;
   a->K = d->K;
   a->H = d->H;
   a->E = (int)d->E;
   a->topk = (int)d->topk;
+  a->wide = false;
   return GT_OK;
 }
 bool moe_empty(const MoeArgs& a) { return a.H == 0 || a.E == 0 || a.topk == 0; }
@@ -182,6 +183,7 @@ gt_status moe(const gt_moe_desc* d) {
     if (dev->fake) return GT_OK;
     return launched(launch_copy_rows(a.base, a.y, a.M, a.K, a.ldb, a.ldy, a.out_dtype, a.stream), "gt_moe");
   }
+  a.wide = moe_wide(a);
   const int64_t most = moe_range(a);
   return on_workspace(*dev, a, most_bytes(a, most, moe_workspace_bytes), d->workspace, d->workspace_bytes, [&](MoeArgs& all) {
     for (int64_t m = 0; m < all.M; m += most) {
@@ -207,6 +209,7 @@ gt_status moe_workspace(const gt_moe_desc* d, int64_t* bytes) {
   DeviceState* dev = nullptr;
   GT_CHECK(current_device(&dev));
   a.cus = dev->cus;
+  a.wide = moe_wide(a);
   *bytes = (int64_t)most_bytes(a, moe_range(a), moe_workspace_bytes);
   return GT_OK;
 }
@@ -219,7 +222,7 @@ gt_status lora_shape(const gt_lora_desc* d, LoraArgs* a) {
   GT_CHECK(float_type(d->out_dtype, a->x_dtype, "y", &a->out_dtype));
   if (d->adapters > kMostExperts) return refuse(GT_ERR_UNSUPPORTED, "gt_lora takes at most 4096 adapters");
   if (d->rank > kMostRank) return refuse(GT_ERR_UNSUPPORTED, "gt_lora takes ranks up to 256");
-  if (d->K > (INT64_C(1) << 30) || d->N > (INT64_C(1) << 30)) return refuse(GT_ERR_UNSUPPORTED, "gt_lora takes K and N up to 2^30");
+  if (d->K > (INT64_C(1) << 24) || d->N > (INT64_C(1) << 24)) return refuse(GT_ERR_UNSUPPORTED, "gt_lora takes K and N up to 2^24");
   a->M = d->M;
   a->K = d->K;
   a->N = d->N;

@@ -134,6 +134,7 @@ struct MoeArgs {
   int64_t M, K, H, ldx, ldi, ldw, ldb, ldy;
   int E, topk;
   int x_dtype, out_dtype, format, scale_dtype, group_lg, activation;
+  bool wide;  // tiles of 64 rows, not 16: moe_wide
   char* ws;
   int cus;
   hipStream_t stream;

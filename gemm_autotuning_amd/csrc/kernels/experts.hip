@@ -2,7 +2,7 @@
 // into fp32 activations per (token, slot) pair, the down product of each pair
 // (grouped.h), and the pairs' weighted sum.
 #include "elements.h"
-#include "grouped.h"
+#include "grouped_wide.h"
 #include "launchers.h"
 
 namespace gtk {
@@ -115,8 +115,9 @@ struct MoeSpace {
   int64_t act_ld, part_ld, split;
   size_t act, part, bytes;  // offsets; the table of tiles comes first
 };
-MoeSpace space(const MoeArgs& a, int64_t tokens) {
+MoeSpace space(MoeArgs a, int64_t tokens) {
   MoeSpace s;
+  a.M = tokens;
   const int64_t pairs = tokens * a.topk;
   s.act_ld = (a.H + 3) / 4 * 4;
   s.part_ld = (a.K + 3) / 4 * 4;
@@ -154,6 +155,15 @@ struct MoeCut : gtk::GroupedCut {
 MoeCut cut(const MoeArgs& a, bool down) {
   MoeCut c;
   const int64_t K = down ? a.H : a.K;
+  if (a.wide) {
+    c.units = (int)((K + 127) / 128);
+    // along K as many workgroups as find a CU where each expert has a tile, of four units at least
+    const int64_t items = std::max<int64_t>(a.E, a.M * a.topk / 64) * ((a.K + 255) / 256);
+    c.split = down ? (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(a.cus / items, c.units / 4), 8)) : 1;
+    c.wk = c.turns = 1;
+    c.cols = 8;
+    return c;
+  }
   const int unit = a.format < 0 ? 128 : 256;
   c.units = (int)((K + unit - 1) / unit);
   if (a.format >= 0) {
@@ -177,7 +187,7 @@ int product(const MoeArgs& a, gtk::GroupedParams& p, int phase, int64_t tiles) {
   const MoeCut c = cut(a, phase == gtk::GROUPED_DOWN);
   fill_cut(p, c, c.units, c.split);
   if (!fill_list(p, tiles, (pairs + c.cols - 1) / c.cols, a.cus)) return LS_UNSUPPORTED;
-  return launcher(a)(p, phase, c, a.stream);
+  return a.wide ? (a.x_dtype == DT_BF16 ? grouped_wide_bf16 : grouped_wide_f16)(p, phase, a.stream) : launcher(a)(p, phase, c, a.stream);
 }
 
 int down_split(const MoeArgs& a) { return cut(a, true).split; }
@@ -185,8 +195,21 @@ int down_split(const MoeArgs& a) { return cut(a, true).split; }
 }  // namespace
 
 int64_t moe_range(const MoeArgs& a) {
-  const int64_t pairs = ((int64_t)64 << 20) / (4 * (a.H + down_split(a) * a.K + 6) + (int64_t)sizeof(gtk::RowTile));
+  // (a wide call's slices of K are not counted: there are some only where all
+  // their sums together stay below 256 columns of 64 rows to a CU, 16 MiB)
+  const int64_t slices = a.wide ? 1 : down_split(a);
+  const int64_t pairs = ((int64_t)64 << 20) / (4 * (a.H + slices * a.K + 6) + (int64_t)sizeof(gtk::RowTile));
   return std::max<int64_t>(1, std::min(pairs, kMostPairs) / a.topk);
+}
+// Whether an expert has at least 16 rows on average: 8 experts 4096 x 2048
+// bf16 take 97 us with tiles of 64 rows and 120 with tiles of 16 there (128 tokens: 115 and 166,
+// 512: 274 and 582), 97 and 92 with 12 rows.  Expanding 4-bit weights less
+// often gains nothing (134 us both ways with 64 rows to an expert), so they
+// have tiles of 16 only.
+bool moe_wide(const MoeArgs& a) {
+  MoeArgs wide = a;
+  wide.wide = true;
+  return a.format < 0 && std::min(a.M, moe_range(wide)) * a.topk >= 16 * (int64_t)a.E;
 }
 size_t moe_workspace_bytes(const MoeArgs& a, int64_t tokens) { return space(a, tokens).bytes; }
 
@@ -199,9 +222,9 @@ int launch_moe(const MoeArgs& a) {
     hipLaunchKernelGGL(gtk::moe_down_kernel, dim3((unsigned)((a.K + 3) / 4), (unsigned)a.M), dim3(256), 0, a.stream, a, act);
     return hipGetLastError() == hipSuccess ? LS_OK : LS_HIP_ERROR;
   }
-  const int64_t pairs = a.M * a.topk, tiles = most_tiles(pairs, a.E);
+  const int64_t pairs = a.M * a.topk, tiles = most_tiles(pairs, a.E, a.wide ? 64 : 16);
   gtk::GroupedParams p{};
-  p.ix = gtk::RowIndex{a.index, a.ldi, (int)pairs, a.topk, a.E, ((1u << 20) + a.topk - 1) / a.topk, 0, bits_of(a.E - 1)};
+  p.ix = gtk::RowIndex{a.index, a.ldi, (int)pairs, a.topk, a.E, ((1u << 20) + a.topk - 1) / a.topk, 0, bits_of(a.E - 1), a.wide ? 6 : 4};
   p.table = reinterpret_cast<gtk::RowTable*>(a.ws);
   p.scale_dtype = a.scale_dtype;
   p.group = 1 << a.group_lg;

@@ -34,14 +34,14 @@ namespace gtk {
 constexpr int kMostRows = 4096;      // of one launch
 constexpr int kMostMatrices = 4096;  // counted in LDS
 constexpr int kFewRows = 128;        // whose tiles every workgroup finds by itself
-constexpr int kTileRows = 16;
+constexpr int kMostTileRows = 64;
 enum { GROUPED_16 = -1 };            // weights of the rows' type; else W4_INT4, W4_E2M1
 enum { GROUPED_GATE_UP = 0, GROUPED_DOWN = 1, GROUPED_SHRINK = 2 };
 
 // A tile of rows: the matrix, how many rows, which.
 struct RowTile {
   int matrix, count;
-  int rows[kTileRows];
+  int rows[kMostTileRows];
 };
 // All of them, made by the first launch of a call for the others.
 struct RowTable {
@@ -59,6 +59,7 @@ struct RowIndex {
   uint32_t per_inverse;  // 2^20 / per, rounded up: exact for up to 4096 rows
   int none;  // whether rows without a matrix form tiles too (of matrix `matrices`)
   int bits;  // of the largest matrix's number
+  int tile_lg;  // a tile has up to 2^tile_lg rows
 };
 
 // Division by a number that the host knows: with floor(2^32 / n) the quotient
@@ -91,13 +92,13 @@ struct GroupedParams {
   int wk_inverse;      // 2^16 / wk, rounded up: exact for what is divided (at most 16)
 };
 
-// The tiles of rows: rows that name the same matrix, 16 to a tile.  Up to 128
+// The tiles of rows: rows that name the same matrix, 16 or 64 to a tile.  Up to 128
 // rows every workgroup finds by itself: one wave compares all of them at once,
 // bit by bit of what they name, and the tiles have the order of their first
 // rows.  For more a launch of one workgroup makes the table first (row_tiles.hip).
 struct TileSearch {
   int tiles, matrix, count;
-  int rows[kTileRows];
+  int rows[kMostTileRows];
 };
 __device__ __forceinline__ int row_of(const RowIndex& ix, int i) { return (int)((uint32_t)i * ix.per_inverse >> 20); }
 __device__ __forceinline__ int row_matrix(const RowIndex& ix, int i) {
@@ -115,6 +116,7 @@ __device__ __forceinline__ FewRows few_rows(const RowIndex& ix) {
   int lane = threadIdx.x & 63;
   asm volatile("" : "+v"(lane));  // computed where it is asked for and not kept
   const uint64_t before = (1ull << lane) - 1;
+  const int in_tile = (1 << ix.tile_lg) - 1;
   FewRows f;
   f.e[0] = lane < ix.n ? row_matrix(ix, lane) : -1;
   f.e[1] = -1;
@@ -141,14 +143,14 @@ __device__ __forceinline__ FewRows few_rows(const RowIndex& ix) {
     }
     f.rank[0] = __popcll(same[0] & before);
     f.rank[1] = __popcll(same[1]) + __popcll(same[2] & before);
-    f.leaders[1] = __ballot(f.e[1] >= 0 && f.rank[1] % kTileRows == 0);
+    f.leaders[1] = __ballot(f.e[1] >= 0 && (f.rank[1] & in_tile) == 0);
   }
-  f.leaders[0] = __ballot(f.e[0] >= 0 && f.rank[0] % kTileRows == 0);
+  f.leaders[0] = __ballot(f.e[0] >= 0 && (f.rank[0] & in_tile) == 0);
   return f;
 }
 __device__ __forceinline__ int few_tiles(const FewRows& f) { return __popcll(f.leaders[0]) + __popcll(f.leaders[1]); }
 // Tile t of them into LDS, by one wave.
-__device__ __forceinline__ void few_tile(const FewRows& f, int t, TileSearch& s) {
+__device__ __forceinline__ void few_tile(const RowIndex& ix, const FewRows& f, int t, TileSearch& s) {
   const int lane = threadIdx.x & 63;
   const uint64_t before = (1ull << lane) - 1;
   const int n0 = __popcll(f.leaders[0]), j = t < n0 ? 0 : 1;
@@ -159,7 +161,7 @@ __device__ __forceinline__ void few_tile(const FewRows& f, int t, TileSearch& s)
   int n = 0;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const bool in = f.e[i] == matrix && f.rank[i] >= first && f.rank[i] < first + kTileRows;
+    const bool in = f.e[i] == matrix && f.rank[i] >= first && f.rank[i] < first + (1 << ix.tile_lg);
     if (in) s.rows[f.rank[i] - first] = 64 * i + lane;
     n += __popcll(__ballot(in));
   }
@@ -204,8 +206,79 @@ struct UnitOf {
   static constexpr int kPitch = kBytes + 16;          // of a column in LDS: reads of 16 columns fall on different banks
 };
 
-// What a wave lays out through LDS: weights of a unit (and its scales per 32
-// k), before that 16 rows' 128 elements.
+// A workgroup's part of the list: tile by tile, slice of K by slice, groups of
+// columns from g0 on, `left` of them.
+struct Part {
+  int left, t, slice, g0;
+};
+__device__ __forceinline__ Part part_of(const GroupedParams& p, int tiles) {
+  Part o;
+  uint32_t in;
+  const uint32_t to_each = p.workgroups.n / (uint32_t)max(tiles, 1);
+  if (to_each >= 4) {  // no workgroup has the ends of two tiles, though up to a fifth of them have nothing
+    o.t = blockIdx.x / to_each;
+    const uint32_t at = blockIdx.x - o.t * to_each, each = p.of_tile.n / to_each, rest = p.of_tile.n - each * to_each;
+    in = at * each + min(at, rest);
+    o.left = o.t < tiles ? each + (at < rest) : 0;
+  } else {
+    const uint32_t all = (uint32_t)tiles * p.of_tile.n;
+    const uint32_t each = quotient(p.workgroups, all), rest = all - each * p.workgroups.n;
+    const uint32_t begin = blockIdx.x * each + min(blockIdx.x, rest);
+    o.left = each + (blockIdx.x < rest);
+    o.t = quotient(p.of_tile, begin);
+    in = begin - o.t * p.of_tile.n;
+  }
+  o.slice = p.split > 1 ? quotient(p.groups, in) : 0;
+  o.g0 = in - o.slice * p.groups.n;
+  return o;
+}
+// The part, and where the workgroups search by themselves its first tile.
+__device__ __forceinline__ Part first_part(const GroupedParams& p, bool search, int wave, TileSearch& tile) {
+  if (search) {
+    if (wave == 0) {
+      const FewRows f = few_rows(p.ix);
+      const int tiles = few_tiles(f);
+      const Part o = part_of(p, tiles);
+      if (o.left > 0) few_tile(p.ix, f, o.t, tile);
+      if (threadIdx.x == 0) tile.tiles = tiles;
+    }
+    __syncthreads();
+    if (blockIdx.x == 0 && threadIdx.x == 0) p.table->tiles = tile.tiles;
+  }
+  return part_of(p, __builtin_amdgcn_readfirstlane(search ? tile.tiles : p.table->tiles));
+}
+// The part's next groups of one tile and slice, and the tile.  found: first_part has found it.
+struct Stretch {
+  int slice, g0, g1;
+};
+__device__ __forceinline__ Stretch next_stretch(const GroupedParams& p, bool search, bool found, int wave, Part& part, TileSearch& tile) {
+  const int tid = threadIdx.x, t = part.t;
+  const Stretch s = {part.slice, part.g0, min((int)p.groups.n, part.g0 + part.left)};
+  part.left -= s.g1 - s.g0;
+  part.g0 = 0;
+  part.slice = s.slice + 1 == p.split ? 0 : s.slice + 1;
+  part.t = t + (part.slice == 0);
+  if (!found) __syncthreads();  // the last tile's rows are no longer read
+  if (search) {
+    if (!found) {
+      if (wave == 0) few_tile(p.ix, few_rows(p.ix), t, tile);
+      __syncthreads();
+    }
+    if (s.g0 == 0 && s.slice == 0 && tid < 1 << p.ix.tile_lg) {
+      RowTile& e = p.table->tile[t];
+      if (tid == 0) e.matrix = tile.matrix;
+      if (tid == 0) e.count = tile.count;
+      e.rows[tid] = tid < tile.count ? tile.rows[tid] : 0;
+    }
+  } else {
+    if (tid < 2 + (1 << p.ix.tile_lg)) (&tile.matrix)[tid] = reinterpret_cast<const int*>(&p.table->tile[t])[tid];
+    __syncthreads();
+  }
+  return s;
+}
+
+// What a wave lays out through LDS: weights of a unit (and its scales, a
+// column's groups), before that 16 rows' 128 elements.
 struct alignas(16) GroupedStage {
   char q[16 * 272];
 };
@@ -216,15 +289,115 @@ struct ScaleStage {
 template <>
 struct ScaleStage<GROUPED_16> {};
 
+// A wave's weights: for group g of columns its pair of tiles of 16, each half
+// in units along K, from memory into registers and from there into LDS.
+template <int PHASE, int FMT, int BYTES, int G, int WIDE>
+struct PairWeights {
+  typedef UnitOf<FMT, BYTES> Unit;
+  typedef typename std::conditional<WIDE, uint32_t, uint16_t>::type Scale;
+  static constexpr int kGroups = Unit::k4 ? Unit::kK / G : 1;  // of a unit
+  static constexpr int kScales = kGroups > 4 ? kGroups / 4 : 1;  // of a lane: every fourth
+  const GroupedParams& p;
+  const int cols, g1, lane, piece, sub;
+  const uint32_t row_bytes, ld, s_ldn, s_ldg, lane_q, lane_s, bf16_scales;
+  const int scale_groups;
+  const char *const wm, *const sm;
+  char* const st;
+  float (*const ss)[12];
+  const int64_t half_columns, pair_columns;
+  int c0, nc;  // the slice: its first unit, and how many
+  // the next pair to load from: its group, first column's weights and scales
+  int load_g;
+  const char *load_q, *load_s;
+
+  __device__ __forceinline__ PairWeights(const GroupedParams& p, int matrix, int cols, int g1, int lane, char* st, float (*ss)[12])
+      : p(p), cols(cols), g1(g1), lane(lane), piece(lane % Unit::kLanes), sub(lane / Unit::kLanes),
+        row_bytes(Unit::k4 ? (p.K + 1) / 2 : 2 * p.K), ld((uint32_t)p.w.ld), s_ldn((uint32_t)p.w.s_ldn * sizeof(Scale)),
+        s_ldg((uint32_t)p.w.s_ldg * sizeof(Scale)), lane_q(sub * ld + 16 * piece), lane_s((lane >> 2) * s_ldn + (lane & 3) * s_ldg),
+        bf16_scales(p.scale_dtype == DT_BF16 ? ~0u : 0u), scale_groups((p.K + G - 1) / G), wm(p.w.p + matrix * p.w.stride),
+        sm(Unit::k4 ? static_cast<const char*>(p.w.scales) + matrix * p.w.s_lde * sizeof(Scale) : nullptr), st(st), ss(ss),
+        half_columns(PHASE == GROUPED_GATE_UP ? p.up : 16), pair_columns(p.cols * (PHASE == GROUPED_GATE_UP ? 16 : 32)) {}
+  __device__ __forceinline__ void slice(int s) {
+    c0 = s * p.units_each + min(s, p.units_rest);
+    nc = p.units_each + (s < p.units_rest);
+  }
+  __device__ __forceinline__ int column_of(int g, int half) const {
+    const int pair = g * p.cols + cols;
+    return PHASE == GROUPED_GATE_UP ? pair * 16 : (2 * pair + half) * 16;
+  }
+  // a half's columns less one, below 0 where there is none
+  __device__ __forceinline__ int last_of(int g, int half) const {
+    return g < g1 && cols < p.cols ? min(p.N - 1 - column_of(g, half), 15) : -1;  // a wave may be left over
+  }
+  __device__ __forceinline__ void load_from(int g) {
+    load_g = g;
+    load_q = wm + column_of(g, 0) * p.w.ld;
+    load_s = Unit::k4 ? sm + column_of(g, 0) * p.w.s_ldn * (int64_t)sizeof(Scale) : nullptr;
+  }
+  __device__ __forceinline__ void load_next_pair() {
+    ++load_g;
+    load_q += pair_columns * p.w.ld;
+    if (Unit::k4) load_s += pair_columns * p.w.s_ldn * (int64_t)sizeof(Scale);
+  }
+  // Unit `un` of a half, or for all lanes one address.  An offset past the
+  // half's last piece is cut to that; between a row's end and it there are
+  // other rows, whose bytes stage() takes out.
+  __device__ __forceinline__ void load(bool any, int half, int un, u32x4 (&q)[Unit::kLoads], Scale (&sc)[kScales]) const {
+    const int last = last_of(load_g, half);
+    any = any && un < nc && last >= 0;
+    const char* const base = any ? load_q + half * half_columns * p.w.ld : wm;
+    const uint32_t some = any ? ~0u : 0u, most = (last * ld + row_bytes - 16) & some, from = (uint32_t)(c0 + un) * Unit::kBytes;
+#pragma unroll
+    for (int i = 0; i < Unit::kLoads; ++i)
+      q[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(base + min(lane_q + (i * Unit::kCols * ld + from), most)));
+    if constexpr (Unit::k4) {
+      const char* const scales = any ? load_s + half * half_columns * p.w.s_ldn * (int64_t)sizeof(Scale) : sm;
+      const uint32_t s_most = (last * s_ldn + (scale_groups - 1) * s_ldg) & some;
+#pragma unroll
+      for (int i = 0; i < kScales; ++i)
+        sc[i] = *reinterpret_cast<const Scale*>(scales + min(lane_s + ((c0 + un) * kGroups + 4 * i) * s_ldg, s_most));
+    }
+  }
+  __device__ __forceinline__ void stage(int half_last, int un, u32x4 (&q)[Unit::kLoads], const Scale (&sc)[kScales]) const {
+    const uint32_t from = (uint32_t)(c0 + un) * Unit::kBytes;
+    if (from + Unit::kBytes > row_bytes) {  // the row ends in it
+      const uint32_t most = half_last * ld + row_bytes - 16;
+      const int here = (int)(row_bytes - from) - 16 * piece;  // bytes of the lane's 16 that are the row's
+#pragma unroll
+      for (int i = 0; i < Unit::kLoads; ++i) {
+        const uint32_t want = lane_q + (i * Unit::kCols * ld + from);
+        q[i] = bytes_upto(bytes_from(q[i], want > most ? (int)min(want - most, 16u) : 0), here);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < Unit::kLoads; ++i)
+      *reinterpret_cast<u32x4*>(st + (i * Unit::kCols + sub) * Unit::kPitch + 16 * piece) = q[i];
+    if constexpr (Unit::k4) {
+#pragma unroll
+      for (int i = 0; i < kScales; ++i) {
+        Scale b = sc[i];
+        asm volatile("" : "+v"(b));  // converted here and not where it was loaded, which would wait for it there
+        float f;
+        if constexpr (WIDE)
+          f = __uint_as_float(b);
+        else  // both conversions and a selection by bits
+          f = __uint_as_float(((uint32_t)b << 16 & bf16_scales) | (__float_as_uint(f16_bits_to_f32(b)) & ~bf16_scales));
+        const int g = (c0 + un) * kGroups + 4 * i + (lane & 3);
+        ss[lane >> 2][4 * i + (lane & 3)] = g < scale_groups ? f : 0.f;  // past K: nothing, whatever the last scale is
+      }
+    }
+    wave_lds_order();
+  }
+};
+
 // BYTES: a unit's of a column; G: a group's k and WIDE: its scale is fp32 (4
 // bits); ONE: the slices are loaded once a tile (K in one turn); W: waves.
 template <int PHASE, int XT, int FMT, int BYTES, int G, int WIDE, int U, int D, int B, int W, bool ONE>
 __global__ __launch_bounds__(64 * W, W > 8 ? 4 : 2) void grouped_kernel(GroupedParams p) {
   typedef UnitOf<FMT, BYTES> Unit;
+  typedef PairWeights<PHASE, FMT, BYTES, G, WIDE> Weights;
   typedef W4Operand<XT, FMT == GROUPED_16 ? W4_E2M1 : FMT> Op;  // e2m1: elements in order
-  typedef typename std::conditional<WIDE, uint32_t, uint16_t>::type Scale;
-  constexpr int kGroups = Unit::k4 ? Unit::kK / G : 1;  // of a unit
-  constexpr int kScales = kGroups > 4 ? kGroups / 4 : 1;  // of a lane: every fourth
+  constexpr int kGroups = Weights::kGroups;
   // with a group to 128 k a lane takes its 32 of them as they lie, eight to a step; else a step's 32 k are of one group
   constexpr bool kPieces = Unit::k4 && G == 128;
   constexpr bool kSplit = PHASE == GROUPED_DOWN;  // fp32 rows, in two parts
@@ -235,168 +408,31 @@ __global__ __launch_bounds__(64 * W, W > 8 ? 4 : 2) void grouped_kernel(GroupedP
   static_assert((B * kAll) % D == 0 && (ONE || D <= B * kAll), "places in the ring are known when compiled");
   __shared__ TileSearch tile;
   __shared__ GroupedStage stages[W];
-  __shared__ ScaleStage<FMT> scale_stage[Unit::k4 ? W : 1];
+  __shared__ ScaleStage<Unit::k4 ? FMT : W4_INT4> scale_stage[Unit::k4 ? W : 1];
   // the waves' sums of B pairs; with one pair at a time two buffers take turns, and one barrier is enough
   constexpr int kBuffers = B == 1 ? 2 : B;
   __shared__ float red[kBuffers][W][2][256];
-  __shared__ float unscale[kScaled ? W : 1][kTileRows];
+  __shared__ float unscale[kScaled ? W : 1][16];
 
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  // this workgroup's part of the list: tile by tile, slice by slice, its groups of columns
   const bool search = PHASE != GROUPED_DOWN && p.ix.n <= kFewRows;  // else there is a table
-  struct Part {
-    int left, t, slice, g0;
-  };
-  auto part_of = [&](int tiles) {
-    Part o;
-    uint32_t in;
-    const uint32_t to_each = (uint32_t)p.workgroups.n / (uint32_t)max(tiles, 1);
-    if (to_each >= 4) {  // no workgroup has the ends of two tiles, though up to a fifth of them have nothing
-      o.t = blockIdx.x / to_each;
-      const uint32_t at = blockIdx.x - o.t * to_each, each = p.of_tile.n / to_each, rest = p.of_tile.n - each * to_each;
-      in = at * each + min(at, rest);
-      o.left = o.t < tiles ? each + (at < rest) : 0;
-    } else {
-      const uint32_t all = (uint32_t)tiles * p.of_tile.n;
-      const uint32_t each = quotient(p.workgroups, all), rest = all - each * p.workgroups.n;
-      const uint32_t begin = blockIdx.x * each + min(blockIdx.x, rest);
-      o.left = each + (blockIdx.x < rest);
-      o.t = quotient(p.of_tile, begin);
-      in = begin - o.t * p.of_tile.n;
-    }
-    o.slice = PHASE != GROUPED_GATE_UP ? quotient(p.groups, in) : 0;
-    o.g0 = in - o.slice * p.groups.n;
-    return o;
-  };
-  if (search) {
-    if (wave == 0) {
-      const FewRows f = few_rows(p.ix);
-      const int tiles = few_tiles(f);
-      const Part o = part_of(tiles);
-      if (o.left > 0) few_tile(f, o.t, tile);
-      if (tid == 0) tile.tiles = tiles;
-    }
-    __syncthreads();
-    if (blockIdx.x == 0 && tid == 0) p.table->tiles = tile.tiles;
-  }
-  Part part = part_of(__builtin_amdgcn_readfirstlane(search ? tile.tiles : p.table->tiles));
-
+  Part part = first_part(p, search, wave, tile);
   // this wave's slice of K and its columns
   const int cols = (wave * p.wk_inverse) >> 16, along = wave - cols * p.wk;
-  const uint32_t row_bytes = Unit::k4 ? (p.K + 1) / 2 : 2 * p.K;
-  const uint32_t ld = (uint32_t)p.w.ld;
-  const uint32_t s_ldn = (uint32_t)p.w.s_ldn * sizeof(Scale), s_ldg = (uint32_t)p.w.s_ldg * sizeof(Scale);
-  const int scale_groups = (p.K + G - 1) / G;
-  const uint32_t bf16_scales = p.scale_dtype == DT_BF16 ? ~0u : 0u;
   char* const st = stages[wave].q;
   int buf = 0;
 
   for (bool found = search; part.left > 0; found = false) {
-    const int slice_of = part.slice, g0 = part.g0, g1 = min((int)p.groups.n, g0 + part.left), t = part.t;
-    part.left -= g1 - g0;
-    part.g0 = 0;
-    part.slice = slice_of + 1 == p.split ? 0 : slice_of + 1;
-    part.t = t + (part.slice == 0);
-    if (!found) __syncthreads();  // the last tile's rows are no longer read
-    if (search) {
-      if (!found) {
-        if (wave == 0) few_tile(few_rows(p.ix), t, tile);
-        __syncthreads();
-      }
-      if (g0 == 0 && slice_of == 0 && tid < kTileRows) {
-        RowTile& e = p.table->tile[t];
-        if (tid == 0) e.matrix = tile.matrix;
-        if (tid == 0) e.count = tile.count;
-        e.rows[tid] = tid < tile.count ? tile.rows[tid] : 0;
-      }
-    } else {
-      if (tid < 2 + kTileRows) (&tile.matrix)[tid] = reinterpret_cast<const int*>(&p.table->tile[t])[tid];
-      __syncthreads();
-    }
+    const Stretch stretch = next_stretch(p, search, found, wave, part, tile);
+    const int g0 = stretch.g0, g1 = stretch.g1;
     const int matrix = __builtin_amdgcn_readfirstlane(tile.matrix);
     if (matrix >= p.ix.matrices) continue;
     const int rows = __builtin_amdgcn_readfirstlane(tile.count);
     int lane = tid & 63;
     asm volatile("" : "+v"(lane));  // what follows from it is not kept over the search above
     const int r = lane & 15, kq = lane >> 4;
-    const int piece = lane % Unit::kLanes, sub = lane / Unit::kLanes;
-    const char* const wm = p.w.p + matrix * p.w.stride;
-    const char* const sm = Unit::k4 ? static_cast<const char*>(p.w.scales) + matrix * p.w.s_lde * sizeof(Scale) : nullptr;
-    int c0, nc;
-    auto slice = [&](int turn) {
-      const int s = (slice_of * p.turns + turn) * p.wk + along;
-      c0 = s * p.units_each + min(s, p.units_rest);
-      nc = p.units_each + (s < p.units_rest);
-    };
-
-    // ---- weights.  Group g has one pair of tiles for each wave along the
-    // columns; a half's columns less one, below 0 where there is none
-    auto column_of = [&](int g, int half) {
-      const int pair = g * p.cols + cols;
-      return PHASE == GROUPED_GATE_UP ? pair * 16 : (2 * pair + half) * 16;
-    };
-    auto last_of = [&](int g, int half) {
-      return g < g1 && cols < p.cols ? min(p.N - 1 - column_of(g, half), 15) : -1;  // a wave may be left over
-    };
-    // the next pair to load from: its group, first column's weights and scales
-    int load_g;
-    const char *load_q, *load_s;
-    const int64_t half_columns = PHASE == GROUPED_GATE_UP ? p.up : 16, pair_columns = p.cols * (PHASE == GROUPED_GATE_UP ? 16 : 32);
-    auto load_from = [&](int g) {
-      load_g = g;
-      load_q = wm + column_of(g, 0) * p.w.ld;
-      load_s = Unit::k4 ? sm + column_of(g, 0) * p.w.s_ldn * (int64_t)sizeof(Scale) : nullptr;
-    };
-    // Unit `un` of a half, or for all lanes one address.  An offset past the
-    // half's last piece is cut to that; between a row's end and it there are
-    // other rows, whose bytes stage_unit takes out.
-    const uint32_t lane_q = sub * ld + 16 * piece, lane_s = (lane >> 2) * s_ldn + (lane & 3) * s_ldg;
-    auto load_unit = [&](bool any, int half, int un, u32x4 (&q)[Unit::kLoads], Scale (&sc)[kScales]) __attribute__((always_inline)) {
-      const int last = last_of(load_g, half);
-      any = any && un < nc && last >= 0;
-      const char* const base = any ? load_q + half * half_columns * p.w.ld : wm;
-      const uint32_t some = any ? ~0u : 0u, most = (last * ld + row_bytes - 16) & some, from = (uint32_t)(c0 + un) * Unit::kBytes;
-#pragma unroll
-      for (int i = 0; i < Unit::kLoads; ++i)
-        q[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(base + min(lane_q + (i * Unit::kCols * ld + from), most)));
-      if constexpr (Unit::k4) {
-        const char* const scales = any ? load_s + half * half_columns * p.w.s_ldn * (int64_t)sizeof(Scale) : sm;
-        const uint32_t s_most = (last * s_ldn + (scale_groups - 1) * s_ldg) & some;
-#pragma unroll
-        for (int i = 0; i < kScales; ++i)
-          sc[i] = *reinterpret_cast<const Scale*>(scales + min(lane_s + ((c0 + un) * kGroups + 4 * i) * s_ldg, s_most));
-      }
-    };
-    auto stage_unit = [&](int half_last, int un, u32x4 (&q)[Unit::kLoads], const Scale (&sc)[kScales]) __attribute__((always_inline)) {
-      const uint32_t from = (uint32_t)(c0 + un) * Unit::kBytes;
-      if (from + Unit::kBytes > row_bytes) {  // the row ends in it
-        const uint32_t most = half_last * ld + row_bytes - 16;
-        const int here = (int)(row_bytes - from) - 16 * piece;  // bytes of the lane's 16 that are the row's
-#pragma unroll
-        for (int i = 0; i < Unit::kLoads; ++i) {
-          const uint32_t want = lane_q + (i * Unit::kCols * ld + from);
-          q[i] = bytes_upto(bytes_from(q[i], want > most ? (int)min(want - most, 16u) : 0), here);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < Unit::kLoads; ++i)
-        *reinterpret_cast<u32x4*>(st + (i * Unit::kCols + sub) * Unit::kPitch + 16 * piece) = q[i];
-      if constexpr (Unit::k4) {
-#pragma unroll
-        for (int i = 0; i < kScales; ++i) {
-          Scale b = sc[i];
-          asm volatile("" : "+v"(b));  // converted here and not where it was loaded, which would wait for it there
-          float f;
-          if constexpr (WIDE)
-            f = __uint_as_float(b);
-          else  // both conversions and a selection by bits
-            f = __uint_as_float(((uint32_t)b << 16 & bf16_scales) | (__float_as_uint(f16_bits_to_f32(b)) & ~bf16_scales));
-          const int g = (c0 + un) * kGroups + 4 * i + (lane & 3);
-          scale_stage[wave].s[lane >> 2][4 * i + (lane & 3)] = g < scale_groups ? f : 0.f;  // past K: nothing, whatever the last scale is
-        }
-      }
-      wave_lds_order();
-    };
+    Weights w(p, matrix, cols, g1, lane, st, scale_stage[Unit::k4 ? wave : 0].s);
+    auto slice = [&](int turn) { w.slice((stretch.slice * p.turns + turn) * p.wk + along); };
 
     // ---- rows, as operands: [unit][step][part]
     Chunk xf[U][Unit::kSteps][kParts];
@@ -409,7 +445,7 @@ __global__ __launch_bounds__(64 * W, W > 8 ? 4 : 2) void grouped_kernel(GroupedP
           const uint16_t* x = static_cast<const uint16_t*>(p.x) + row_of(p.ix, row) * p.ldx;
 #pragma unroll
           for (int un = 0; un < U * Unit::kRowUnits; ++un) {
-            const int k = (c0 * Unit::kRowUnits + un) * 128 + 8 * r;
+            const int k = (w.c0 * Unit::kRowUnits + un) * 128 + 8 * r;
             raw[un][i] = *reinterpret_cast<const u32x4_any*>(x + min(k, p.K - 8));
           }
         }
@@ -417,7 +453,7 @@ __global__ __launch_bounds__(64 * W, W > 8 ? 4 : 2) void grouped_kernel(GroupedP
     auto place_rows16 = [&](u32x4 (&raw)[U * Unit::kRowUnits][4]) __attribute__((always_inline)) {
 #pragma unroll
       for (int un = 0; un < U * Unit::kRowUnits; ++un) {
-        const int k0 = (c0 * Unit::kRowUnits + un) * 128;
+        const int k0 = (w.c0 * Unit::kRowUnits + un) * 128;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           if (4 * i < rows) {
@@ -441,7 +477,7 @@ __global__ __launch_bounds__(64 * W, W > 8 ? 4 : 2) void grouped_kernel(GroupedP
           const float* x = static_cast<const float*>(p.x) + row_at(2 * i + (lane >> 5)) * p.ldx;
 #pragma unroll
           for (int un = 0; un < U * Unit::kRowUnits; ++un) {
-            const int k = (c0 * Unit::kRowUnits + un) * 128 + 4 * (lane & 31);
+            const int k = (w.c0 * Unit::kRowUnits + un) * 128 + 4 * (lane & 31);
             raw[un][i] = *reinterpret_cast<const f32x4*>(x + min(k, (p.K - 1) & ~3));
           }
         }
@@ -453,10 +489,10 @@ __global__ __launch_bounds__(64 * W, W > 8 ? 4 : 2) void grouped_kernel(GroupedP
           uint32_t most = 0;
 #pragma unroll
           for (int un = 0; un < U * Unit::kRowUnits; ++un) {
-            const int k = (c0 * Unit::kRowUnits + un) * 128 + 4 * (lane & 31);
+            const int k = (w.c0 * Unit::kRowUnits + un) * 128 + 4 * (lane & 31);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              if (k + e >= p.K || un >= nc * Unit::kRowUnits) raw[un][i][e] = 0.f;
+              if (k + e >= p.K || un >= w.nc * Unit::kRowUnits) raw[un][i][e] = 0.f;
               most = max(most, __float_as_uint(raw[un][i][e]) & 0x7fffffffu);
             }
           }
@@ -514,20 +550,16 @@ __global__ __launch_bounds__(64 * W, W > 8 ? 4 : 2) void grouped_kernel(GroupedP
     };
 
     u32x4 ring[D][Unit::kLoads];
-    Scale ring_s[D][kScales];
+    typename Weights::Scale ring_s[D][Weights::kScales];
     // the unit `at` places after a pair's first (a half's U units, then the other's), in order
     auto load_at = [&](int at, bool any, int place) __attribute__((always_inline)) {
-      load_unit(any, at / U, at % U, ring[place], ring_s[place]);
-      if (at == kAll - 1) {
-        ++load_g;
-        load_q += pair_columns * p.w.ld;
-        if (Unit::k4) load_s += pair_columns * p.w.s_ldn * (int64_t)sizeof(Scale);
-      }
+      w.load(any, at / U, at % U, ring[place], ring_s[place]);
+      if (at == kAll - 1) w.load_next_pair();
     };
     // the rows' slice, and the ring from group g on
     auto rows_and_ring = [&](int g) __attribute__((always_inline)) {
       auto fill = [&]() __attribute__((always_inline)) {
-        load_from(g);
+        w.load_from(g);
 #pragma unroll
         for (int d = 0; d < D; ++d) load_at(d % kAll, true, d);
       };
@@ -549,10 +581,10 @@ __global__ __launch_bounds__(64 * W, W > 8 ? 4 : 2) void grouped_kernel(GroupedP
       if constexpr (!Unit::k4) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          Chunk w;
-          __builtin_memcpy(&w, st + r * Unit::kPitch + 16 * (4 * j + kq), 16);
+          Chunk v;
+          __builtin_memcpy(&v, st + r * Unit::kPitch + 16 * (4 * j + kq), 16);
 #pragma unroll
-          for (int part = 0; part < kParts; ++part) Op::mma(acc, xf[un][j][part], w);
+          for (int part = 0; part < kParts; ++part) Op::mma(acc, xf[un][j][part], v);
         }
       } else {
         uint32_t v[Unit::kSteps];
@@ -565,15 +597,15 @@ __global__ __launch_bounds__(64 * W, W > 8 ? 4 : 2) void grouped_kernel(GroupedP
         }
         float sc[kGroups];
 #pragma unroll
-        for (int g = 0; g < kGroups; ++g) sc[g] = scale_stage[wave].s[r][g];
+        for (int g = 0; g < kGroups; ++g) sc[g] = w.ss[r][g];
 #pragma unroll
         for (int g = 0; g < kGroups; ++g) {
           f32x4 sum = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int j = g * (G / 32); j < (g + 1) * (G / 32); ++j) {
-            const Chunk w = Op::weights(v[j]);
+            const Chunk e = Op::weights(v[j]);
 #pragma unroll
-            for (int part = 0; part < kParts; ++part) Op::mma(sum, xf[un][j][part], w);
+            for (int part = 0; part < kParts; ++part) Op::mma(sum, xf[un][j][part], e);
           }
 #pragma unroll
           for (int e = 0; e < 4; ++e) acc[e] += sc[g] * sum[e];
@@ -606,8 +638,9 @@ __global__ __launch_bounds__(64 * W, W > 8 ? 4 : 2) void grouped_kernel(GroupedP
 #pragma unroll
             for (int un = 0; un < U; ++un) {
               const int at = b * kAll + half * U + un;
-              if (un < nc && last_of(g + b, half) >= 0) {
-                stage_unit(last_of(g + b, half), un, ring[at % D], ring_s[at % D]);
+              const int last = w.last_of(g + b, half);
+              if (un < w.nc && last >= 0) {
+                w.stage(last, un, ring[at % D], ring_s[at % D]);
                 multiply_unit(acc[b][half], un);
               }
               load_at((at + D) % kAll, ONE || at + D < B * kAll, at % D);
@@ -638,20 +671,20 @@ __global__ __launch_bounds__(64 * W, W > 8 ? 4 : 2) void grouped_kernel(GroupedP
           for (int w0 = 0; w0 < W; w0 += 4) {
             float part[4][2];
 #pragma unroll
-            for (int w = 0; w < 4; ++w)
+            for (int v4 = 0; v4 < 4; ++v4)
 #pragma unroll
-              for (int half = 0; half < 2; ++half) part[w][half] = at[min(w0 + w, p.wk - 1) * 512 + half * 256];
+              for (int half = 0; half < 2; ++half) part[v4][half] = at[min(w0 + v4, p.wk - 1) * 512 + half * 256];
 #pragma unroll
-            for (int w = 0; w < 4; ++w)
+            for (int v4 = 0; v4 < 4; ++v4)
 #pragma unroll
-              for (int half = 0; half < 2; ++half) v[half] += w0 + w < p.wk ? part[w][half] : 0.f;
+              for (int half = 0; half < 2; ++half) v[half] += w0 + v4 < p.wk ? part[v4][half] : 0.f;
           }
           float* out = p.out + tile.rows[m] * p.ld_out;
           if constexpr (PHASE == GROUPED_GATE_UP) {
             const int n = pair * 16 + c;
             if (n < p.N) out[n] = activated(v[0], v[1], p.activation);
           } else {
-            out += slice_of * p.out_slice;
+            out += stretch.slice * p.out_slice;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
               const int n = (2 * pair + half) * 16 + c;
@@ -746,8 +779,8 @@ int grouped_f16_e2m1(const gtk::GroupedParams& p, int phase, const gtk::GroupedC
 int launch_row_tiles(const gtk::RowIndex& ix, gtk::RowTable* table, hipStream_t stream);
 
 // The rows' tiles that there can be, whatever the rows name.
-inline int64_t most_tiles(int64_t n, int matrices) {
-  return std::min<int64_t>(n, n / gtk::kTileRows + std::min<int64_t>(n, matrices));
+inline int64_t most_tiles(int64_t n, int matrices, int rows = 16) {
+  return std::min<int64_t>(n, n / rows + std::min<int64_t>(n, matrices));
 }
 inline void fill_cut(gtk::GroupedParams& p, const gtk::GroupedCut& c, int units, int split) {
   const int slices = c.wk * c.turns * split;

@@ -42,6 +42,7 @@ int launch_w4_expand(const W4ExpandArgs& a, int cus);
 // A launch takes the rows that one range has (all of them where there is no
 // workspace); ws: the bytes for that many, 16-byte aligned.
 int launch_route(const RouteArgs& a);
+bool moe_wide(const MoeArgs& a);  // of a whole call, M of it: what `wide` has to be set to before the others
 int64_t moe_range(const MoeArgs& a);  // tokens that one launch takes at most
 size_t moe_workspace_bytes(const MoeArgs& a, int64_t tokens);
 int launch_moe(const MoeArgs& a);

@@ -39,7 +39,7 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(ExpandParams p) {
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, kq = lane >> 4;
   if ((int)blockIdx.y >= p.table->tiles) return;
-  if (tid < 2 + kTileRows) reinterpret_cast<int*>(&tile)[tid] = reinterpret_cast<const int*>(&p.table->tile[blockIdx.y])[tid];
+  if (tid < 2 + 16) reinterpret_cast<int*>(&tile)[tid] = reinterpret_cast<const int*>(&p.table->tile[blockIdx.y])[tid];
   __syncthreads();
   const int matrix = __builtin_amdgcn_readfirstlane(tile.matrix);
   const int rows = __builtin_amdgcn_readfirstlane(tile.count);
@@ -313,7 +313,7 @@ int launch_lora(const LoraArgs& a) {
   const int64_t tiles = most_tiles(a.M, a.adapters + none);
   gtk::RowTable* table = reinterpret_cast<gtk::RowTable*>(a.ws);
   float* mid = reinterpret_cast<float*>(a.ws + s.mid);
-  const gtk::RowIndex ix{a.index, 1, (int)a.M, 1, a.adapters, 1u << 20, none, bits_of(a.adapters - 1 + none)};
+  const gtk::RowIndex ix{a.index, 1, (int)a.M, 1, a.adapters, 1u << 20, none, bits_of(a.adapters - 1 + none), 4};
   int split = 1;
   const bool units = in_units(a);
   if (!units || a.M > gtk::kFewRows) {

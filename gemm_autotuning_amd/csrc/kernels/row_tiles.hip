@@ -8,9 +8,9 @@
 namespace gtk {
 
 __global__ __launch_bounds__(1024) void row_tiles_kernel(RowIndex ix, RowTable* table) {
-  __shared__ int count[kMostMatrices + 1], place[kMostMatrices + 1];  // rows; 16 times the first tile, then the next place
+  __shared__ int count[kMostMatrices + 1], place[kMostMatrices + 1];  // rows; the first tile's place, then the next
   __shared__ int of_wave[16];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, all = ix.matrices + ix.none;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, all = ix.matrices + ix.none, in_tile = (1 << ix.tile_lg) - 1;
   constexpr int kRows = kMostRows / 1024, kEach = (kMostMatrices + 1 + 1023) / 1024;
   int e[kRows];
 #pragma unroll
@@ -34,7 +34,7 @@ __global__ __launch_bounds__(1024) void row_tiles_kernel(RowIndex ix, RowTable* 
   const int m0 = tid * kEach;
   int mine = 0;
 #pragma unroll
-  for (int m = m0; m < m0 + kEach; ++m) mine += m < all ? (count[m] + kTileRows - 1) / kTileRows : 0;
+  for (int m = m0; m < m0 + kEach; ++m) mine += m < all ? (count[m] + in_tile) >> ix.tile_lg : 0;
   int upto = mine;
 #pragma unroll
   for (int d = 1; d < 64; d *= 2) {
@@ -49,8 +49,8 @@ __global__ __launch_bounds__(1024) void row_tiles_kernel(RowIndex ix, RowTable* 
 #pragma unroll
   for (int m = m0; m < m0 + kEach; ++m)
     if (m < all) {
-      place[m] = tile * kTileRows;
-      tile += (count[m] + kTileRows - 1) / kTileRows;
+      place[m] = tile << ix.tile_lg;
+      tile += (count[m] + in_tile) >> ix.tile_lg;
     }
   __syncthreads();
   int at[kRows];
@@ -66,11 +66,11 @@ __global__ __launch_bounds__(1024) void row_tiles_kernel(RowIndex ix, RowTable* 
 #pragma unroll
   for (int j = 0; j < kRows; ++j)
     if (e[j] >= 0) {
-      RowTile& t = table->tile[at[j] / kTileRows];
-      t.rows[at[j] % kTileRows] = 1024 * j + tid;
-      if (at[j] % kTileRows == 0) {
+      RowTile& t = table->tile[at[j] >> ix.tile_lg];
+      t.rows[at[j] & in_tile] = 1024 * j + tid;
+      if ((at[j] & in_tile) == 0) {
         t.matrix = e[j];
-        t.count = min(place[e[j]] - at[j], kTileRows);
+        t.count = min(place[e[j]] - at[j], in_tile + 1);
       }
     }
 }

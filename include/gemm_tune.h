@@ -433,9 +433,10 @@ typedef enum gt_activation { GT_ACT_SILU = 0, GT_ACT_GELU = 1 /* its tanh form *
  * name an expert twice; a slot whose index is outside 0..E-1 adds nothing.
  *
  * The weights of the experts that are named are read once for up to 16 of
- * their rows, so this is for the few tokens of a decode batch: any M is
- * taken, in ranges of tokens whose intermediate values fit 64 MiB, but a
- * prompt's rows belong in one product per expert.
+ * their rows (64 where 16-bit experts have 16 rows or more on average), so
+ * this is for the few tokens of a decode batch: any M is taken, in ranges of
+ * tokens whose intermediate values take about 64 MiB, but a prompt's rows
+ * belong in one product per expert.
  *
  * The intermediate values take gt_moe_workspace bytes of device memory: the
  * caller's workspace (16-byte aligned), or, where that is NULL, the stream's,
@@ -456,7 +457,7 @@ typedef struct gt_moe_desc {
   void* y;                    /* M x K, ldy                                  */
   void* workspace;            /* or NULL                                     */
   int64_t workspace_bytes;
-  int64_t M, K, H, E, topk;   /* E <= 4096, topk <= 64                       */
+  int64_t M, K, H, E, topk;   /* E <= 4096, topk <= 64, K and H <= 2^24      */
   int64_t ldx, ldi, ldw, ldb, ldy;
   int64_t gate_up_ld, gate_up_stride; /* of rows and of experts, in elements */
   int64_t down_ld, down_stride;       /* (4 bits: bytes); <= 0: dense        */
@@ -475,7 +476,7 @@ typedef struct gt_moe_desc {
  * dimension, stride or group, a misaligned pointer, a workspace that is too
  * small; also when the stream's would have to grow while the stream is being
  * captured.  GT_ERR_UNSUPPORTED: f32 or e4m3 rows, e4m3 output or scales, E >
- * 4096, topk > 64.  GT_ERR_OOM: no memory for the workspace.  M == 0 or K ==
+ * 4096, topk > 64, K or H > 2^24.  GT_ERR_OOM: no memory for the workspace.  M == 0 or K ==
  * 0 is a no-op; H, E or topk == 0 leaves y = base (zeros without one). */
 gt_status gt_moe(const gt_moe_desc* d);
 /* The workspace's bytes (0 for none); pointers are not looked at. */
@@ -500,7 +501,7 @@ typedef struct gt_lora_desc {
   void* y;              /* M x N, ldy                                        */
   void* workspace;      /* or NULL                                           */
   int64_t workspace_bytes;
-  int64_t M, K, N, adapters, rank; /* adapters <= 4096, rank <= 256          */
+  int64_t M, K, N, adapters, rank; /* adapters <= 4096, rank <= 256, K and N <= 2^24 */
   int64_t ldx, ldb, ldy;
   int64_t a_ld, a_stride, b_ld, b_stride; /* elements; <= 0: dense           */
   int32_t x_dtype;   /* f16, bf16: x, a and b                                */
@@ -508,8 +509,8 @@ typedef struct gt_lora_desc {
   void* stream;
 } gt_lora_desc;
 
-/* Errors as gt_moe (GT_ERR_UNSUPPORTED: adapters > 4096, rank > 256).  M == 0
- * or N == 0 is a no-op; K, adapters or rank == 0 leaves y = base. */
+/* Errors as gt_moe (GT_ERR_UNSUPPORTED: adapters > 4096, rank > 256, K or N >
+ * 2^24).  M == 0 or N == 0 is a no-op; K, adapters or rank == 0 leaves y = base. */
 gt_status gt_lora(const gt_lora_desc* d);
 gt_status gt_lora_workspace(const gt_lora_desc* d, int64_t* bytes);
 

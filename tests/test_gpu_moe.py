@@ -234,3 +234,52 @@ def test_the_callers_workspace_is_enough_and_not_left(T, E, k, K, H):
     torch.cuda.synchronize()
     assert (buf[n:] == 0x5A).all(), "written past the workspace"
     assert torch.equal(y.cpu(), run(x, index, weight, w))
+
+
+@pytest.mark.parametrize("dtype", [BF, F16])
+@pytest.mark.parametrize("T,E,k,K,H", [(16, 1, 1, 96, 40), (63, 2, 1, 257, 130), (64, 1, 1, 128, 256), (65, 1, 1, 500, 9), (33, 2, 2, 8, 8),
+                                       (129, 3, 2, 100, 300), (150, 2, 2, 640, 17), (40, 2, 2, 1100, 600), (17, 1, 1, 31, 1500)])
+def test_many_rows_of_an_expert(dtype, T, E, k, K, H):
+    same(T, E, k, K, H, dtype, act="gelu" if T % 2 else "silu", out=F32 if T % 3 else None, absent=T > 100, base=T > 64,
+         pad=3 * (T % 2), spread=bool(T % 2), seed=T)
+
+
+def test_the_rows_of_one_expert_among_many():
+    # on average 16 rows to an expert and more, and all of them name one
+    T, E, K, H = 200, 5, 130, 70
+    x = ref.loud(T, K, 1).to(BF)
+    w = layer(E, H, K, BF, "none", 128, "bf16", 2)
+    weight = torch.rand(T, 1, generator=ref.rng(3))
+    index = torch.full((T, 1), 3, dtype=torch.int32)
+    index[77] = -1
+    for e in (0, 1, 2, 4):
+        w["gate_up"][e], w["down"][e] = math.nan, math.nan
+    got = run(x, index, weight, w)
+    want, far = br.moe(x, index, weight, w["gate_up"], w["down"])
+    ref.check(got, want, far, "y")
+
+
+@pytest.mark.parametrize("dtype", [BF, F16])
+def test_non_finite_rows_among_many_stay_their_own(dtype):
+    T = 90
+    x = ref.loud(T, 200, 1).to(dtype)
+    w = layer(2, 70, 200, dtype, "none", 128, "bf16", 2)
+    index, weight = br.choices(T, 2, 2, 3)
+    clean = run(x, index, weight, w)
+    x[3, 17], x[70, 199] = math.inf, math.nan
+    got = run(x, index, weight, w)
+    keep = [m for m in range(T) if m not in (3, 70)]
+    assert torch.equal(got[keep], clean[keep]) and torch.isnan(got[70].float()).all()
+    assert not torch.isfinite(got[3].float()).any()
+
+
+def test_large_and_small_activations_of_many_f16_rows():
+    for big in (2.0 ** 9, 2.0 ** -9):
+        x = (ref.loud(80, 128, 1) * big).to(F16)
+        w = layer(2, 300, 128, F16, "none", 128, "bf16", 2)
+        index, weight = br.choices(80, 2, 2, 3)
+        if big > 1:
+            weight *= 2.0 ** -14
+        got = run(x, index, weight, w, out=F32)
+        want, far = br.moe(x, index, weight, w["gate_up"], w["down"])
+        ref.check(got, want, far)

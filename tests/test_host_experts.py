@@ -62,6 +62,7 @@ REFUSED = [
     ("moe", dict(M=-1), INVALID), ("moe", dict(K=-1), INVALID), ("moe", dict(H=-1), INVALID), ("moe", dict(E=-1), INVALID),
     ("moe", dict(topk=-1), INVALID), ("moe", dict(E=4097), UNSUPPORTED), ("moe", dict(topk=65), UNSUPPORTED),
     ("moe", dict(K=(1 << 30) + 1), UNSUPPORTED), ("moe", dict(H=(1 << 30) + 1), UNSUPPORTED),
+    ("moe", dict(K=(1 << 24) + 1), UNSUPPORTED), ("moe", dict(H=(1 << 24) + 1), UNSUPPORTED),
     ("moe", dict(x_dtype=gt.F32), UNSUPPORTED), ("moe", dict(x_dtype=gt.FP8_E4M3), UNSUPPORTED), ("moe", dict(x_dtype=-1), INVALID),
     ("moe", dict(out_dtype=gt.FP8_E4M3), UNSUPPORTED), ("moe", dict(out_dtype=7), INVALID), ("moe", dict(format=2), INVALID),
     ("moe", dict(format=-2), INVALID), ("moe", dict(activation=2), INVALID), ("moe", dict(activation=-1), INVALID),
@@ -84,6 +85,7 @@ REFUSED = [
     ("lora", dict(y=None), INVALID), ("lora", dict(M=-1), INVALID), ("lora", dict(K=-1), INVALID), ("lora", dict(N=-1), INVALID),
     ("lora", dict(adapters=-1), INVALID), ("lora", dict(rank=-1), INVALID), ("lora", dict(adapters=4097), UNSUPPORTED),
     ("lora", dict(rank=257), UNSUPPORTED), ("lora", dict(K=(1 << 30) + 1), UNSUPPORTED), ("lora", dict(N=(1 << 30) + 1), UNSUPPORTED),
+    ("lora", dict(K=(1 << 24) + 1), UNSUPPORTED), ("lora", dict(N=(1 << 24) + 1), UNSUPPORTED),
     ("lora", dict(x_dtype=gt.F32), UNSUPPORTED), ("lora", dict(x_dtype=9), INVALID), ("lora", dict(out_dtype=gt.FP8_E4M3), UNSUPPORTED),
     ("lora", dict(ldx=63), INVALID), ("lora", dict(ldb=31), INVALID), ("lora", dict(ldy=31), INVALID), ("lora", dict(a_ld=63), INVALID),
     ("lora", dict(b_ld=15), INVALID), ("lora", dict(a_stride=63), INVALID), ("lora", dict(b_stride=15), INVALID),
