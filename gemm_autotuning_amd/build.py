@@ -35,7 +35,7 @@ HOST_SOURCES = ["key.cpp", "candidates.cpp", "tuner.cpp", "cache.cpp", "device.c
                 "operators.cpp", "experts.cpp"]
 # the kernels written out by hand; the tile kernels are generated beside them
 HIP_SOURCES = ["small_kernels.hip", "gemv.hip", "scratch.hip", "rmsnorm.hip", "w4.hip", "route.hip",
-               "experts.hip", "lora.hip", "row_tiles.hip"] + [
+               "experts.hip", "experts_token.hip", "lora.hip", "row_tiles.hip"] + [
     "w4_%s_%s.hip" % (x, f) for x in ("bf16", "f16", "e4m3") for f in ("int4", "e2m1")] + [
     "grouped_%s%s.hip" % (x, f) for x in ("bf16", "f16") for f in ("", "_int4", "_e2m1")] + [
     "grouped_wide_bf16.hip", "grouped_wide_f16.hip"]

@@ -1,6 +1,6 @@
 // experts.hip -- a layer of gated experts for a few tokens: the gated product
 // into fp32 activations per (token, slot) pair, the down product of each pair
-// (grouped.h), and the pairs' weighted sum.
+// (grouped.h), and the pairs' weighted sum; single tokens in experts_token.hip.
 #include "elements.h"
 #include "grouped_wide.h"
 #include "launchers.h"
@@ -146,6 +146,24 @@ bool in_units(const MoeArgs& a, const ExpertWeights& w, int64_t K) {
   return w.s_ldn <= most / 32 / e && w.s_ldg <= most / 2 / e / ((K >> a.group_lg) + 1);
 }
 
+// Whether so few tokens name the same experts that each may read its own
+// (experts_token.hip): up to 32 MiB of weights read again, of 4 bits 4 MiB
+// (their expansion costs more than their bytes), where every choice is as
+// likely.  bf16, 8 of 128 experts 2048 x 768: 1 token 18.4 us and 24.4 with
+// tiles, 4 tokens (27 MB) 50 and 53, 6 (61 MB) 70 and 66; 2 of 8 experts 256 x
+// 512: 8 tokens 9.7 and 16.  int4, 4 of 64 experts 4096 x 2048: 1 token 20.8 and 24.5,
+// 2 (3 MB) 34.0 and 34.4, 4 (20 MB) 55 and 51; 4 of 32 experts 1024 x 512: 4 tokens
+// (3 MB) 15.8 and 20.5.  More than 8 tokens would gain only where the experts are
+// tiny (16 tokens, 2 of 8 experts 256 x 512: 11.4 and 17.2) and have the tiles.
+bool hardly_share(const MoeArgs& a) {
+  if (a.M > 8) return false;
+  double left = 1.0;  // the share of experts that no token names
+  for (int64_t t = 0; t < a.M; ++t) left *= std::max(0.0, 1.0 - (double)a.topk / a.E);
+  const double again = (double)(a.M * a.topk) - a.E * (1.0 - left);
+  const double bytes = 3.0 * a.H * a.K * (a.format < 0 ? 2.0 : 0.5);
+  return again * bytes <= (a.format < 0 ? 32.0 : 4.0) * (1 << 20);
+}
+
 // How a product's K is cut: into units, a wave's slice of them, and where one
 // workgroup's waves do not hold all of them, turns (the gated product) or
 // workgroups whose sums the join adds (the down product).
@@ -222,6 +240,7 @@ int launch_moe(const MoeArgs& a) {
     hipLaunchKernelGGL(gtk::moe_down_kernel, dim3((unsigned)((a.K + 3) / 4), (unsigned)a.M), dim3(256), 0, a.stream, a, act);
     return hipGetLastError() == hipSuccess ? LS_OK : LS_HIP_ERROR;
   }
+  if (hardly_share(a)) return launch_moe_tokens(a, act, s.act_ld);
   const int64_t pairs = a.M * a.topk, tiles = most_tiles(pairs, a.E, a.wide ? 64 : 16);
   gtk::GroupedParams p{};
   p.ix = gtk::RowIndex{a.index, a.ldi, (int)pairs, a.topk, a.E, ((1u << 20) + a.topk - 1) / a.topk, 0, bits_of(a.E - 1), a.wide ? 6 : 4};

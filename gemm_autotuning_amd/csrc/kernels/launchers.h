@@ -46,6 +46,7 @@ bool moe_wide(const MoeArgs& a);  // of a whole call, M of it: what `wide` has t
 int64_t moe_range(const MoeArgs& a);  // tokens that one launch takes at most
 size_t moe_workspace_bytes(const MoeArgs& a, int64_t tokens);
 int launch_moe(const MoeArgs& a);
+int launch_moe_tokens(const MoeArgs& a, float* act, int64_t act_ld);  // launch_moe's, where there are few
 int64_t lora_range(const LoraArgs& a);
 size_t lora_workspace_bytes(const LoraArgs& a, int64_t rows);
 int launch_lora(const LoraArgs& a);

@@ -83,6 +83,28 @@ def test_sizes(fmt, group, scales, K, H):
          spread=True, absent=True, base=bool(K % 2), seed=K)
 
 
+@pytest.mark.parametrize("fmt,group,scales", [("none", 128, "bf16"), ("int4", 32, "f32"), ("e2m1", 64, "f16"), ("int4", 128, "bf16")])
+@pytest.mark.parametrize("K,H", [(1, 1), (2, 3), (7, 9), (8, 8), (15, 17), (31, 33), (32, 64), (63, 65), (100, 129), (127, 130),
+                                 (257, 255), (300, 511), (520, 70)])
+def test_sizes_of_more_tokens(fmt, group, scales, K, H):
+    same(11, 4, 2, K, H, BF if K % 2 else F16, fmt, group, scales, act="gelu" if H % 2 else "silu", out=F32 if K % 3 else None, pad=3,
+         spread=True, absent=True, base=bool(K % 2), seed=K)
+
+
+@pytest.mark.parametrize("fmt", ["none", "int4", "e2m1"])
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (2, 64, 8), (4, 40, 3), (8, 300, 2), (8, 9, 9)])
+def test_few_tokens_of_many_experts(fmt, T, E, k):
+    same(T, E, k, 72, 40, F16 if T % 4 else BF, fmt, 32, "f16", absent=T > 1, base=E > 40, out=F32 if k == 9 else None, pad=T, spread=E < 40,
+         seed=E)
+
+
+@pytest.mark.parametrize("fmt", ["none", "int4"])
+def test_long_rows_of_more_tokens(fmt):
+    same(9, 2, 2, 1100, 1500, BF, fmt, 64, seed=1)
+    same(9, 2, 1, 5000, 40, F16, fmt, 32, seed=2)
+    same(10, 2, 1, 40, 9001, BF, fmt, 128, seed=3)
+
+
 @pytest.mark.parametrize("fmt", ["none", "int4"])
 def test_long_rows(fmt):
     same(2, 3, 2, 1100, 1500, BF, fmt, 64, seed=1)
@@ -119,13 +141,15 @@ def test_whole_numbers(fmt, dtype, T, E, k, K, H):
     assert torch.equal(got.double(), want)
 
 
-def test_an_expert_named_twice_and_indices_out_of_range():
-    x = ref.loud(4, 96, 1).to(BF)
+@pytest.mark.parametrize("times", [1, 4])
+def test_an_expert_named_twice_and_indices_out_of_range(times):
+    x = ref.loud(4 * times, 96, 1).to(BF)
     w = layer(3, 64, 96, BF, "none", 128, "bf16", 2)
     index = torch.tensor([[1, 1, 1], [0, 3, 0], [-1, -7, 2 ** 31 - 1], [2, -2 ** 31, 0]], dtype=torch.int32)
     weight = torch.rand(4, 3, generator=ref.rng(3))
     weight[1, 1] = math.nan  # of a slot that is never followed
-    base = br.normal((4, 96), 1.0, BF, 4)
+    index, weight = index.repeat(times, 1), weight.repeat(times, 1)
+    base = br.normal((4 * times, 96), 1.0, BF, 4)
     for b in (None, base):
         got = run(x, index, weight, w, base=b)
         want, far = br.moe(x, index, weight, w["gate_up"], w["down"], base=b)
@@ -133,45 +157,49 @@ def test_an_expert_named_twice_and_indices_out_of_range():
         assert torch.equal(got[2].double(), want[2])
 
 
-def test_in_place():
-    x = ref.loud(6, 100, 1).to(F16)
+@pytest.mark.parametrize("T", [6, 11])
+def test_in_place(T):
+    x = ref.loud(T, 100, 1).to(F16)
     w = layer(3, 50, 100, F16, "none", 128, "bf16", 2)
-    index, weight = br.choices(6, 3, 2, 3)
-    base = br.normal((6, 100), 1.0, F16, 4)
+    index, weight = br.choices(T, 3, 2, 3)
+    base = br.normal((T, 100), 1.0, F16, 4)
     a = run(x, index, weight, w, base=base, pad=5)
     assert torch.equal(a, run(x, index, weight, w, base=base, pad=5, in_place=True))
 
 
+@pytest.mark.parametrize("T", [7, 9])
 @pytest.mark.parametrize("dtype", [BF, F16])
-def test_non_finite_rows_stay_their_own(dtype):
+def test_non_finite_rows_stay_their_own(dtype, T):
     # an infinity or NaN in a row makes that row's results what the formula gives and leaves the others
-    x = ref.loud(9, 200, 1).to(dtype)
+    x = ref.loud(T, 200, 1).to(dtype)
     w = layer(2, 70, 200, dtype, "none", 128, "bf16", 2)
-    index, weight = br.choices(9, 2, 2, 3)
+    index, weight = br.choices(T, 2, 2, 3)
     clean = run(x, index, weight, w)
     x[3, 17], x[5, 199] = math.inf, math.nan
     got = run(x, index, weight, w)
-    keep = [m for m in range(9) if m not in (3, 5)]
+    keep = [m for m in range(T) if m not in (3, 5)]
     assert torch.equal(got[keep], clean[keep]) and torch.isnan(got[5].float()).all()
     assert not torch.isfinite(got[3].float()).any()
 
 
-def test_infinite_results_have_their_sign():
+@pytest.mark.parametrize("T", [2, 10])
+def test_infinite_results_have_their_sign(T):
     # an activation past every number, times weights of one sign: an infinity, not a NaN
-    x = torch.full((2, 64), 1.0).to(BF)
+    x = torch.full((T, 64), 1.0).to(BF)
     gate_up = torch.ones(1, 2 * 32, 64).to(BF) * 2.0 ** 70
     down = torch.ones(1, 64, 32).to(BF)
     down[0, 1::2] = -1.0
-    got = run(x, torch.zeros(2, 1, dtype=torch.int32), torch.ones(2, 1), dict(gate_up=gate_up, down=down))
+    got = run(x, torch.zeros(T, 1, dtype=torch.int32), torch.ones(T, 1), dict(gate_up=gate_up, down=down))
     assert (got[:, 0::2] == math.inf).all() and (got[:, 1::2] == -math.inf).all()
 
 
-def test_large_and_small_activations_of_f16():
+@pytest.mark.parametrize("T", [3, 12])
+def test_large_and_small_activations_of_f16(T):
     # values between the products far outside f16's own range, above and below
     for big in (2.0 ** 9, 2.0 ** -9):
-        x = (ref.loud(3, 128, 1) * big).to(F16)
+        x = (ref.loud(T, 128, 1) * big).to(F16)
         w = layer(2, 96, 128, F16, "none", 128, "bf16", 2)
-        index, weight = br.choices(3, 2, 2, 3)
+        index, weight = br.choices(T, 2, 2, 3)
         if big > 1:
             weight *= 2.0 ** -14
         got = run(x, index, weight, w, out=F32)
@@ -179,12 +207,13 @@ def test_large_and_small_activations_of_f16():
         ref.check(got, want, far)
 
 
-def test_weights_that_nothing_reads():
+@pytest.mark.parametrize("T", [2, 12])
+def test_weights_that_nothing_reads(T):
     # experts that no token names may hold anything
-    x = ref.loud(2, 64, 1).to(BF)
+    x = ref.loud(T, 64, 1).to(BF)
     w = layer(5, 32, 64, BF, "none", 128, "bf16", 2)
-    index = torch.tensor([[1, 3], [3, 1]], dtype=torch.int32)
-    weight = torch.rand(2, 2, generator=ref.rng(1))
+    index = torch.tensor([[1, 3], [3, 1]], dtype=torch.int32).repeat(T // 2, 1)
+    weight = torch.rand(T, 2, generator=ref.rng(1))
     clean = run(x, index, weight, w)
     for e in (0, 2, 4):
         w["gate_up"][e], w["down"][e] = math.nan, math.nan
