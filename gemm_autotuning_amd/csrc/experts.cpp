@@ -249,6 +249,7 @@ gt_status lora(const gt_lora_desc* d) {
   GT_CHECK(operand(d->base, false, a.M, a.ldb, elem_bytes(a.out_dtype), "base"));
   GT_CHECK(operand(d->y, true, a.M, a.ldy, elem_bytes(a.out_dtype), "y"));
   if (d->base == d->y && a.ldb != a.ldy) return invalid("base is y with another leading dimension");
+  if (!empty && d->x == d->y) return invalid("y is x");
   a.x = d->x;
   a.index = d->index;
   a.scale = d->scale;

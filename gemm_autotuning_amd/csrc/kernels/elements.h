@@ -155,6 +155,12 @@ template <int CTRL>
 __device__ __forceinline__ uint32_t dpp(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, true);
 }
+// The lower or upper 16-bit element of a dword.
+template <int XT>
+__device__ __forceinline__ float half_to_f32(uint32_t u, int upper) {
+  if constexpr (XT == DT_BF16) return __uint_as_float(upper ? u & 0xffff0000u : u << 16);
+  return f16_bits_to_f32((uint16_t)(upper ? u >> 16 : u));
+}
 template <class F>
 __device__ __forceinline__ uint32_t wave_join(uint32_t v, F f) {
   v = f(v, dpp<0xB1>(v));   // lanes 1 0 3 2

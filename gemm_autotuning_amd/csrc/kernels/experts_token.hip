@@ -33,13 +33,6 @@ __device__ __forceinline__ float wave_sum(float v) {
   }));
 }
 
-// The lower or upper half of a dword.
-template <int XT>
-__device__ __forceinline__ float bits_to_f32(uint32_t u, int upper) {
-  if constexpr (XT == DT_BF16) return __uint_as_float(upper ? u & 0xffff0000u : u << 16);
-  return f16_bits_to_f32((uint16_t)(upper ? u >> 16 : u));
-}
-
 // The eight weights of a dword of codes: e2m1 as they are, integers as
 // sixteenths (the conversion's own unit).
 template <int FMT>
@@ -125,7 +118,7 @@ __global__ __launch_bounds__(512, 4) void token_kernel(gt::MoeArgs a, float* act
         x[e] = __uint_as_float(u.x[e / 4][e % 4]) * f;
         if (tail && u.k0 + e >= K) x[e] = 0.f;
       } else {
-        x[e] = bits_to_f32<XT>(u.x[e / 8][e / 2 % 4], e & 1);
+        x[e] = half_to_f32<XT>(u.x[e / 8][e / 2 % 4], e & 1);
       }
     }
 #pragma unroll
@@ -146,7 +139,7 @@ __global__ __launch_bounds__(512, 4) void token_kernel(gt::MoeArgs a, float* act
         acc[i] += (FMT == W4_INT4 ? 16.f * s : s) * sum;
       } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) acc[i] = fmaf(bits_to_f32<XT>(u.q[i][e / 2], e & 1), x[e], acc[i]);
+        for (int e = 0; e < 8; ++e) acc[i] = fmaf(half_to_f32<XT>(u.q[i][e / 2], e & 1), x[e], acc[i]);
       }
     }
   };

@@ -1,7 +1,7 @@
 // lora.hip -- adapters of many requests beside a shared projection: the first
 // product of each row (grouped.h, slices of K to workgroups where the rows are
 // few) into fp32 values, then the second one, which adds the slices, and the
-// base to its results.
+// base to its results; few rows of small adapters in one launch.
 #include "elements.h"
 #include "grouped.h"
 #include "launchers.h"
@@ -209,6 +209,91 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(ExpandParams p) {
   }
 }
 
+constexpr int kFewThreads = 1024;
+
+// A few rows of small adapters in one launch: every workgroup computes its row's
+// first product anew, its waves along the rank and K (16 bytes of a row of a to
+// a lane, 16 rows at once), and then 1024 columns of the second, one to a
+// thread, whose rows of b it has loaded meanwhile.  All in fp32.  It is a chain
+// of waits (the adapter's number, its weights, two barriers) rather than of
+// bytes: one row of rank 16, 4096 x 4096, 5.5 us for 0.3 MB; 77 rows of rank 12, 1001 x 999,
+// 5.6 us where the tiles' two launches take 11.6.
+template <int XT>
+__global__ __launch_bounds__(kFewThreads) void lora_few_kernel(gt::LoraArgs a) {
+  constexpr int kRows = 16, kEach = 4, kWaves = kFewThreads / 64;
+  __shared__ float sums[kWaves][256], h[256];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t m = blockIdx.y, n = (int64_t)blockIdx.x * kFewThreads + tid;
+  const int e = a.index[m], K = (int)a.K;
+  const float base = a.base && n < a.N ? load_any(a.base, m * a.ldb + n, a.out_dtype) : 0.f;
+  if (e < 0 || e >= a.adapters) {
+    if (a.base != a.y && n < a.N) store_out(a.y, m * a.ldy + n, base, a.out_dtype);
+    return;
+  }
+  const uint16_t* const b = reinterpret_cast<const uint16_t*>(a.b.p + e * a.b.stride + min(n, a.N - 1) * a.b.ld);
+  u32x4 part[kEach];  // of the column's row, its first 32 ahead
+  auto load_part = [&](int r) __attribute__((always_inline)) {
+    if (a.rank >= 8)
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) part[i] = *reinterpret_cast<const u32x4_any*>(b + min(r + 8 * i, a.rank - 8));
+  };
+  load_part(0);
+  const uint16_t* const x = static_cast<const uint16_t*>(a.x) + m * a.ldx;
+  const char* const w = a.a.p + e * a.a.stride;
+  const int groups = (a.rank + kRows - 1) / kRows, along = kWaves / groups;  // of the rank; waves along K
+  const int r0 = wave % groups * kRows, part_k = wave / groups;
+  if (part_k < along) {
+    float acc[kRows] = {};
+    for (int k0 = 512 * part_k; k0 < K; k0 += 512 * along) {
+      const int k = k0 + 8 * lane, at = min(k, K - 8);
+      u32x4 v = *reinterpret_cast<const u32x4_any*>(x + at), q[kRows];
+#pragma unroll
+      for (int i = 0; i < kRows; ++i)
+        q[i] = *reinterpret_cast<const u32x4_any*>(w + (int64_t)min(r0 + i, a.rank - 1) * a.a.ld + 2 * at);
+      if (k0 + 512 > K) {  // what lies past the end becomes zero
+        v = bytes_from(v, min(2 * (k - at), 16));
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) q[i] = bytes_from(q[i], min(2 * (k - at), 16));
+      }
+#pragma unroll
+      for (int i = 0; i < kRows; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[i] = fmaf(half_to_f32<XT>(q[i][j / 2], j & 1), half_to_f32<XT>(v[j / 2], j & 1), acc[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const float v = wave_sum(acc[i]);
+      if (lane == 0 && r0 + i < a.rank) sums[part_k][r0 + i] = v;
+    }
+  }
+  __syncthreads();
+  if (tid < a.rank) {
+    float v = 0.f;
+    for (int i = 0; i < along; ++i) v += sums[i][tid];
+    h[tid] = v;
+  }
+  __syncthreads();
+  if (n >= a.N) return;
+  float v = 0.f;
+  if (a.rank < 8) {
+    for (int j = 0; j < a.rank; ++j) v = fmaf(load_any(b, j, a.x_dtype), h[j], v);
+  } else {
+    auto add = [&](int r, const u32x4& q) __attribute__((always_inline)) {
+      const int at = min(r, a.rank - 8);  // the last eight may hold some twice
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (at + j >= r) v = fmaf(half_to_f32<XT>(q[j / 2], j & 1), h[at + j], v);
+    };
+    for (int r = 0; r < a.rank; r += 8 * kEach) {
+      if (r > 0) load_part(r);
+#pragma unroll
+      for (int i = 0; i < kEach; ++i)
+        if (r + 8 * i < a.rank) add(r + 8 * i, part[i]);
+    }
+  }
+  store_out(a.y, m * a.ldy + n, base + (a.scale ? a.scale[e] : 1.f) * v, a.out_dtype);
+}
+
 // Rows of x or of the adapters' first matrices too short for a lane's 16
 // bytes, or the latter so far apart that a tile's offsets pass 32 bits: a wave
 // to a value.
@@ -239,8 +324,22 @@ namespace {
 
 bool in_units(const LoraArgs& a) { return a.K >= 8 && a.a.ld <= (INT64_C(1) << 27); }
 
-// The first product's slices: one workgroup's K where the tiles alone fill the
-// CUs, more where they do not.
+// Whether one launch that computes the first product again for every 1024
+// columns is the faster: matrices a of up to 256 KB, and rows and columns for
+// one workgroup to a CU, or two where the rows are so many that the tiles'
+// table would be a launch of its own.  bf16, against the tiles: 1 row, rank 16, 4096 x 4096 5.5 us and
+// 8.5, rank 32 7.5 and 9.3; 64 rows of rank 16 7.6 and 9.8, 128 (512 workgroups)
+// 13.2 and 11.2; 256 rows 2048 x 2048 (512) 11.4 and 14.8; 1 row of rank 32 and
+// 8192 x 2048 (512 KB) 10.8 and 9.5; rank 64, 1024 x 1024, 10.1 and 9.6.
+bool few_rows(const LoraArgs& a) {
+  const int64_t workgroups = a.M * ((a.N + gtk::kFewThreads - 1) / gtk::kFewThreads);
+  return a.K >= 8 && a.rank <= 32 && a.rank * a.K <= 128 << 10 && workgroups <= (a.M > gtk::kFewRows ? 2 : 1) * a.cus;
+}
+
+// The first product's slices: one workgroup's K where the tiles alone give
+// eight workgroups to a CU, more where they do not (4096 rows of 6 adapters rank 32, 4096
+// long: 42 us with 4 slices, 44 with one; a number of slices that does not
+// divide the waves' units loses, 50 with 3).
 struct LoraCut {
   gtk::GroupedCut c;
   int units, split;
@@ -250,9 +349,9 @@ LoraCut cut(const LoraArgs& a, int64_t rows) {
   const int64_t tiles = most_tiles(rows, a.adapters);
   l.units = (int)((a.K + 127) / 128);
   const int pairs = (a.rank + 31) / 32;
-  const int64_t want = std::max<int64_t>(1, 2 * a.cus / (tiles * pairs));
+  const int64_t want = (int64_t)1 << (bits_of((int)std::min<int64_t>(std::max<int64_t>(1, 8 * a.cus / (tiles * pairs)), 16)) - 1);
   l.c.wk = std::min(8, l.units);
-  l.split = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, 16), l.units / l.c.wk));
+  l.split = (int)std::max<int64_t>(1, std::min<int64_t>(want, l.units / l.c.wk));
   const int each = (l.units + l.c.wk * l.split - 1) / (l.c.wk * l.split);  // of a wave
   l.c.U = each > 2 ? 4 : (each > 1 ? 2 : 1);
   l.c.turns = (each + l.c.U - 1) / l.c.U;
@@ -308,6 +407,14 @@ int64_t lora_range(const LoraArgs& a) {
 size_t lora_workspace_bytes(const LoraArgs& a, int64_t rows) { return space(a, rows).bytes; }
 
 int launch_lora(const LoraArgs& a) {
+  if (few_rows(a)) {
+    const dim3 grid((unsigned)((a.N + gtk::kFewThreads - 1) / gtk::kFewThreads), (unsigned)a.M);
+    if (a.x_dtype == DT_BF16)
+      hipLaunchKernelGGL((gtk::lora_few_kernel<DT_BF16>), grid, dim3(gtk::kFewThreads), 0, a.stream, a);
+    else
+      hipLaunchKernelGGL((gtk::lora_few_kernel<DT_F16>), grid, dim3(gtk::kFewThreads), 0, a.stream, a);
+    return hipGetLastError() == hipSuccess ? LS_OK : LS_HIP_ERROR;
+  }
   const LoraSpace s = space(a, a.M);
   const int none = a.base != a.y;
   const int64_t tiles = most_tiles(a.M, a.adapters + none);

@@ -485,7 +485,8 @@ gt_status gt_moe_workspace(const gt_moe_desc* d, int64_t* bytes);
 /* Adapters of many requests beside a shared projection: with a = index[m],
  *   y[m] = base[m] + scale[a] * b_a (a_a x[m])
  * where a_a is rank x K and b_a is N x rank (smaller ranks are padded with
- * zeros).  base is the projection's own result, y itself to add in place; a
+ * zeros).  base is the projection's own result, y itself to add in place (x
+ * must not overlap y: all of a row is read for each of its results); a
  * row without an adapter (an index outside 0..adapters-1) is left as base, not
  * written at all in place.  Sums and what passes between the products are
  * fp32 (two 16-bit parts of it in the second, as gt_moe); y is rounded once.
@@ -509,7 +510,7 @@ typedef struct gt_lora_desc {
   void* stream;
 } gt_lora_desc;
 
-/* Errors as gt_moe (GT_ERR_UNSUPPORTED: adapters > 4096, rank > 256, K or N >
+/* Errors as gt_moe, and GT_ERR_INVALID_ARG where y is x (GT_ERR_UNSUPPORTED: adapters > 4096, rank > 256, K or N >
  * 2^24).  M == 0 or N == 0 is a no-op; K, adapters or rank == 0 leaves y = base. */
 gt_status gt_lora(const gt_lora_desc* d);
 gt_status gt_lora_workspace(const gt_lora_desc* d, int64_t* bytes);

@@ -61,7 +61,7 @@ static gt_lora_desc adapters(int64_t M, int64_t K, int64_t N, int64_t rank) {
   memset(&d, 0, sizeof(d));
   d.x = d.a = d.b = P;
   d.index = (const int32_t*)P;
-  d.y = P;
+  d.y = (char*)P + 4096;
   d.M = M;
   d.K = K;
   d.N = N;

@@ -79,14 +79,31 @@ def test_columns(N):
     same(20, 4, 8, 96, N, BF if N % 2 else F16, seed=N, pad=3, out=F32 if N % 3 == 0 else None)
 
 
+@pytest.mark.parametrize("r", [1, 4, 7, 8, 9, 15, 16, 17, 24, 31, 32])
+def test_ranks_of_many_rows(r):
+    same(700, 7, r, 72, 40, BF if r % 2 else F16, out=F32 if r > 8 else None, pad=r % 4, spread=r > 4, seed=r)
+
+
+@pytest.mark.parametrize("K", [8, 9, 31, 100, 127, 128, 129, 300, 1000, 2050])
+def test_lengths_of_wide_results(K):
+    same(90, 7, 16, K, 2100, F16 if K % 2 else BF, out=F32, pad=K % 2, spread=K > 128, seed=K)
+
+
+@pytest.mark.parametrize("r,K", [(32, 4096), (32, 4097), (33, 64), (16, 8193), (20, 520), (1, 1 << 17)])
+@pytest.mark.parametrize("M", [2, 19])
+def test_ranks_and_lengths_of_few_rows(M, r, K):
+    same(M, 3, r, K, 1030, BF if M == 2 else F16, out=F32, seed=r)
+
+
+@pytest.mark.parametrize("N", [80, 2700])
 @pytest.mark.parametrize("order", ["one", "runs", "each", "none", "alternate", "out of range"])
-def test_orders(order):
+def test_orders(order, N):
     M, L = 100, 100
     index = {"one": torch.full((M,), 7), "runs": torch.arange(M) // 30, "each": torch.randperm(L, generator=ref.rng(1)),
              "none": torch.full((M,), -1), "alternate": torch.arange(M) % 2 * 50,
              "out of range": torch.where(torch.arange(M) % 3 == 0, 2 ** 31 - 1, torch.where(torch.arange(M) % 3 == 1, -2 ** 31, 3))}[order]
     for in_place in (False, True):
-        same(M, L, 8, 64, 80, BF, index=index.int(), in_place=in_place, pad=2)
+        same(M, L, 8, 64, N, BF, index=index.int(), in_place=in_place, pad=2)
 
 
 @pytest.mark.parametrize("dtype", [BF, F16])
@@ -107,10 +124,11 @@ def test_whole_numbers(dtype, M, L, r, K, N):
     assert torch.equal(got.double(), want)
 
 
+@pytest.mark.parametrize("r", [8, 40])
 @pytest.mark.parametrize("dtype", [BF, F16])
-def test_non_finite_rows_stay_their_own(dtype):
+def test_non_finite_rows_stay_their_own(dtype, r):
     x = ref.loud(20, 100, 1).to(dtype)
-    a, b = br.normal((3, 8, 100), 0.1, dtype, 2), br.normal((3, 60, 8), 0.3, dtype, 3)
+    a, b = br.normal((3, r, 100), 0.1, dtype, 2), br.normal((3, 60, r), 0.3, dtype, 3)
     index = torch.arange(20).int() % 4 - 1
     clean = run(x, index, a, b)
     x[5, 3], x[6, 99], x[4, 0] = math.inf, math.nan, math.inf  # row 4 has no adapter
@@ -120,9 +138,10 @@ def test_non_finite_rows_stay_their_own(dtype):
     assert torch.isnan(got[6].float()).all() and not torch.isfinite(got[5].float()).any()
 
 
-def test_a_base_that_is_not_finite():
+@pytest.mark.parametrize("r", [8, 40])
+def test_a_base_that_is_not_finite(r):
     x = ref.loud(4, 64, 1).to(BF)
-    a, b = br.normal((2, 8, 64), 0.1, BF, 2), br.normal((2, 40, 8), 0.3, BF, 3)
+    a, b = br.normal((2, r, 64), 0.1, BF, 2), br.normal((2, 40, r), 0.3, BF, 3)
     base = torch.zeros(4, 40).to(BF)
     base[0, 0], base[1, 39], base[3, 5] = math.inf, math.nan, -math.inf
     got = run(x, torch.tensor([0, 1, -1, -1], dtype=torch.int32), a, b, base=base)
@@ -130,11 +149,12 @@ def test_a_base_that_is_not_finite():
     assert torch.isfinite(got.float()).sum() == 4 * 40 - 3
 
 
-def test_large_and_small_values_of_f16():
+@pytest.mark.parametrize("r", [8, 40])
+def test_large_and_small_values_of_f16(r):
     for big in (2.0 ** 9, 2.0 ** -12):
         x = (ref.loud(6, 200, 1) * big).to(F16)
-        a = (br.normal((2, 8, 200), big, F32, 2)).to(F16)
-        b = br.normal((2, 30, 8), 0.3, F16, 3)
+        a = (br.normal((2, r, 200), big, F32, 2)).to(F16)
+        b = br.normal((2, 30, r), 0.3, F16, 3)
         index = torch.arange(6).int() % 2
         got = run(x, index, a, b, out=F32)
         want, far = br.lora(x, index, a, b)

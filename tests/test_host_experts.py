@@ -90,7 +90,7 @@ REFUSED = [
     ("lora", dict(ldx=63), INVALID), ("lora", dict(ldb=31), INVALID), ("lora", dict(ldy=31), INVALID), ("lora", dict(a_ld=63), INVALID),
     ("lora", dict(b_ld=15), INVALID), ("lora", dict(a_stride=63), INVALID), ("lora", dict(b_stride=15), INVALID),
     ("lora", dict(a_ld=FAR), INVALID), ("lora", dict(b_stride=FAR), INVALID), ("lora", dict(ldx=FAR), INVALID),
-    ("lora", dict(x=P + 1), INVALID), ("lora", dict(a=P + 1), INVALID), ("lora", dict(b=P + 1), INVALID), ("lora", dict(scale=P + 2), INVALID),
+    ("lora", dict(y=P), INVALID), ("lora", dict(x=P + 1), INVALID), ("lora", dict(a=P + 1), INVALID), ("lora", dict(b=P + 1), INVALID), ("lora", dict(scale=P + 2), INVALID),
     ("lora", dict(index=P + 1), INVALID), ("lora", dict(y=P, base=P, ldy=40), INVALID), ("lora", dict(workspace=P, workspace_bytes=16), INVALID),
     ("lora", dict(workspace=P + 4, workspace_bytes=1 << 30), INVALID),
 ]
@@ -114,7 +114,7 @@ TAKEN = [
     ("moe", dict(E=4096, topk=64, x_dtype=gt.F16, out_dtype=gt.F32)), ("moe", dict(workspace=P, workspace_bytes=1 << 26)),
     ("moe", dict(gate_up_ld=8 * 64, gate_up_stride=64)), ("moe", dict(format=0, gate_up=P + 1, down=P + 3)),
     ("moe", dict(gate_up_scales=None, down_scales=None)),
-    ("lora", {}), ("lora", dict(base=None, scale=None)), ("lora", dict(base=P, y=P)), ("lora", dict(M=0, x=None, y=None)),
+    ("lora", {}), ("lora", dict(base=None, scale=None)), ("lora", dict(base=2 * P, y=2 * P)), ("lora", dict(M=0, x=None, y=None)),
     ("lora", dict(N=0, b=None, y=None)), ("lora", dict(rank=0, a=None, b=None)), ("lora", dict(K=0, x=None)),
     ("lora", dict(adapters=0, a=None, b=None)), ("lora", dict(adapters=4096, rank=256)), ("lora", dict(workspace=P, workspace_bytes=1 << 26)),
 ]
