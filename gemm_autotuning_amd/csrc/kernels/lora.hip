@@ -14,6 +14,7 @@ struct ExpandParams {
   const float* mid;  // slice s, row m, rank r at (s * M + m) * ld + r
   int64_t ld, slice;
   int slices, blocks, blocks_each;  // blocks of 64 columns; of a wave
+  int parts_lg;                     // a tile of the table is 2^parts_lg of 16 rows
 };
 
 __device__ __forceinline__ float wave_sum(float v) {
@@ -38,11 +39,16 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(ExpandParams p) {
   const gt::LoraArgs& a = p.a;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, kq = lane >> 4;
-  if ((int)blockIdx.y >= p.table->tiles) return;
-  if (tid < 2 + 16) reinterpret_cast<int*>(&tile)[tid] = reinterpret_cast<const int*>(&p.table->tile[blockIdx.y])[tid];
+  const int t = blockIdx.y >> p.parts_lg, row0 = 16 * (blockIdx.y - (t << p.parts_lg));
+  if (t >= p.table->tiles) return;
+  const RowTile& whole_tile = p.table->tile[t];
+  if (tid < 16) tile.rows[tid] = whole_tile.rows[row0 + tid];
+  if (tid == 16) tile.matrix = whole_tile.matrix;
+  if (tid == 17) tile.count = whole_tile.count;
   __syncthreads();
   const int matrix = __builtin_amdgcn_readfirstlane(tile.matrix);
-  const int rows = __builtin_amdgcn_readfirstlane(tile.count);
+  const int rows = min(__builtin_amdgcn_readfirstlane(tile.count) - row0, 16);
+  if (rows <= 0) return;
   const bool some = matrix < a.adapters;
   const int block0 = (blockIdx.x * 4 + wave) * p.blocks_each, block1 = min(block0 + p.blocks_each, p.blocks);
 
@@ -209,6 +215,84 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(ExpandParams p) {
   }
 }
 
+// The first product of many rows: a workgroup to a tile of 64 rows and a slice
+// of K, of which it takes 128 a step, the rows' and the matrix' pieces in LDS (two
+// buffers in turn) and four steps of them in flight in registers.  Its waves
+// are four blocks of 16 rows times two halves of the rank.  Against tiles of 16
+// (grouped.h) the matrix is read a quarter as often: 4096 rows 4096 long, rank
+// 32, 11.8 us for 34 MB where those take 17.9, of which the table's read, the
+// rows' first load and the launch are some 6.
+template <int XT, int C>
+__global__ __launch_bounds__(512, 2) void lora_many_kernel(gt::LoraArgs a, const RowTable* table, float* mid, int64_t ld, int64_t slice_ld,
+                                                           int split) {
+  typedef W4Rows<XT> Op;
+  constexpr int kPitch = 272, kAhead = 4, kLoads = 2 + C;
+  __shared__ RowTile tile;
+  __shared__ alignas(16) char lds[2][(64 + 32 * C) * kPitch];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = lane & 15, kq = lane >> 4, K = (int)a.K;
+  if ((int)blockIdx.y >= table->tiles) return;
+  if (tid < 2 + 64) reinterpret_cast<int*>(&tile)[tid] = reinterpret_cast<const int*>(&table->tile[blockIdx.y])[tid];
+  __syncthreads();
+  const int matrix = __builtin_amdgcn_readfirstlane(tile.matrix), rows = __builtin_amdgcn_readfirstlane(tile.count);
+  if (matrix >= a.adapters) return;
+  const int units = (K + 127) / 128, each = units / split, rest = units - each * split, slice = blockIdx.x;
+  const int first = slice * each + min(slice, rest), steps = each + (slice < rest);
+  // a piece is 16 bytes: of rows tid / 16 and 32 more, of the matrix' rows likewise
+  const char* from[kLoads];
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i)
+    from[i] = i < 2 ? static_cast<const char*>(a.x) + tile.rows[min(tid / 16 + 32 * i, rows - 1)] * a.ldx * 2
+                    : a.a.p + matrix * a.a.stride + min(tid / 16 + 32 * (i - 2), a.rank - 1) * a.a.ld;
+  u32x4 ring[kAhead][kLoads];
+  auto load = [&](int step, u32x4 (&v)[kLoads]) __attribute__((always_inline)) {
+    const int k = (first + min(step, steps - 1)) * 128 + 8 * (tid & 15);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) v[i] = *reinterpret_cast<const u32x4_any*>(from[i] + 2 * min(k, K - 8));
+  };
+  auto place = [&](int step, u32x4 (&v)[kLoads], char* at) __attribute__((always_inline)) {
+    const int k0 = (first + step) * 128, k = k0 + 8 * (tid & 15);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      if (k0 + 128 > K) v[i] = bytes_from(v[i], min(max(0, 2 * (k - (K - 8))), 16));
+      *reinterpret_cast<u32x4*>(at + (tid / 16 + 32 * i) * kPitch + 16 * (tid & 15)) = v[i];
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) load(i, ring[i]);
+  const int block = wave & 3, half = wave >> 2;
+  f32x4 acc[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) acc[c] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+  for (int n = 0; n < steps; n += kAhead)
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (n + i >= steps) break;
+      char* const at = lds[i & 1];
+      place(n + i, ring[i], at);
+      load(n + i + kAhead, ring[i]);
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        Chunk x, w;
+        __builtin_memcpy(&x, at + (16 * block + r) * kPitch + 64 * j + 16 * kq, 16);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          __builtin_memcpy(&w, at + (64 + 16 * (C * half + c) + r) * kPitch + 64 * j + 16 * kq, 16);
+          Op::mma(acc[c], x, w);
+        }
+      }
+    }
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int m = 16 * block + 4 * kq + e, n = 16 * (C * half + c) + r;
+      if (m < rows && n < a.rank) mid[slice * slice_ld + tile.rows[m] * ld + n] = acc[c][e];
+    }
+}
+
 constexpr int kFewThreads = 1024;
 
 // A few rows of small adapters in one launch: every workgroup computes its row's
@@ -344,9 +428,9 @@ struct LoraCut {
   gtk::GroupedCut c;
   int units, split;
 };
-LoraCut cut(const LoraArgs& a, int64_t rows) {
+LoraCut cut(const LoraArgs& a) {
   LoraCut l;
-  const int64_t tiles = most_tiles(rows, a.adapters);
+  const int64_t tiles = most_tiles(a.M, a.adapters);
   l.units = (int)((a.K + 127) / 128);
   const int pairs = (a.rank + 31) / 32;
   const int64_t want = (int64_t)1 << (bits_of((int)std::min<int64_t>(std::max<int64_t>(1, 8 * a.cus / (tiles * pairs)), 16)) - 1);
@@ -359,15 +443,28 @@ LoraCut cut(const LoraArgs& a, int64_t rows) {
   l.c.waves = 8;
   return l;
 }
+// Whether the first product takes tiles of 64 rows: where an adapter has some
+// 256 of them and all together fill the CUs.  4096 long, rank 32, 4096 rows of 6
+// adapters 38.4 us and 42.3, rank 64 49 and 66, 2048 rows 36.0 and 38.5; 1024 rows
+// of 8 adapters 22 and 18.7, 4096 of 64 adapters 51 and 47.
+bool many_rows(const LoraArgs& a) {
+  return a.K >= 8 && a.rank >= 8 && a.rank <= 64 && a.M >= 2048 && a.M >= 256 * (int64_t)a.adapters;
+}
+// Its slices: two workgroups to a CU, of two units at least (a power of two, as above).
+int many_split(const LoraArgs& a) {
+  const int64_t want = 2 * a.cus / most_tiles(a.M, a.adapters, 64), units = (a.K + 127) / 128;
+  return 1 << (bits_of((int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, 16), units / 2))) - 1);
+}
 struct LoraSpace {
   int64_t ld;
   size_t mid, bytes;
 };
-LoraSpace space(const LoraArgs& a, int64_t rows) {
+LoraSpace space(LoraArgs a, int64_t rows) {
   LoraSpace s;
+  a.M = rows;
   s.ld = (a.rank + 3) / 4 * 4;
   s.mid = gtk::row_table_bytes(most_tiles(rows, a.adapters + 1));
-  s.bytes = s.mid + (size_t)cut(a, rows).split * rows * s.ld * 4;
+  s.bytes = s.mid + (size_t)(many_rows(a) ? many_split(a) : cut(a).split) * rows * s.ld * 4;
   return s;
 }
 
@@ -417,18 +514,33 @@ int launch_lora(const LoraArgs& a) {
   }
   const LoraSpace s = space(a, a.M);
   const int none = a.base != a.y;
-  const int64_t tiles = most_tiles(a.M, a.adapters + none);
+  const bool many = many_rows(a);
+  const int64_t tiles = most_tiles(a.M, a.adapters + none, many ? 64 : 16);
   gtk::RowTable* table = reinterpret_cast<gtk::RowTable*>(a.ws);
   float* mid = reinterpret_cast<float*>(a.ws + s.mid);
-  const gtk::RowIndex ix{a.index, 1, (int)a.M, 1, a.adapters, 1u << 20, none, bits_of(a.adapters - 1 + none), 4};
+  const gtk::RowIndex ix{a.index, 1, (int)a.M, 1, a.adapters, 1u << 20, none, bits_of(a.adapters - 1 + none), many ? 6 : 4};
   int split = 1;
   const bool units = in_units(a);
   if (!units || a.M > gtk::kFewRows) {
     const int rc = launch_row_tiles(ix, table, a.stream);
     if (rc != LS_OK) return rc;
   }
-  if (units) {
-    const LoraCut l = cut(a, a.M);
+  if (many) {
+    split = many_split(a);
+    const dim3 grid((unsigned)split, (unsigned)tiles);
+    if (a.x_dtype == DT_BF16) {
+      if (a.rank <= 32)
+        hipLaunchKernelGGL((gtk::lora_many_kernel<DT_BF16, 1>), grid, dim3(512), 0, a.stream, a, table, mid, s.ld, a.M * s.ld, split);
+      else
+        hipLaunchKernelGGL((gtk::lora_many_kernel<DT_BF16, 2>), grid, dim3(512), 0, a.stream, a, table, mid, s.ld, a.M * s.ld, split);
+    } else {
+      if (a.rank <= 32)
+        hipLaunchKernelGGL((gtk::lora_many_kernel<DT_F16, 1>), grid, dim3(512), 0, a.stream, a, table, mid, s.ld, a.M * s.ld, split);
+      else
+        hipLaunchKernelGGL((gtk::lora_many_kernel<DT_F16, 2>), grid, dim3(512), 0, a.stream, a, table, mid, s.ld, a.M * s.ld, split);
+    }
+  } else if (units) {
+    const LoraCut l = cut(a);
     split = l.split;
     gtk::GroupedParams p{};
     p.ix = ix;
@@ -450,10 +562,10 @@ int launch_lora(const LoraArgs& a) {
   } else {
     hipLaunchKernelGGL(gtk::lora_shrink_kernel, dim3(at_most(a.M, 65536), (a.rank + 3) / 4), dim3(256), 0, a.stream, a, mid, s.ld);
   }
-  gtk::ExpandParams e{a, table, mid, s.ld, a.M * s.ld, split, (int)((a.N + 63) / 64), 1};
-  const int64_t groups = (e.blocks + 3) / 4;
-  e.blocks_each = (int)std::max<int64_t>(1, std::min<int64_t>(16, groups * tiles / (4 * a.cus)));
-  const dim3 grid((unsigned)((e.blocks + 4 * e.blocks_each - 1) / (4 * e.blocks_each)), (unsigned)tiles);
+  gtk::ExpandParams e{a, table, mid, s.ld, a.M * s.ld, split, (int)((a.N + 63) / 64), 1, many ? 2 : 0};
+  const int64_t groups = (e.blocks + 3) / 4, parts = many ? 4 * tiles : tiles;
+  e.blocks_each = (int)std::max<int64_t>(1, std::min<int64_t>(16, groups * parts / (4 * a.cus)));
+  const dim3 grid((unsigned)((e.blocks + 4 * e.blocks_each - 1) / (4 * e.blocks_each)), (unsigned)parts);
   return a.x_dtype == DT_BF16 ? expand<DT_BF16>(e, grid) : expand<DT_F16>(e, grid);
 }
 

@@ -84,6 +84,15 @@ def test_ranks_of_many_rows(r):
     same(700, 7, r, 72, 40, BF if r % 2 else F16, out=F32 if r > 8 else None, pad=r % 4, spread=r > 4, seed=r)
 
 
+@pytest.mark.parametrize("r,K,N", [(8, 8, 5), (9, 130, 64), (16, 100, 70), (31, 257, 33), (32, 1290, 65), (33, 128, 100), (40, 31, 9),
+                                   (64, 600, 130)])
+def test_thousands_of_rows(r, K, N):
+    M = 2100
+    runs = torch.div(torch.arange(M), 300, rounding_mode="floor").int() - 1
+    same(M, 8 if K < 100 else 5, r, K, N, BF if r % 2 else F16, out=F32 if r > 16 else None, pad=r % 4, spread=r > 16, seed=r,
+         index=runs if r % 3 else None, in_place=r == 32)
+
+
 @pytest.mark.parametrize("K", [8, 9, 31, 100, 127, 128, 129, 300, 1000, 2050])
 def test_lengths_of_wide_results(K):
     same(90, 7, 16, K, 2100, F16 if K % 2 else BF, out=F32, pad=K % 2, spread=K > 128, seed=K)
@@ -185,7 +194,8 @@ def test_nothing_to_add(none):
 
 
 @pytest.mark.parametrize("M,L,r,K", [(1, 1, 16, 4096), (3, 2, 40, 9000), (500, 1, 8, 5000), (4096, 3, 16, 256), (4097, 1, 16, 4096), (4596, 1, 16, 8192),
-                                     (9000, 9, 12, 2000), (5, 2, 7, 4)])
+                                     (9000, 9, 12, 2000), (5, 2, 7, 4), (4096 + 2047, 2, 64, 4000),
+                                     (4096 + 200, 3, 40, 9000), (2048, 1, 8, 3000)])
 def test_the_callers_workspace_is_enough_and_not_left(M, L, r, K):
     g = ref.rng(M)
     x = torch.randint(-1, 2, (M, K), generator=g).to(BF)
