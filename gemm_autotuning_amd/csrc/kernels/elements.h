@@ -172,5 +172,10 @@ __device__ __forceinline__ uint32_t wave_join(uint32_t v, F f) {
   const auto h = __builtin_amdgcn_permlane32_swap(v, v, false, false);
   return f(h[0], h[1]);
 }
+__device__ __forceinline__ float wave_sum(float v) {
+  return __uint_as_float(wave_join(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+    return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+  }));
+}
 
 }  // namespace gtk

@@ -7,12 +7,6 @@
 
 namespace gtk {
 
-__device__ __forceinline__ float wave_sum(float v) {
-  return __uint_as_float(wave_join(__float_as_uint(v), [](uint32_t a, uint32_t b) {
-    return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
-  }));
-}
-
 // Weight (e, n, k) as a float.
 __device__ __forceinline__ float expert_weight(const gt::ExpertWeights& w, int64_t e, int64_t n, int64_t k, int dtype, int format,
                                                int scale_dtype, int group_lg) {

@@ -27,12 +27,6 @@ namespace {
 
 constexpr int kRows = 8;  // of weights, to a workgroup
 
-__device__ __forceinline__ float wave_sum(float v) {
-  return __uint_as_float(wave_join(__float_as_uint(v), [](uint32_t a, uint32_t b) {
-    return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
-  }));
-}
-
 // The eight weights of a dword of codes: e2m1 as they are, integers as
 // sixteenths (the conversion's own unit).
 template <int FMT>

@@ -3,10 +3,10 @@
 //
 //   out[row, n] = sum_k x[row, k] * w[of(row), n, k]
 //
-// Rows that name the same matrix form tiles of 16.  The weights are read once
+// Rows that name the same matrix form tiles of 16 (grouped_wide.h: 64).  The weights are read once
 // per tile and bound the time; everything is arranged around that stream, as
 // for the rows times shared 4-bit weights (w4_mma.h).  A wave owns a slice of
-// K, U units of 256 bytes of a 16-bit row (128 or 64 of a 4-bit one), keeps
+// K, U units of 256 bytes of a 16-bit row (128 of a 4-bit one), keeps
 // the rows' slice in registers as operands of 16x16x32 matrix-core blocks,
 // and walks pairs of tiles of 16 columns with D units of weights in flight.
 // A unit's load has neighbouring lanes on consecutive bytes of a column and is
@@ -393,7 +393,7 @@ struct PairWeights {
 // BYTES: a unit's of a column; G: a group's k and WIDE: its scale is fp32 (4
 // bits); ONE: the slices are loaded once a tile (K in one turn); W: waves.
 template <int PHASE, int XT, int FMT, int BYTES, int G, int WIDE, int U, int D, int B, int W, bool ONE>
-__global__ __launch_bounds__(64 * W, W > 8 ? 4 : 2) void grouped_kernel(GroupedParams p) {
+__global__ __launch_bounds__(64 * W, 2) void grouped_kernel(GroupedParams p) {
   typedef UnitOf<FMT, BYTES> Unit;
   typedef PairWeights<PHASE, FMT, BYTES, G, WIDE> Weights;
   typedef W4Operand<XT, FMT == GROUPED_16 ? W4_E2M1 : FMT> Op;  // e2m1: elements in order

@@ -17,12 +17,6 @@ struct ExpandParams {
   int parts_lg;                     // a tile of the table is 2^parts_lg of 16 rows
 };
 
-__device__ __forceinline__ float wave_sum(float v) {
-  return __uint_as_float(wave_join(__float_as_uint(v), [](uint32_t a, uint32_t b) {
-    return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
-  }));
-}
-
 // The second product: a wave holds the tile's 16 rows of up to 32 R values as
 // operands in two 16-bit parts and walks blocks of 64 columns, whose weights
 // (64 rows of the rank) and base it loads a block ahead.  What bounds it is

@@ -438,12 +438,13 @@ typedef enum gt_activation { GT_ACT_SILU = 0, GT_ACT_GELU = 1 /* its tanh form *
  * tokens whose intermediate values take about 64 MiB, but a prompt's rows
  * belong in one product per expert.
  *
- * The intermediate values take gt_moe_workspace bytes of device memory: the
- * caller's workspace (16-byte aligned), or, where that is NULL, the stream's,
- * which the first (largest) call allocates: make that call outside stream
- * capture.  Calls and graph replays that overlap in time must not share a
- * workspace: graphs captured on one stream and replayed on several need the
- * caller's, one each. */
+ * The intermediate values take gt_moe_workspace bytes of device memory (fewer
+ * tokens may take more than many, whose sums are cut into fewer slices: ask
+ * for each M): the caller's workspace (16-byte aligned), or, where that is
+ * NULL, the stream's, which a call that needs more than those before
+ * allocates: make one of the same sizes outside stream capture first.  Calls
+ * and graph replays that overlap in time must not share a workspace: graphs
+ * captured on one stream and replayed on several need the caller's, one each. */
 typedef struct gt_moe_desc {
   const void* x;              /* M x K, ldx                                  */
   const int32_t* index;       /* M x topk, ldi                               */
