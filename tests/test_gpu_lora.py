@@ -183,6 +183,25 @@ def test_many_rows():
         assert torch.equal(run(x, index, a, b, out=F32).double(), want)
 
 
+@pytest.mark.parametrize("r,L,out,base", [(8, 3, F32, True), (40, 90, BF, True), (130, 5, F32, False), (3, 4, F16, True), (200, 3, F32, True)])
+def test_results_past_the_caches(r, L, out, base):
+    M, K, N = 2300, 72, 5001
+    g = ref.rng(r)
+    dt = F16 if out == F16 else BF
+    x, a = torch.randint(-1, 2, (M, K), generator=g).to(dt), torch.randint(-1, 2, (L, r, K), generator=g).to(dt)
+    b = torch.randint(-1, 2, (L, N, r), generator=g).to(dt)
+    b[:, :, 2:] = 0  # sums that 8 bits hold
+    a[:, :, 30:] = 0
+    bs = torch.randint(-40, 41, (M, N), generator=g).to(out) if base else None
+    index = torch.randint(-1, L, (M,), generator=g, dtype=torch.int32)
+    want = bs.double() if base else torch.zeros(M, N, dtype=torch.float64)
+    for e in range(L):
+        m = index == e
+        want[m] += (x[m].double() @ a[e].double().t()) @ b[e].double().t()
+    assert want.abs().max() < 256
+    assert torch.equal(run(x, index, a, b, base=bs, out=out, pad=5).double(), want)
+
+
 @pytest.mark.parametrize("none", ["K", "adapters", "rank"])
 def test_nothing_to_add(none):
     M, L, r, K, N = 5, 2, 4, 32, 33
