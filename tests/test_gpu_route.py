@@ -65,18 +65,20 @@ def test_masks(E, k, score):
             same(logits, k, score, normalise)
 
 
-def test_ties_go_to_the_lowest_index():
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_ties_go_to_the_lowest_index(dtype):
     for E in (10, 64, 100, 256, 1000):
         logits = torch.zeros(5, E)
         logits[1, 1::2] = -0.0  # the same number
         logits[2, E // 2:] = 1.0
         logits[3] = torch.arange(E) % 3
         logits[4] = torch.arange(E) // 2
-        same(logits, min(E, 16))
+        same(logits.to(ref.DT[dtype]), min(E, 16))
 
 
-def test_nan_and_infinity():
-    logits = torch.randn(6, 50, generator=ref.rng(1))
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_nan_and_infinity(dtype):
+    logits = torch.randn(6, 50, generator=ref.rng(1)).to(ref.DT[dtype])
     logits[0, 7] = math.nan
     logits[1, 7], logits[1, 30] = -math.nan, math.nan
     logits[2, 9] = math.inf
