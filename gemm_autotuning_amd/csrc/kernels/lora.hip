@@ -1,10 +1,12 @@
 // lora.hip -- adapters of many requests beside a shared projection: the first
 // product of each row (grouped.h, slices of K to workgroups where the rows are
 // few) into fp32 values, then the second one, which adds the slices, and the
-// base to its results; few rows of small adapters in one launch.
+// base to its results; few rows of small adapters in one launch; the first
+// product row by row, or in tiles of 64 rows, where that is less.
 #include "elements.h"
 #include "grouped.h"
 #include "launchers.h"
+#include "row_tiles.h"
 
 namespace gtk {
 
@@ -387,6 +389,57 @@ __global__ __launch_bounds__(kFewThreads) void lora_few_kernel(gt::LoraArgs a) {
   store_out(a.y, m * a.ldy + n, base + (a.scale ? a.scale[e] : 1.f) * v, a.out_dtype);
 }
 
+// The first product of rows whose adapters' matrices are small altogether,
+// row by row, and beside it, in the first workgroup, the tiles' table for the
+// second: 16 values of a row to a workgroup, eight waves along K times two of
+// eight values.  A chain of waits (the adapter's number, its weights, a barrier):
+// 48 rows of 64 adapters rank 64, 4096 long, 7.1 us for 25 MB, most of it waits.
+template <int XT>
+__global__ __launch_bounds__(1024) void lora_dot_kernel(gt::LoraArgs a, RowIndex ix, RowTable* table, float* mid, int64_t ld) {
+  constexpr int kRows = 8, kAlong = 8;
+  __shared__ float sums[kAlong][2 * kRows];
+  if (blockIdx.x == 0) {
+    make_row_table(ix, table);
+    return;
+  }
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), K = (int)a.K;
+  const int groups = (a.rank + 2 * kRows - 1) / (2 * kRows), m = (blockIdx.x - 1) / groups;
+  const int first = ((int)blockIdx.x - 1 - m * groups) * 2 * kRows, r0 = first + wave % 2 * kRows;
+  const int e = a.index[m];
+  if (e < 0 || e >= a.adapters) return;
+  const uint16_t* const x = static_cast<const uint16_t*>(a.x) + m * a.ldx;
+  const char* const w = a.a.p + e * a.a.stride;
+  float acc[kRows] = {};
+  for (int k0 = 512 * (wave / 2); k0 < K; k0 += 512 * kAlong) {
+    const int k = k0 + 8 * lane, at = min(k, K - 8);
+    u32x4 v = *reinterpret_cast<const u32x4_any*>(x + at), q[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i)
+      q[i] = *reinterpret_cast<const u32x4_any*>(w + (int64_t)min(r0 + i, a.rank - 1) * a.a.ld + 2 * at);
+    if (k0 + 512 > K) {  // what lies past the end becomes zero
+      v = bytes_from(v, min(2 * (k - at), 16));
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) q[i] = bytes_from(q[i], min(2 * (k - at), 16));
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[i] = fmaf(half_to_f32<XT>(q[i][j / 2], j & 1), half_to_f32<XT>(v[j / 2], j & 1), acc[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const float v = wave_sum(acc[i]);
+    if (lane == 0) sums[wave / 2][wave % 2 * kRows + i] = v;
+  }
+  __syncthreads();
+  if (tid < 2 * kRows && first + tid < a.rank) {
+    float v = 0.f;
+#pragma unroll
+    for (int i = 0; i < kAlong; ++i) v += sums[i][tid];
+    mid[m * ld + first + tid] = v;
+  }
+}
+
 // Rows of x or of the adapters' first matrices too short for a lane's 16
 // bytes, or the latter so far apart that a tile's offsets pass 32 bits: a wave
 // to a value.
@@ -464,6 +517,15 @@ int many_split(const LoraArgs& a) {
   const int64_t want = 2 * a.cus / most_tiles(a.M, a.adapters, 64), units = (a.K + 127) / 128;
   return 1 << (bits_of((int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, 16), units / 2))) - 1);
 }
+// Whether the first product goes row by row, which spares the table's launch
+// or its search: two workgroups of 4096 long rows to a CU at most (short rows
+// count as 2048).  48 rows of 64 adapters rank 64, 4096 x 16384, 24.5 us and
+// 26.5 with tiles; rank 16, 4096 x 4096, 512 rows 13.3 and 16.2, 1024 rows (1024
+// workgroups) 19.2 and 18.6; 1000 rows 1024 long 14.6 and 18.5; 277 rows of rank
+// 34 2945 long (831) 18.0 and 17.4.
+bool row_by_row(const LoraArgs& a) {
+  return a.K >= 8 && a.M * ((a.rank + 15) / 16) * std::max<int64_t>(a.K, 2048) <= (int64_t)8192 * a.cus;
+}
 struct LoraSpace {
   int64_t ld;
   size_t mid, bytes;
@@ -538,11 +600,18 @@ int launch_lora(const LoraArgs& a) {
   const gtk::RowIndex ix{a.index, 1, (int)a.M, 1, a.adapters, 1u << 20, none, bits_of(a.adapters - 1 + none), many ? 6 : 4};
   int split = 1;
   const bool units = in_units(a);
-  if (!units || a.M > gtk::kFewRows) {
+  const bool dots = row_by_row(a);
+  if (!dots && (!units || a.M > gtk::kFewRows)) {
     const int rc = launch_row_tiles(ix, table, a.stream);
     if (rc != LS_OK) return rc;
   }
-  if (many) {
+  if (dots) {
+    const dim3 grid((unsigned)(1 + a.M * ((a.rank + 15) / 16)));
+    if (a.x_dtype == DT_BF16)
+      hipLaunchKernelGGL((gtk::lora_dot_kernel<DT_BF16>), grid, dim3(1024), 0, a.stream, a, ix, table, mid, s.ld);
+    else
+      hipLaunchKernelGGL((gtk::lora_dot_kernel<DT_F16>), grid, dim3(1024), 0, a.stream, a, ix, table, mid, s.ld);
+  } else if (many) {
     split = many_split(a);
     const dim3 grid((unsigned)split, (unsigned)tiles);
     if (a.x_dtype == DT_BF16) {

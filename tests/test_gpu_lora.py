@@ -81,7 +81,24 @@ def test_columns(N):
 
 @pytest.mark.parametrize("r", [1, 4, 7, 8, 9, 15, 16, 17, 24, 31, 32])
 def test_ranks_of_many_rows(r):
-    same(700, 7, r, 72, 40, BF if r % 2 else F16, out=F32 if r > 8 else None, pad=r % 4, spread=r > 4, seed=r)
+    for M in (700, 1100):
+        same(M, 7, r, 72, 40, BF if r % 2 else F16, out=F32 if r > 8 else None, pad=r % 4, spread=r > 4, seed=r)
+
+
+@pytest.mark.parametrize("r", [130, 200, 256])
+@pytest.mark.parametrize("K", [8, 31, 100, 129, 1000, 2051])
+def test_lengths_of_high_ranks(r, K):
+    same(128, 5, r, K, 33, F16 if K % 2 else BF, out=F32, pad=K % 2, spread=K > 100, seed=K)
+
+
+@pytest.mark.parametrize("K", [8, 9, 31, 100, 127, 128, 129, 300, 1000, 2050])
+def test_lengths_of_many_rows(K):
+    same(1100, 9, 20, K, 30, F16 if K % 2 else BF, out=F32, pad=K % 2, spread=K > 128, seed=K)
+
+
+def test_long_rows_of_a_batch():
+    same(64, 6, 64, 16500, 70, BF, out=F32, seed=1)
+    same(24, 6, 100, 20001, 70, F16, out=F32, seed=2, spread=True)
 
 
 @pytest.mark.parametrize("r,K,N", [(8, 8, 5), (9, 130, 64), (16, 100, 70), (31, 257, 33), (32, 1290, 65), (33, 128, 100), (40, 31, 9),
