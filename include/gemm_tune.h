@@ -491,8 +491,8 @@ gt_status gt_moe_workspace(const gt_moe_desc* d, int64_t* bytes);
  * row without an adapter (an index outside 0..adapters-1) is left as base, not
  * written at all in place.  Sums and what passes between the products are
  * fp32 (two 16-bit parts of it in the second, as gt_moe); y is rounded once.
- * An adapter's weights are read once for up to 16 of its rows.  Workspace as
- * gt_moe. */
+ * An adapter's b is read once for up to 16 of its rows, its a once a row or, in
+ * larger calls, for up to 16 or 64 rows.  Workspace as gt_moe. */
 typedef struct gt_lora_desc {
   const void* x;        /* M x K, ldx                                        */
   const int32_t* index; /* M                                                 */
