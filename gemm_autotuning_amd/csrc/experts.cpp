@@ -73,8 +73,10 @@ gt_status matrix_scales(const void* p, int64_t E, int64_t N, int64_t groups, int
   w->scales = p;
   w->s_ldn = ldn > 0 ? ldn : std::max<int64_t>(groups, 1);
   w->s_ldg = ldg > 0 ? ldg : 1;
-  if (w->s_ldn > INT64_MAX / 16 / std::max<int64_t>(N, 1)) return invalid(std::string(what) + " spans more than 64-bit offsets");
-  w->s_lde = lde > 0 ? lde : N * w->s_ldn;
+  if (w->s_ldn > INT64_MAX / 16 / std::max<int64_t>(N, 1) || w->s_ldg > INT64_MAX / 16 / std::max<int64_t>(groups, 1))
+    return invalid(std::string(what) + " spans more than 64-bit offsets");
+  // one matrix after another, whether its rows or its groups lie further apart
+  w->s_lde = lde > 0 ? lde : std::max(N * w->s_ldn, groups * w->s_ldg);
   if (E == 0 || N == 0 || groups == 0) return GT_OK;
   GT_CHECK(operand(p, true, N, w->s_ldn, elem_bytes(dtype), what));
   GT_CHECK(operand(p, true, groups, w->s_ldg, 1, what));

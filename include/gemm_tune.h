@@ -462,7 +462,8 @@ typedef struct gt_moe_desc {
   int64_t ldx, ldi, ldw, ldb, ldy;
   int64_t gate_up_ld, gate_up_stride; /* of rows and of experts, in elements */
   int64_t down_ld, down_stride;       /* (4 bits: bytes); <= 0: dense        */
-  int64_t gate_up_scale_lde, gate_up_scale_ldn, gate_up_scale_ldg; /* elements; <= 0: dense */
+  int64_t gate_up_scale_lde, gate_up_scale_ldn, gate_up_scale_ldg; /* elements; <= 0: _ldn the groups of a row, _ldg 1,
+                                 _lde rows * _ldn or, if that is more, groups * _ldg */
   int64_t down_scale_lde, down_scale_ldn, down_scale_ldg;
   int32_t x_dtype;     /* f16, bf16: x, and 16-bit weights                   */
   int32_t out_dtype;   /* f32, f16, bf16; -1: x_dtype                        */
