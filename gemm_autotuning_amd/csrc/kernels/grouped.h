@@ -500,7 +500,8 @@ __global__ __launch_bounds__(64 * W, 2) void grouped_kernel(GroupedParams p) {
             }
           }
           if constexpr (kScaled) {
-            // a power of two that brings the row's largest of this slice to 2^14..2^15; 1 for infinities and NaN
+            // a power of two that brings the row's largest of this slice to 2^14..2^15; beside an infinity or
+            // NaN 2^-114, under which no finite value becomes one
             auto largest = [](uint32_t a, uint32_t b) { return max(a, b); };
             most = largest(most, dpp<0xB1>(most));
             most = largest(most, dpp<0x4E>(most));
@@ -509,7 +510,7 @@ __global__ __launch_bounds__(64 * W, 2) void grouped_kernel(GroupedParams p) {
             const auto both = __builtin_amdgcn_permlane16_swap(most, most, false, false);
             most = largest(both[0], both[1]);
             const uint32_t ex = most >> 23;
-            const uint32_t to = ex == 255 || ex == 0 ? 127u : min(253u, 268u - ex);
+            const uint32_t to = ex == 0 ? 127u : min(253u, 268u - ex);
             if ((lane & 31) == 0) unscale[wave][2 * i + (lane >> 5)] = __uint_as_float((254u - to) << 23);
             const float s = __uint_as_float(to << 23);
 #pragma unroll

@@ -120,7 +120,7 @@ __global__ __launch_bounds__(512, 2) void grouped_wide_kernel(GroupedParams p) {
       most = max(most, dpp<0xB1>(most));
       most = max(most, dpp<0x4E>(most));
       most = max(most, dpp<0x141>(most));
-      const uint32_t ex = most >> 23, to = ex == 255 || ex == 0 ? 127u : min(253u, 268u - ex);
+      const uint32_t ex = most >> 23, to = ex == 0 ? 127u : min(253u, 268u - ex);
       scale = __uint_as_float(to << 23);
       if (xc == 0) unscale[xr] = __uint_as_float((254u - to) << 23);
     }

@@ -124,7 +124,7 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(ExpandParams p) {
       const auto both = __builtin_amdgcn_permlane32_swap(most, most, false, false);
       most = max(both[0], both[1]);
       const uint32_t ex = most >> 23;
-      const uint32_t to = ex == 255 || ex == 0 ? 127u : min(253u, 268u - ex);
+      const uint32_t to = ex == 0 ? 127u : min(253u, 268u - ex);
       const float s = __uint_as_float(to << 23);
 #pragma unroll
       for (int j = 0; j < R; ++j)

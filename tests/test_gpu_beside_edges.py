@@ -1,6 +1,8 @@
 """Experts and adapters beside the product at the edges of what their calls
-take: default strides of scales.
+take: default strides of scales, infinities between the products.
 """
+import math
+
 import pytest
 import torch
 
@@ -37,3 +39,39 @@ def test_scales_one_matrix_after_another_by_default(T, first):
     torch.cuda.synchronize()
     want, far = br.moe(x, index, weight, gu, dn, gs, ds, "int4", group)
     ref.check(y.cpu(), want, far, "y")
+
+
+@pytest.mark.parametrize("dtype", [BF, F16])
+@pytest.mark.parametrize("T", [3, 10, 40])
+def test_an_infinite_activation_beside_large_ones(dtype, T):
+    # one row of gate is infinite, the others give values that f16 does not hold: the result is the
+    # infinity, of the sign that down gives it
+    K, H, n = 64, 40, 5
+    x = torch.full((T, K), 16.0).to(dtype)
+    gate_up = torch.full((1, 2 * H, K), 16.0).to(dtype)
+    gate_up[0, n] = math.inf
+    down = torch.ones(1, K, H).to(dtype)
+    down[0, :, n] = -1.0
+    down[0, 1::2] *= -1.0
+    y = torch.empty(T, K, device="cuda")
+    gt.gt_moe(gt.make_moe_desc(x.cuda(), torch.zeros(T, 1, dtype=torch.int32, device="cuda"), torch.ones(T, 1, device="cuda"), gate_up.cuda(),
+                               down.cuda(), y, stream=stream()))
+    torch.cuda.synchronize()
+    assert (y[:, 0::2] == -math.inf).all() and (y[:, 1::2] == math.inf).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F16])
+@pytest.mark.parametrize("M", [2, 40, 2100])
+@pytest.mark.parametrize("r", [12, 40])
+def test_an_infinite_value_of_an_adapter_beside_large_ones(dtype, r, M):
+    K, N = 64, 70
+    x = torch.full((M, K), 64.0).to(dtype)
+    a = torch.full((1, r, K), 64.0).to(dtype)
+    a[0, 3] = math.inf
+    b = torch.ones(1, N, r).to(dtype)
+    b[0, :, 3] = -1.0
+    b[0, 1::2] *= -1.0
+    y = torch.empty(M, N, device="cuda")
+    gt.gt_lora(gt.make_lora_desc(x.cuda(), torch.zeros(M, dtype=torch.int32, device="cuda"), a.cuda(), b.cuda(), y, stream=stream()))
+    torch.cuda.synchronize()
+    assert (y[:, 0::2] == -math.inf).all() and (y[:, 1::2] == math.inf).all()
