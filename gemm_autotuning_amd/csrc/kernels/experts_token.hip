@@ -134,7 +134,7 @@ __global__ __launch_bounds__(512, 4) void token_kernel(gt::MoeArgs a, float* act
           s = __uint_as_float(u.s[i]);
         else
           s = a.scale_dtype == DT_BF16 ? __uint_as_float((uint32_t)u.s[i] << 16) : f16_bits_to_f32(u.s[i]);
-        acc[i] += s * sum;
+        acc[i] += u.k0 < K ? s * sum : 0.f;  // past the end nothing, whatever the last scale is
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[i] = fmaf(half_to_f32<XT>(u.q[i][e / 2], e & 1), x[e], acc[i]);

@@ -1,5 +1,6 @@
 """Experts and adapters beside the product at the edges of what their calls
-take: default strides of scales, infinities between the products.
+take: default strides of scales, infinities between the
+products and in scales.
 """
 import math
 
@@ -75,3 +76,23 @@ def test_an_infinite_value_of_an_adapter_beside_large_ones(dtype, r, M):
     gt.gt_lora(gt.make_lora_desc(x.cuda(), torch.zeros(M, dtype=torch.int32, device="cuda"), a.cuda(), b.cuda(), y, stream=stream()))
     torch.cuda.synchronize()
     assert (y[:, 0::2] == -math.inf).all() and (y[:, 1::2] == math.inf).all()
+
+
+@pytest.mark.parametrize("fmt,scales", [("int4", "f32"), ("e2m1", "bf16")])
+@pytest.mark.parametrize("T", [1, 3, 12])
+@pytest.mark.parametrize("where", ["gate", "down"])
+def test_an_infinite_scale_of_the_last_group(where, T, fmt, scales):
+    # positive codes under it: the results are infinite, and no NaN comes from what lies past the row's end
+    E, K, H, group = 1, 100, 72, 32
+    gu, gs = br.nibbles(E, 2 * H, K, group, scales, 1, codes=[1, 2, 3])
+    dn, ds = br.nibbles(E, K, H, group, scales, 2, codes=[1, 2, 3])
+    if where == "gate":
+        gs[:, :H, -1] = math.inf
+    else:
+        ds[:, :, -1] = math.inf
+    x = (ref.loud(T, K, 3).abs() + 0.5).to(BF)
+    y = torch.empty(T, K, device="cuda")
+    gt.gt_moe(gt.make_moe_desc(x.cuda(), torch.zeros(T, 1, dtype=torch.int32, device="cuda"), torch.ones(T, 1, device="cuda"), gu.cuda(),
+                               dn.cuda(), y, gate_up_scales=gs.cuda(), down_scales=ds.cuda(), format=fmt, group=group, stream=stream()))
+    torch.cuda.synchronize()
+    assert (y == math.inf).all()
