@@ -123,8 +123,11 @@ MoeSpace space(MoeArgs a, int64_t tokens) {
   return s;
 }
 
-GroupedLaunch launcher(const MoeArgs& a) {
-  const bool bf = a.x_dtype == DT_BF16;
+// The down product of 4-bit weights, which are exact in f16, takes the
+// activations as two f16 parts whatever x is: 22 bits of them, where two of bf16
+// have 16 and three more matrix-core work.
+GroupedLaunch launcher(const MoeArgs& a, bool down) {
+  const bool bf = a.x_dtype == DT_BF16 && !(down && a.format >= 0);
   if (a.format == gtk::W4_INT4) return bf ? grouped_bf16_int4 : grouped_f16_int4;
   if (a.format == gtk::W4_E2M1) return bf ? grouped_bf16_e2m1 : grouped_f16_e2m1;
   return bf ? grouped_bf16 : grouped_f16;
@@ -182,6 +185,9 @@ MoeCut cut(const MoeArgs& a, bool down) {
   if (a.format >= 0) {
     c.U = down ? 1 : 2;
     c.waves = 8;
+  } else if (down && a.x_dtype == DT_BF16) {  // three parts: registers for two units
+    c.waves = c.units > 8 ? 8 : 4;
+    c.U = 2;
   } else {
     c.waves = c.units > 16 ? 8 : 4;
     c.U = c.units > 2 * c.waves ? 4 : 2;
@@ -200,7 +206,7 @@ int product(const MoeArgs& a, gtk::GroupedParams& p, int phase, int64_t tiles) {
   const MoeCut c = cut(a, phase == gtk::GROUPED_DOWN);
   fill_cut(p, c, c.units, c.split);
   if (!fill_list(p, tiles, (pairs + c.cols - 1) / c.cols, a.cus)) return LS_UNSUPPORTED;
-  return a.wide ? (a.x_dtype == DT_BF16 ? grouped_wide_bf16 : grouped_wide_f16)(p, phase, a.stream) : launcher(a)(p, phase, c, a.stream);
+  return a.wide ? (a.x_dtype == DT_BF16 ? grouped_wide_bf16 : grouped_wide_f16)(p, phase, a.out_dtype == DT_F32, a.stream) : launcher(a, phase == gtk::GROUPED_DOWN)(p, phase, c, a.stream);
 }
 
 int down_split(const MoeArgs& a) { return cut(a, true).split; }

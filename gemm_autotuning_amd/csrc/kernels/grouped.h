@@ -180,6 +180,34 @@ __device__ __forceinline__ float activated(float g, float u, int activation) {
   return g * __builtin_amdgcn_rcpf(1.f + __expf(-z)) * u;
 }
 
+// An fp32 value as 16-bit operands of the matrix core: take_part takes the
+// next one off it and leaves the rest.  bf16's are cut off, eight bits each, and
+// three of them are all of the value.  f16's are rounded; two leave at most 2^-22
+// of it, or the least subnormal, under a power of two that brings the largest of
+// the values in a sum to 2^14..2^15: row_power, the exponent field of that.
+// Beside an infinity or NaN it is 2^-114, under which no finite value becomes one.
+template <int XT>
+struct ValueParts {
+  static constexpr int n = XT == DT_BF16 ? 3 : 2;
+};
+template <int XT>
+__device__ __forceinline__ uint16_t take_part(float& v) {
+  uint16_t part;
+  float back;
+  if constexpr (XT == DT_BF16) {
+    const uint32_t top = __float_as_uint(v) & 0xffff0000u;
+    part = (uint16_t)(top >> 16);
+    back = __uint_as_float(top);
+  } else {
+    part = f32_to_f16_bits(v);
+    back = f16_bits_to_f32(part);
+  }
+  const float left = v - back;
+  v = left == left ? left : 0.f;  // of an infinity or NaN the first part has it all
+  return part;
+}
+__device__ __forceinline__ uint32_t row_power(uint32_t largest) { return min(253u, 268u - (largest >> 23)); }
+
 // 16 bytes less their first d (d >= 0), zeros behind.
 __device__ __forceinline__ u32x4 bytes_from(u32x4 v, int d) {
   unsigned __int128 w;
@@ -403,8 +431,8 @@ __global__ __launch_bounds__(64 * W, 2) void grouped_kernel(GroupedParams p) {
   constexpr int kGroups = Weights::kGroups;
   // with a group to 128 k a lane takes its 32 of them as they lie, eight to a step; else a step's 32 k are of one group
   constexpr bool kPieces = Unit::k4 && G == 128;
-  constexpr bool kSplit = PHASE == GROUPED_DOWN;  // fp32 rows, in two parts
-  constexpr int kParts = kSplit ? 2 : 1;
+  constexpr bool kSplit = PHASE == GROUPED_DOWN;  // fp32 rows, in parts
+  constexpr int kParts = kSplit ? ValueParts<XT>::n : 1;
   constexpr bool kScaled = kSplit && XT == DT_F16;
   static_assert(ONE || !kScaled, "turns whose rows have scales of their own");
   constexpr int kAll = 2 * U;  // units of a pair
@@ -500,8 +528,7 @@ __global__ __launch_bounds__(64 * W, 2) void grouped_kernel(GroupedParams p) {
             }
           }
           if constexpr (kScaled) {
-            // a power of two that brings the row's largest of this slice to 2^14..2^15; beside an infinity or
-            // NaN 2^-114, under which no finite value becomes one
+            // the row's power of two, of this slice
             auto largest = [](uint32_t a, uint32_t b) { return max(a, b); };
             most = largest(most, dpp<0xB1>(most));
             most = largest(most, dpp<0x4E>(most));
@@ -509,8 +536,7 @@ __global__ __launch_bounds__(64 * W, 2) void grouped_kernel(GroupedParams p) {
             most = largest(most, dpp<0x140>(most));
             const auto both = __builtin_amdgcn_permlane16_swap(most, most, false, false);
             most = largest(both[0], both[1]);
-            const uint32_t ex = most >> 23;
-            const uint32_t to = ex == 0 ? 127u : min(253u, 268u - ex);
+            const uint32_t to = row_power(most);
             if ((lane & 31) == 0) unscale[wave][2 * i + (lane >> 5)] = __uint_as_float((254u - to) << 23);
             const float s = __uint_as_float(to << 23);
 #pragma unroll
@@ -520,7 +546,7 @@ __global__ __launch_bounds__(64 * W, 2) void grouped_kernel(GroupedParams p) {
 #pragma unroll
       for (int un = 0; un < U * Unit::kRowUnits; ++un)
 #pragma unroll
-        for (int part = 0; part < 2; ++part) {
+        for (int part = 0; part < kParts; ++part) {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             if (2 * i < rows) {
@@ -528,18 +554,9 @@ __global__ __launch_bounds__(64 * W, 2) void grouped_kernel(GroupedParams p) {
               uint16_t h[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                float back;
-                if constexpr (XT == DT_BF16) {
-                  // the first part is cut off, not rounded: it cannot pass bf16's range
-                  const uint32_t top = __float_as_uint(v[e]) & 0xffff0000u;
-                  h[e] = part == 0 ? (uint16_t)(top >> 16) : f32_to_bf16_bits(v[e]);
-                  back = __uint_as_float(top);
-                } else {
-                  h[e] = f32_to_f16_bits(v[e]);
-                  back = f16_bits_to_f32(h[e]);
-                }
-                const float left = v[e] - back;
-                v[e] = left == left ? left : 0.f;  // of an infinity or NaN the first part has it all
+                float rest = v[e];
+                h[e] = take_part<XT>(rest);
+                v[e] = rest;
               }
               raw[un][i] = v;
               __builtin_memcpy(st + (2 * i + (lane >> 5)) * 272 + 8 * (lane & 31), h, 8);
@@ -717,14 +734,15 @@ int grouped_sizes(const GroupedParams& p, const GroupedCut& c, hipStream_t strea
   // bytes of a unit, U, D, B, waves, K in one turn
   if constexpr (FMT == GROUPED_16) {
     constexpr int D = PHASE == GROUPED_DOWN ? 2 : 4;
+    constexpr bool kThree = PHASE == GROUPED_DOWN && ValueParts<XT>::n == 3;  // rows' parts: registers for two units
     if constexpr (PHASE == GROUPED_SHRINK) GT_GROUPED(256, 1, 2, 1, 8, true)
     GT_GROUPED(256, 2, 4, 1, 8, true)
-    GT_GROUPED(256, 4, D, 1, 8, true)
+    if constexpr (!kThree) GT_GROUPED(256, 4, D, 1, 8, true)
     if constexpr (PHASE == GROUPED_GATE_UP) GT_GROUPED(256, 4, 4, 2, 8, false)
     if constexpr (PHASE == GROUPED_SHRINK) GT_GROUPED(256, 4, 4, 1, 8, false)
     if constexpr (PHASE != GROUPED_SHRINK) {
       GT_GROUPED(256, 2, 4, 1, 4, true)
-      GT_GROUPED(256, 4, D, 1, 4, true)
+      if constexpr (!kThree) GT_GROUPED(256, 4, D, 1, 4, true)
     }
   } else if constexpr (PHASE == GROUPED_DOWN) {
     GT_GROUPED(128, 1, 2, 2, 8, true)
@@ -757,8 +775,9 @@ int grouped_launch(const GroupedParams& p, int phase, const GroupedCut& c, hipSt
       default: return grouped_sizes<GROUPED_SHRINK, XT, FMT, 128, 0>(p, c, stream);
     }
   } else {
-    return phase == GROUPED_GATE_UP ? grouped_scales<GROUPED_GATE_UP, XT, FMT>(p, c, stream)
-                                    : grouped_scales<GROUPED_DOWN, XT, FMT>(p, c, stream);
+    if (phase == GROUPED_GATE_UP) return grouped_scales<GROUPED_GATE_UP, XT, FMT>(p, c, stream);
+    if constexpr (XT == DT_F16) return grouped_scales<GROUPED_DOWN, XT, FMT>(p, c, stream);  // for either type of x
+    return gt::LS_UNSUPPORTED;
   }
 }
 // One source file per row type and format defines its launcher.

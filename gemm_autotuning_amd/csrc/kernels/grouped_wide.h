@@ -9,7 +9,7 @@
 // is joined.  8 experts 4096 x 2048 bf16, two to a token: 64 tokens 97 us (120
 // with tiles of 16 rows), 256 tokens 159 (299), 512 tokens 274 (582): at 64
 // tokens 402 MB of weights are 4.1 TB/s, at 512 the products' 77 GFLOP (the
-// second one's rows are two parts) and the waits of eight waves for each other
+// second one's rows are parts) and the waits of eight waves for each other
 // bound it.  Halving K between the waves (256 workgroups instead of 128 for
 // the first product) and loading the rows' pieces two steps ahead changed
 // nothing or lost.
@@ -19,14 +19,18 @@
 
 namespace gtk {
 
-template <int PHASE, int XT>
+// PARTS: of an fp32 row's value (ValueParts).  bf16's three are all of it, for an
+// fp32 y; two, 16 bits, are enough below a y that is rounded to 16 bits itself,
+// and save a third of the second product's matrix-core work (256 tokens 159 us and
+// 171 with three, 512 tokens 290 and 310).
+template <int PHASE, int XT, int PARTS>
 __global__ __launch_bounds__(512, 2) void grouped_wide_kernel(GroupedParams p) {
   typedef UnitOf<GROUPED_16, 256> Unit;
   typedef PairWeights<PHASE, GROUPED_16, 256, 128, 0> Weights;
   typedef W4Operand<XT, W4_E2M1> Op;  // elements in order
   constexpr int D = 4, R = D / 2;  // halves of units in flight; steps unrolled
   constexpr bool kSplit = PHASE == GROUPED_DOWN, kScaled = kSplit && XT == DT_F16;
-  constexpr int kParts = kSplit ? 2 : 1;
+  constexpr int kParts = kSplit ? PARTS : 1;
   constexpr int kPitch = 272;  // bytes of a row's 128 elements
   __shared__ TileSearch tile;
   __shared__ GroupedStage stages[8];
@@ -79,7 +83,7 @@ __global__ __launch_bounds__(512, 2) void grouped_wide_kernel(GroupedParams p) {
         float v[16];
         values(un, raw, v);
 #pragma unroll
-        for (int part = 0; part < 2; ++part)
+        for (int part = 0; part < kParts; ++part)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             uint16_t h[8];
@@ -87,17 +91,8 @@ __global__ __launch_bounds__(512, 2) void grouped_wide_kernel(GroupedParams p) {
             for (int e = 0; e < 8; ++e) {
               float& f = v[8 * i + e];
               if (kScaled && part == 0) f *= scale;
-              float back;
-              if constexpr (XT == DT_BF16) {  // as in grouped.h
-                const uint32_t top = __float_as_uint(f) & 0xffff0000u;
-                h[e] = part == 0 ? (uint16_t)(top >> 16) : f32_to_bf16_bits(f);
-                back = __uint_as_float(top);
-              } else {
-                h[e] = f32_to_f16_bits(f);
-                back = f16_bits_to_f32(h[e]);
-              }
-              const float left = f - back;
-              f = left == left ? left : 0.f;
+              // of two, bf16's second is rounded
+              h[e] = XT == DT_BF16 && kParts == 2 && part == 1 ? f32_to_bf16_bits(f) : take_part<XT>(f);
             }
             u32x4 b;
             __builtin_memcpy(&b, h, 16);
@@ -120,7 +115,7 @@ __global__ __launch_bounds__(512, 2) void grouped_wide_kernel(GroupedParams p) {
       most = max(most, dpp<0xB1>(most));
       most = max(most, dpp<0x4E>(most));
       most = max(most, dpp<0x141>(most));
-      const uint32_t ex = most >> 23, to = ex == 0 ? 127u : min(253u, 268u - ex);
+      const uint32_t to = row_power(most);
       scale = __uint_as_float(to << 23);
       if (xc == 0) unscale[xr] = __uint_as_float((254u - to) << 23);
     }
@@ -218,17 +213,20 @@ __global__ __launch_bounds__(512, 2) void grouped_wide_kernel(GroupedParams p) {
 }
 
 template <int XT>
-int grouped_wide_launch(const GroupedParams& p, int phase, hipStream_t stream) {
+int grouped_wide_launch(const GroupedParams& p, int phase, bool whole, hipStream_t stream) {
   if (phase == GROUPED_GATE_UP)
-    hipLaunchKernelGGL((grouped_wide_kernel<GROUPED_GATE_UP, XT>), dim3(p.workgroups.n), dim3(512), 0, stream, p);
+    hipLaunchKernelGGL((grouped_wide_kernel<GROUPED_GATE_UP, XT, 1>), dim3(p.workgroups.n), dim3(512), 0, stream, p);
+  else if (whole)
+    hipLaunchKernelGGL((grouped_wide_kernel<GROUPED_DOWN, XT, ValueParts<XT>::n>), dim3(p.workgroups.n), dim3(512), 0, stream, p);
   else
-    hipLaunchKernelGGL((grouped_wide_kernel<GROUPED_DOWN, XT>), dim3(p.workgroups.n), dim3(512), 0, stream, p);
+    hipLaunchKernelGGL((grouped_wide_kernel<GROUPED_DOWN, XT, 2>), dim3(p.workgroups.n), dim3(512), 0, stream, p);
   return hipGetLastError() == hipSuccess ? gt::LS_OK : gt::LS_HIP_ERROR;
 }
 
 }  // namespace gtk
 
 namespace gt {
-int grouped_wide_bf16(const gtk::GroupedParams& p, int phase, hipStream_t stream);
-int grouped_wide_f16(const gtk::GroupedParams& p, int phase, hipStream_t stream);
+// whole: all of an fp32 row's values, not 16 bits of them
+int grouped_wide_bf16(const gtk::GroupedParams& p, int phase, bool whole, hipStream_t stream);
+int grouped_wide_f16(const gtk::GroupedParams& p, int phase, bool whole, hipStream_t stream);
 }  // namespace gt

@@ -2,5 +2,5 @@
 #include "grouped_wide.h"
 
 namespace gt {
-int grouped_wide_f16(const gtk::GroupedParams& p, int phase, hipStream_t stream) { return gtk::grouped_wide_launch<DT_F16>(p, phase, stream); }
+int grouped_wide_f16(const gtk::GroupedParams& p, int phase, bool whole, hipStream_t stream) { return gtk::grouped_wide_launch<DT_F16>(p, phase, whole, stream); }
 }  // namespace gt

@@ -428,8 +428,10 @@ typedef enum gt_activation { GT_ACT_SILU = 0, GT_ACT_GELU = 1 /* its tanh form *
  *   y[t] = base[t] + sum_j weight[t,j] * down_e (act(gate_e x[t]) * (up_e x[t]))
  * Each expert's gate_up holds the H rows of gate, then the H rows of up, K
  * long; its down holds K rows of H.  Sums, activations and what passes
- * between the products are fp32; the down product takes them as two 16-bit
- * parts (at least 16 bits of each value), and y is rounded once.  A token may
+ * between the products are fp32.  Where tokens share experts the down product
+ * takes them in 16-bit parts that hold all of a value (bf16 experts) or at least
+ * 22 bits of it beside the row's largest; 16 bits only below a 16-bit y, where
+ * bf16 experts have 16 rows or more on average.  y is rounded once.  A token may
  * name an expert twice; a slot whose index is outside 0..E-1 adds nothing.
  *
  * The weights of the experts that are named are read once for up to 16 of

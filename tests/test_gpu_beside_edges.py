@@ -1,6 +1,7 @@
 """Experts and adapters beside the product at the edges of what their calls
 take: default strides of scales, infinities between the
-products and in scales.
+products and in scales, values between the products that take all of fp32's
+bits.
 """
 import math
 
@@ -96,3 +97,31 @@ def test_an_infinite_scale_of_the_last_group(where, T, fmt, scales):
                                dn.cuda(), y, gate_up_scales=gs.cuda(), down_scales=ds.cuda(), format=fmt, group=group, stream=stream()))
     torch.cuda.synchronize()
     assert (y == math.inf).all()
+
+
+@pytest.mark.parametrize("fmt", ["none", "int4", "e2m1"])
+@pytest.mark.parametrize("dtype", [BF, F16])
+@pytest.mark.parametrize("T,E,k,H", [(1, 2, 2, 40), (12, 3, 2, 40), (12, 2, 2, 1100), (9, 1, 1, 2300), (50, 2, 2, 130), (20, 1, 1, 2300)])
+def test_activations_of_23_bits(fmt, dtype, T, E, k, H):
+    # gates above 32 are their own activation, so that the values between the products are whole numbers
+    # below 2^23, and a row of down names one of them: every result is exact
+    K, g = 256, ref.rng(T + H)
+    x = torch.randint(1, 4, (T, K), generator=g).to(dtype)
+    index, _ = br.choices(T, E, k, 3)
+    at, sign = torch.randint(0, H, (E, K), generator=g), torch.randint(0, 2, (E, K), generator=g) * 2 - 1
+    down = torch.zeros(E, K, H, dtype=torch.int8).scatter_(2, at.unsqueeze(2), sign.unsqueeze(2).to(torch.int8))
+    if fmt == "none":
+        w = dict(gate_up=torch.randint(1, 9, (E, 2 * H, K), generator=g).to(dtype), down=down.to(dtype), gs=None, ds=None)
+    else:
+        few = [1, 2, 3, 4, 5, 6, 7] if fmt == "int4" else [2, 4, 5, 6, 7]  # whole numbers of 1 to 7, or 6
+        one = torch.where(down == 0, 0, torch.where(down > 0, 1, 15) if fmt == "int4" else torch.where(down > 0, 2, 10)).to(torch.uint8)
+        w = dict(gate_up=br.nibbles(E, 2 * H, K, 64, "f32", 1, few)[0], down=one[:, :, 0::2] | one[:, :, 1::2] << 4,
+                 gs=torch.ones(E, 2 * H, K // 64), ds=torch.ones(E, K, -(-H // 64)))
+    want, _ = br.moe(x, index, torch.ones(T, k), w["gate_up"], w["down"], w["gs"], w["ds"], fmt, 64)
+    assert 2 ** 20 < want.abs().max() < 2 ** 24
+    y = torch.empty(T, K, device="cuda")
+    c = {n: t.cuda() for n, t in w.items() if t is not None}
+    gt.gt_moe(gt.make_moe_desc(x.cuda(), index.cuda(), torch.ones(T, k, device="cuda"), c["gate_up"], c["down"], y,
+                               gate_up_scales=c.get("gs"), down_scales=c.get("ds"), format=fmt, group=64, stream=stream()))
+    torch.cuda.synchronize()
+    assert torch.equal(y.cpu().double(), want)
