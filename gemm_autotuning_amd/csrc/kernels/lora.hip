@@ -30,17 +30,20 @@ __device__ __forceinline__ void load_past_caches(const typename Elem<DT>::T* p, 
 }
 
 // The second product: a wave holds the tile's 16 rows of up to 32 R values as
-// operands in two 16-bit parts and walks blocks of 64 columns, whose weights
+// operands in 16-bit parts (ValueParts) and walks blocks of 64 columns, whose weights
 // (64 rows of the rank) it loads a block ahead.  What bounds it is the weights
 // with few rows (48 rows of 64 adapters rank 64, 16384 columns: 16 us, 4.4 TB/s)
 // and base and y with many (4096 rows, 4096 columns bf16: 19 us, 3.5 TB/s); the
 // results go through LDS so that a row's 64 columns are read and written by
-// eight lanes.  PAST: base and y pass by the caches.
+// eight lanes.  PAST: base and y pass by the caches.  The waves to a SIMD are
+// held to what the registers allow without spilling (4096 rows of 6 adapters rank
+// 64: 45 us with four, 52 with three, which the compiler takes by itself).
 template <int XT, int OUT, int R, bool NARROW, bool PAST>
-__global__ __launch_bounds__(256) void lora_expand_kernel(ExpandParams p) {
+__global__ __launch_bounds__(256, R == 1 ? 5 : (R == 2 ? 4 : 1)) void lora_expand_kernel(ExpandParams p) {
   typedef W4Rows<XT> Op;
   typedef typename Elem<OUT>::T TO;
   constexpr int kPitch = 68;  // floats of a row of results in LDS
+  constexpr int kParts = ValueParts<XT>::n;
   __shared__ RowTile tile;
   __shared__ float h[16][32 * R + 4];
   __shared__ float out[4][16][kPitch];
@@ -90,7 +93,7 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(ExpandParams p) {
     for (int c = 0; c < 4; ++c) load_weights(64 * (int64_t)block0 + 16 * c, raw[c]);
 
   // the rows' values: the slices' sums, in order
-  Chunk x[R][2];
+  Chunk x[R][kParts];
   float back[4] = {1.f, 1.f, 1.f, 1.f};  // of this lane's four rows of results
   if (some) {
     for (int i = tid; i < 16 * 32 * R; i += 256) {
@@ -118,13 +121,12 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(ExpandParams p) {
       for (int e = 0; e < 8; ++e) most = max(most, __float_as_uint(v[j][e]) & 0x7fffffffu);
     }
     if constexpr (XT == DT_F16) {
-      // the row's power of two, as in grouped.h
+      // the row's power of two
       const auto half = __builtin_amdgcn_permlane16_swap(most, most, false, false);
       most = max(half[0], half[1]);
       const auto both = __builtin_amdgcn_permlane32_swap(most, most, false, false);
       most = max(both[0], both[1]);
-      const uint32_t ex = most >> 23;
-      const uint32_t to = ex == 0 ? 127u : min(253u, 268u - ex);
+      const uint32_t to = row_power(most);
       const float s = __uint_as_float(to << 23);
 #pragma unroll
       for (int j = 0; j < R; ++j)
@@ -136,22 +138,10 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(ExpandParams p) {
 #pragma unroll
     for (int j = 0; j < R; ++j)
 #pragma unroll
-      for (int part = 0; part < 2; ++part) {
+      for (int part = 0; part < kParts; ++part) {
         uint16_t b[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          float near;
-          if constexpr (XT == DT_BF16) {
-            const uint32_t top = __float_as_uint(v[j][e]) & 0xffff0000u;
-            b[e] = part == 0 ? (uint16_t)(top >> 16) : f32_to_bf16_bits(v[j][e]);
-            near = __uint_as_float(top);
-          } else {
-            b[e] = f32_to_f16_bits(v[j][e]);
-            near = f16_bits_to_f32(b[e]);
-          }
-          const float left = v[j][e] - near;
-          v[j][e] = left == left ? left : 0.f;
-        }
+        for (int e = 0; e < 8; ++e) b[e] = take_part<XT>(v[j][e]);
         __builtin_memcpy(&x[j][part], b, 16);
       }
   }
@@ -195,10 +185,9 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(ExpandParams p) {
       for (int c = 0; c < 4; ++c) {
         f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int j = 0; j < R; ++j) {
-          Op::mma(acc, x[j][0], f[c][j]);
-          Op::mma(acc, x[j][1], f[c][j]);
-        }
+        for (int j = 0; j < R; ++j)
+#pragma unroll
+          for (int part = 0; part < kParts; ++part) Op::mma(acc, x[j][part], f[c][j]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) out[wave][4 * kq + e][16 * c + r] = acc[e] * back[e] * scale;
       }

@@ -493,7 +493,8 @@ gt_status gt_moe_workspace(const gt_moe_desc* d, int64_t* bytes);
  * must not overlap y: all of a row is read for each of its results); a
  * row without an adapter (an index outside 0..adapters-1) is left as base, not
  * written at all in place.  Sums and what passes between the products are
- * fp32 (two 16-bit parts of it in the second, as gt_moe); y is rounded once.
+ * fp32 (in the second 16-bit parts that hold all of it, or at least 22 bits of
+ * it with f16 rows, as gt_moe); y is rounded once.
  * An adapter's b is read once for up to 16 of its rows, its a once a row or, in
  * larger calls, for up to 16 or 64 rows.  Workspace as gt_moe. */
 typedef struct gt_lora_desc {

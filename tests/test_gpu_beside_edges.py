@@ -125,3 +125,23 @@ def test_activations_of_23_bits(fmt, dtype, T, E, k, H):
                                gate_up_scales=c.get("gs"), down_scales=c.get("ds"), format=fmt, group=64, stream=stream()))
     torch.cuda.synchronize()
     assert torch.equal(y.cpu().double(), want)
+
+
+@pytest.mark.parametrize("dtype", [BF, F16])
+@pytest.mark.parametrize("M,r,K", [(5, 12, 4096), (40, 40, 4096), (2100, 40, 4096), (600, 7, 4100), (300, 130, 4096), (90, 256, 3900)])
+def test_an_adapters_values_of_23_bits(dtype, M, r, K):
+    # whole numbers below 2^23 between the products, of which a row of b names one: every result is exact
+    L, N, g = 2, 90, ref.rng(M + r)
+    x, a = torch.randint(1, 65, (M, K), generator=g).to(dtype), torch.randint(1, 65, (L, r, K), generator=g).to(dtype)
+    at, sign = torch.randint(0, r, (L, N), generator=g), torch.randint(0, 2, (L, N), generator=g) * 2 - 1
+    b = torch.zeros(L, N, r).scatter_(2, at.unsqueeze(2), sign.unsqueeze(2).float()).to(dtype)
+    index = torch.randint(-1, L, (M,), generator=g, dtype=torch.int32)
+    want = torch.zeros(M, N, dtype=torch.float64)
+    for e in range(L):
+        m = index == e
+        want[m] = (x[m].double() @ a[e].double().t()) @ b[e].double().t()
+    assert 2 ** 21 < want.abs().max() < 2 ** 23
+    y = torch.empty(M, N, device="cuda")
+    gt.gt_lora(gt.make_lora_desc(x.cuda(), index.cuda(), a.cuda(), b.cuda(), y, stream=stream()))
+    torch.cuda.synchronize()
+    assert torch.equal(y.cpu().double(), want)
