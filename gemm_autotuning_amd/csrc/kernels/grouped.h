@@ -177,7 +177,7 @@ __device__ __forceinline__ void few_tile(const RowIndex& ix, const FewRows& f, i
 __device__ __forceinline__ float activated(float g, float u, int activation) {
   // GELU's tanh form is g / (1 + exp(-2 z)), z = sqrt(2 / pi) (g + 0.044715 g^3)
   const float z = activation == 0 ? g : 1.5957691216057308f * (g + 0.044715f * g * g * g);
-  return g * __builtin_amdgcn_rcpf(1.f + __expf(-z)) * u;
+  return g / (1.f + expf(-z)) * u;
 }
 
 // An fp32 value as 16-bit operands of the matrix core: take_part takes the

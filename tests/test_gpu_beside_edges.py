@@ -1,7 +1,7 @@
 """Experts and adapters beside the product at the edges of what their calls
 take: default strides of scales, infinities between the
 products and in scales, values between the products that take all of fp32's
-bits.
+bits, exponentials far from 0.
 """
 import math
 
@@ -145,3 +145,22 @@ def test_an_adapters_values_of_23_bits(dtype, M, r, K):
     gt.gt_lora(gt.make_lora_desc(x.cuda(), index.cuda(), a.cuda(), b.cuda(), y, stream=stream()))
     torch.cuda.synchronize()
     assert torch.equal(y.cpu().double(), want)
+
+
+@pytest.mark.parametrize("T", [1, 12, 40])
+def test_activations_of_gates_far_below_zero(T):
+    # an activation to each result.  Relatively: the exponential is off by 2 u (an ulp), the sum and the
+    # quotient by u each; bf16's parts are all of it
+    K = H = 256
+    x = torch.zeros(T, K)
+    x[:, 0] = 1.0
+    gates = torch.linspace(-70.0, 70.0, H).to(BF)
+    gate_up = torch.zeros(1, 2 * H, K)
+    gate_up[0, :H, 0], gate_up[0, H:, 0] = gates.float(), 1.0
+    y = torch.empty(T, K, device="cuda")
+    gt.gt_moe(gt.make_moe_desc(x.to(BF).cuda(), torch.zeros(T, 1, dtype=torch.int32, device="cuda"), torch.ones(T, 1, device="cuda"),
+                               gate_up.to(BF).cuda(), torch.eye(K, dtype=BF).unsqueeze(0).cuda(), y, stream=stream()))
+    torch.cuda.synchronize()
+    want = br.activation(gates.double(), "silu")
+    far = (y.cpu().double() - want).abs() / want.abs()
+    assert far.max() <= 5 * br.U, far.max() / br.U
