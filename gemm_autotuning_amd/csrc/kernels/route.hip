@@ -87,6 +87,9 @@ __global__ __launch_bounds__(256) void route_kernel(gt::RouteArgs a) {
   const float most = top > kMasked ? Key::value(top) : 0.f;  // nothing left: no sum is used
   float all = 0.f;
   if (!a.sigmoid && !a.normalise) {
+    // fast exponentials: one of an argument d is off by |d| of fp32's half steps, and with what it
+    // carries of the sum all of 1024 by 4.5 at most, less than the sum's own 22 roundings may be.
+    // Whole ones cost 8192 x 256 8.4 us for 7.5.
 #pragma unroll
     for (int j = 0; j < PER; ++j) all += key[j] > kMasked ? __expf(Key::value(key[j]) - most) : 0.f;
     all = lanes_sum<LANES>(all);
