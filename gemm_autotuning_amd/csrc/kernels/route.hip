@@ -146,20 +146,27 @@ __global__ __launch_bounds__(256) void route_kernel(gt::RouteArgs a) {
 
 namespace gt {
 
+// (launches of 2^22 workgroups: a grid has fewer than 2^32 threads)
 template <int DT>
-int route(const RouteArgs& a) {
-  const bool few = a.topk > 16 || a.E > 256;
-  const int64_t blocks = few ? (a.M + 3) / 4 : (a.M + 15) / 16;
-  if (blocks > 0x7fffff) return LS_UNSUPPORTED;
-  const dim3 grid((unsigned)blocks), block(256);
+int route(const RouteArgs& all) {
+  const bool few = all.topk > 16 || all.E > 256;
+  const int64_t rows = few ? 4 : 16, most = rows << 22;
+  for (int64_t m = 0; m < all.M; m += most) {
+    RouteArgs a = all;
+    a.M = all.M - m < most ? all.M - m : most;
+    a.logits = static_cast<const char*>(all.logits) + m * all.ldl * elem_bytes(DT);
+    a.index = all.index + m * all.ldi;
+    a.weight = all.weight + m * all.ldw;
+    const dim3 grid((unsigned)((a.M + rows - 1) / rows)), block(256);
 #define GT_ROUTE(LANES, PER) \
   if (a.E <= LANES * PER) { hipLaunchKernelGGL((gtk::route_kernel<DT, LANES, PER>), grid, block, 0, a.stream, a); }
-  if (few) {
-    GT_ROUTE(64, 4) else GT_ROUTE(64, 8) else GT_ROUTE(64, 16)
-  } else {
-    GT_ROUTE(16, 4) else GT_ROUTE(16, 8) else GT_ROUTE(16, 16)
-  }
+    if (few) {
+      GT_ROUTE(64, 4) else GT_ROUTE(64, 8) else GT_ROUTE(64, 16)
+    } else {
+      GT_ROUTE(16, 4) else GT_ROUTE(16, 8) else GT_ROUTE(16, 16)
+    }
 #undef GT_ROUTE
+  }
   return hipGetLastError() == hipSuccess ? LS_OK : LS_HIP_ERROR;
 }
 

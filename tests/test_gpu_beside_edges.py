@@ -1,7 +1,8 @@
 """Experts and adapters beside the product at the edges of what their calls
 take: default strides of scales, infinities between the
 products and in scales, values between the products that take all of fp32's
-bits, exponentials far from 0.
+bits, exponentials far from 0,
+more rows than a launch.
 """
 import math
 
@@ -164,3 +165,20 @@ def test_activations_of_gates_far_below_zero(T):
     want = br.activation(gates.double(), "silu")
     far = (y.cpu().double() - want).abs() / want.abs()
     assert far.max() <= 5 * br.U, far.max() / br.U
+
+
+@pytest.mark.parametrize("E,k,M", [(17, 17, (1 << 25) + 4097), (4, 2, (1 << 26) + 5)])
+def test_choices_of_more_rows_than_one_launch_takes(E, k, M):
+    # the rows repeat every 4099, and so do their choices
+    part = torch.randn(4099, E, generator=ref.rng(E)).half()
+    logits = part.cuda().repeat(-(-M // 4099), 1)[:M]
+    index, weight = torch.full((M, k), -7, dtype=torch.int32, device="cuda"), torch.full((M, k), -7.0, device="cuda")
+    gt.gt_route(gt.make_route_desc(logits, index, weight, stream=stream()))
+    torch.cuda.synchronize()
+    want, w = br.route(part, k)
+    # an exponential of an argument of magnitude a is off by (a + 2) u, the sum of positive ones and the
+    # quotient by 40 u more
+    assert ((weight[:4099].cpu().double() - w).abs() <= w * (4 * part.abs().max().item() + 40) * br.U).all()
+    for t, first in ((index, want.cuda()), (weight, weight[:4099])):
+        whole = M // 4099 * 4099
+        assert (t[:whole].view(-1, 4099, k) == first).all() and (t[whole:] == first[:M - whole]).all()
