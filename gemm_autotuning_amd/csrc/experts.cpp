@@ -48,7 +48,7 @@ gt_status route(const gt_route_desc* d) {
 }
 
 // E matrices of N rows, each of `row` elements (bytes for 4-bit codes), `unit`
-// bytes an element.
+// bytes an element.  Their strides; the pointers are looked at by `there`.
 gt_status matrices(const void* p, int64_t E, int64_t N, int64_t row, int unit, int64_t ld, int64_t stride, const char* what,
                    ExpertWeights* w) {
   GT_CHECK(leading(ld, row, what, &ld));
@@ -57,8 +57,8 @@ gt_status matrices(const void* p, int64_t E, int64_t N, int64_t row, int unit, i
   if (stride <= 0) stride = std::max<int64_t>(N, 1) * ld;
   if (stride < row) return invalid(std::string(what) + ": matrices overlap");
   if (E > 0 && N > 0 && row > 0) {
-    GT_CHECK(operand(p, true, N, ld, unit, what));
-    GT_CHECK(operand(p, true, E, stride, unit, what));
+    GT_CHECK(spans(N, ld, what));
+    GT_CHECK(spans(E, stride, what));
   }
   w->p = static_cast<const char*>(p);
   w->scales = nullptr;
@@ -68,7 +68,7 @@ gt_status matrices(const void* p, int64_t E, int64_t N, int64_t row, int unit, i
   return GT_OK;
 }
 
-gt_status matrix_scales(const void* p, int64_t E, int64_t N, int64_t groups, int dtype, int64_t lde, int64_t ldn, int64_t ldg,
+gt_status matrix_scales(const void* p, int64_t E, int64_t N, int64_t groups, int64_t lde, int64_t ldn, int64_t ldg,
                         const char* what, ExpertWeights* w) {
   w->scales = p;
   w->s_ldn = ldn > 0 ? ldn : std::max<int64_t>(groups, 1);
@@ -78,10 +78,12 @@ gt_status matrix_scales(const void* p, int64_t E, int64_t N, int64_t groups, int
   // one matrix after another, whether its rows or its groups lie further apart
   w->s_lde = lde > 0 ? lde : std::max(N * w->s_ldn, groups * w->s_ldg);
   if (E == 0 || N == 0 || groups == 0) return GT_OK;
-  GT_CHECK(operand(p, true, N, w->s_ldn, elem_bytes(dtype), what));
-  GT_CHECK(operand(p, true, groups, w->s_ldg, 1, what));
-  return operand(p, true, E, w->s_lde, 1, what);
+  GT_CHECK(spans(N, w->s_ldn, what));
+  GT_CHECK(spans(groups, w->s_ldg, what));
+  return spans(E, w->s_lde, what);
 }
+// A pointer to weights or scales that there are (`any`), `unit` bytes an element.
+gt_status there(const void* p, bool any, int unit, const char* what) { return any ? operand(p, true, 0, 0, unit, what) : GT_OK; }
 
 // A workspace of the caller's or of the stream's, and what is launched on it.
 template <class A, class L>
@@ -111,7 +113,7 @@ size_t most_bytes(const A& a, int64_t most, B bytes) {
   return a.M > most && a.M % most ? std::max(whole, bytes(a, a.M % most)) : whole;
 }
 
-// The descriptor's sizes and types.
+// The descriptor's sizes, types and the weights' strides.
 gt_status moe_shape(const gt_moe_desc* d, MoeArgs* a) {
   if (d->M < 0 || d->K < 0 || d->H < 0 || d->E < 0 || d->topk < 0) return invalid("negative dimension");
   if (d->x_dtype < 0 || d->x_dtype > DT_E4M3) return invalid("unknown type of x");
@@ -139,6 +141,17 @@ gt_status moe_shape(const gt_moe_desc* d, MoeArgs* a) {
   a->E = (int)d->E;
   a->topk = (int)d->topk;
   a->wide = false;
+  const bool k4 = a->format != GT_WEIGHTS_16BIT;
+  auto row = [&](int64_t n) { return k4 ? n / 2 + n % 2 : n; };
+  GT_CHECK(matrices(d->gate_up, a->E, 2 * a->H, row(a->K), k4 ? 1 : 2, d->gate_up_ld, d->gate_up_stride, "gate_up", &a->gate_up));
+  GT_CHECK(matrices(d->down, a->E, a->K, row(a->H), k4 ? 1 : 2, d->down_ld, d->down_stride, "down", &a->down));
+  if (k4) {
+    const int64_t g = INT64_C(1) << a->group_lg;
+    GT_CHECK(matrix_scales(d->gate_up_scales, a->E, 2 * a->H, (a->K + g - 1) / g, d->gate_up_scale_lde, d->gate_up_scale_ldn,
+                           d->gate_up_scale_ldg, "gate_up_scales", &a->gate_up));
+    GT_CHECK(matrix_scales(d->down_scales, a->E, a->K, (a->H + g - 1) / g, d->down_scale_lde, d->down_scale_ldn, d->down_scale_ldg,
+                           "down_scales", &a->down));
+  }
   return GT_OK;
 }
 bool moe_empty(const MoeArgs& a) { return a.H == 0 || a.E == 0 || a.topk == 0; }
@@ -152,17 +165,11 @@ gt_status moe(const gt_moe_desc* d) {
   GT_CHECK(leading(d->ldw, a.topk, "weight", &a.ldw));
   GT_CHECK(leading(d->ldb, a.K, "base", &a.ldb));
   GT_CHECK(leading(d->ldy, a.K, "y", &a.ldy));
-  const bool wide = a.format == GT_WEIGHTS_16BIT;
-  auto row = [&](int64_t n) { return wide ? n : n / 2 + n % 2; };
-  GT_CHECK(matrices(d->gate_up, a.E, 2 * a.H, row(a.K), wide ? 2 : 1, d->gate_up_ld, d->gate_up_stride, "gate_up", &a.gate_up));
-  GT_CHECK(matrices(d->down, a.E, a.K, row(a.H), wide ? 2 : 1, d->down_ld, d->down_stride, "down", &a.down));
-  if (!wide) {
-    const int64_t g = INT64_C(1) << a.group_lg;
-    GT_CHECK(matrix_scales(d->gate_up_scales, a.E, 2 * a.H, (a.K + g - 1) / g, a.scale_dtype, d->gate_up_scale_lde,
-                           d->gate_up_scale_ldn, d->gate_up_scale_ldg, "gate_up_scales", &a.gate_up));
-    GT_CHECK(matrix_scales(d->down_scales, a.E, a.K, (a.H + g - 1) / g, a.scale_dtype, d->down_scale_lde, d->down_scale_ldn,
-                           d->down_scale_ldg, "down_scales", &a.down));
-  }
+  const bool any = a.E > 0 && a.H > 0 && a.K > 0, k4 = a.format != GT_WEIGHTS_16BIT;
+  GT_CHECK(there(d->gate_up, any, k4 ? 1 : 2, "gate_up"));
+  GT_CHECK(there(d->down, any, k4 ? 1 : 2, "down"));
+  GT_CHECK(there(d->gate_up_scales, any && k4, elem_bytes(a.scale_dtype), "gate_up_scales"));
+  GT_CHECK(there(d->down_scales, any && k4, elem_bytes(a.scale_dtype), "down_scales"));
   if (a.M == 0 || a.K == 0) return GT_OK;
   const bool empty = moe_empty(a);
   GT_CHECK(operand(d->x, !empty, a.M, a.ldx, 2, "x"));
@@ -243,6 +250,8 @@ gt_status lora(const gt_lora_desc* d) {
   GT_CHECK(leading(d->ldy, a.N, "y", &a.ldy));
   GT_CHECK(matrices(d->a, a.adapters, a.rank, a.K, 2, d->a_ld, d->a_stride, "a", &a.a));
   GT_CHECK(matrices(d->b, a.adapters, a.N, a.rank, 2, d->b_ld, d->b_stride, "b", &a.b));
+  GT_CHECK(there(d->a, a.adapters > 0 && a.rank > 0 && a.K > 0, 2, "a"));
+  GT_CHECK(there(d->b, a.adapters > 0 && a.rank > 0 && a.N > 0, 2, "b"));
   if (a.M == 0 || a.N == 0) return GT_OK;
   const bool empty = lora_empty(a);
   GT_CHECK(operand(d->x, !empty, a.M, a.ldx, 2, "x"));

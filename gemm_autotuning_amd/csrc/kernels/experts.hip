@@ -105,20 +105,22 @@ namespace {
 constexpr int64_t kMostPairs = gtk::kMostRows;
 
 int down_split(const MoeArgs& a);
+bool in_tiles(const MoeArgs& a);
 
 struct MoeSpace {
   int64_t act_ld, part_ld, split;
-  size_t act, part, bytes;  // offsets; the table of tiles comes first
+  size_t act, part, bytes;  // offsets; with tiles their table comes first, without there are only activations
 };
 MoeSpace space(MoeArgs a, int64_t tokens) {
   MoeSpace s;
   a.M = tokens;
   const int64_t pairs = tokens * a.topk;
+  const bool tiles = in_tiles(a);
   s.act_ld = (a.H + 3) / 4 * 4;
   s.part_ld = (a.K + 3) / 4 * 4;
-  s.act = gtk::row_table_bytes(pairs);
+  s.act = tiles ? gtk::row_table_bytes(pairs) : 0;
   s.part = s.act + (size_t)pairs * s.act_ld * 4;
-  s.split = down_split(a);
+  s.split = tiles ? down_split(a) : 0;
   s.bytes = s.part + (size_t)(pairs * s.split * s.part_ld * 4);
   return s;
 }
@@ -143,6 +145,7 @@ bool in_units(const MoeArgs& a, const ExpertWeights& w, int64_t K) {
   const int e = elem_bytes(a.scale_dtype);
   return w.s_ldn <= most / 32 / e && w.s_ldg <= most / 2 / e / ((K >> a.group_lg) + 1);
 }
+bool in_units(const MoeArgs& a) { return in_units(a, a.gate_up, a.K) && in_units(a, a.down, a.H); }
 
 // Whether so few tokens name the same experts that each may read its own
 // (experts_token.hip): up to 32 MiB of weights read again, of 4 bits 4 MiB
@@ -153,14 +156,19 @@ bool in_units(const MoeArgs& a, const ExpertWeights& w, int64_t K) {
 // 2 (3 MB) 34.0 and 34.4, 4 (20 MB) 55 and 51; 4 of 32 experts 1024 x 512: 4 tokens
 // (3 MB) 15.8 and 20.5.  More than 8 tokens would gain only where the experts are
 // tiny (16 tokens, 2 of 8 experts 256 x 512: 11.4 and 17.2) and have the tiles.
+// One token always does: should it name experts twice, its tiles' sums would take
+// up to topk * K floats for each slice of H.
 bool hardly_share(const MoeArgs& a) {
   if (a.M > 8) return false;
+  if (a.M == 1) return true;
   double left = 1.0;  // the share of experts that no token names
   for (int64_t t = 0; t < a.M; ++t) left *= std::max(0.0, 1.0 - (double)a.topk / a.E);
   const double again = (double)(a.M * a.topk) - a.E * (1.0 - left);
   const double bytes = 3.0 * a.H * a.K * (a.format < 0 ? 2.0 : 0.5);
   return again * bytes <= (a.format < 0 ? 32.0 : 4.0) * (1 << 20);
 }
+
+bool in_tiles(const MoeArgs& a) { return in_units(a) && !hardly_share(a); }
 
 // How a product's K is cut: into units, a wave's slice of them, and where one
 // workgroup's waves do not hold all of them, turns (the gated product) or
@@ -236,12 +244,12 @@ int launch_moe(const MoeArgs& a) {
   const MoeSpace s = space(a, a.M);
   float* act = reinterpret_cast<float*>(a.ws + s.act);
   float* part = reinterpret_cast<float*>(a.ws + s.part);
-  if (!in_units(a, a.gate_up, a.K) || !in_units(a, a.down, a.H)) {
+  if (!in_units(a)) {
     hipLaunchKernelGGL(gtk::moe_up_kernel, dim3((unsigned)((a.H + 3) / 4), (unsigned)(a.M * a.topk)), dim3(256), 0, a.stream, a, act);
     hipLaunchKernelGGL(gtk::moe_down_kernel, dim3((unsigned)((a.K + 3) / 4), (unsigned)a.M), dim3(256), 0, a.stream, a, act);
     return hipGetLastError() == hipSuccess ? LS_OK : LS_HIP_ERROR;
   }
-  if (hardly_share(a)) return launch_moe_tokens(a, act, s.act_ld);
+  if (!in_tiles(a)) return launch_moe_tokens(a, act, s.act_ld);
   const int64_t pairs = a.M * a.topk, tiles = most_tiles(pairs, a.E, a.wide ? 64 : 16);
   gtk::GroupedParams p{};
   p.ix = gtk::RowIndex{a.index, a.ldi, (int)pairs, a.topk, a.E, ((1u << 20) + a.topk - 1) / a.topk, 0, bits_of(a.E - 1), a.wide ? 6 : 4};

@@ -33,11 +33,14 @@ inline gt_status leading(int64_t ld, int64_t row, const char* what, int64_t* out
 
 // A matrix of `rows` rows must be addressable in 64-bit byte offsets, and
 // its base aligned to its element.
+inline gt_status spans(int64_t rows, int64_t ld, const char* what) {
+  if (rows > 0 && ld > INT64_MAX / 8 / rows) return invalid(std::string(what) + " spans more than 64-bit offsets");
+  return GT_OK;
+}
 inline gt_status operand(const void* p, bool required, int64_t rows, int64_t ld, int bytes, const char* what) {
   if (!p) return required ? invalid(std::string(what) + " is NULL") : GT_OK;
   if ((uintptr_t)p % bytes) return invalid(std::string(what) + " is not aligned to its element");
-  if (rows > 0 && ld > INT64_MAX / 8 / rows) return invalid(std::string(what) + " spans more than 64-bit offsets");
-  return GT_OK;
+  return spans(rows, ld, what);
 }
 
 #define GT_CHECK(expr)                 \

@@ -437,8 +437,9 @@ typedef enum gt_activation { GT_ACT_SILU = 0, GT_ACT_GELU = 1 /* its tanh form *
  * The weights of the experts that are named are read once for up to 16 of
  * their rows (64 where 16-bit experts have 16 rows or more on average), so
  * this is for the few tokens of a decode batch: any M is taken, in ranges of
- * tokens whose intermediate values take about 64 MiB, but a prompt's rows
- * belong in one product per expert.
+ * tokens whose intermediate values take about 64 MiB (one token's activations,
+ * topk * H floats, may be more), but a prompt's rows belong in one product per
+ * expert.
  *
  * The intermediate values take gt_moe_workspace bytes of device memory (fewer
  * tokens may take more than many, whose sums are cut into fewer slices: ask
@@ -483,7 +484,8 @@ typedef struct gt_moe_desc {
  * 4096, topk > 64, K or H > 2^24.  GT_ERR_OOM: no memory for the workspace.  M == 0 or K ==
  * 0 is a no-op; H, E or topk == 0 leaves y = base (zeros without one). */
 gt_status gt_moe(const gt_moe_desc* d);
-/* The workspace's bytes (0 for none); pointers are not looked at. */
+/* The workspace's bytes (0 for none); pointers are not looked at, the weights'
+ * strides are. */
 gt_status gt_moe_workspace(const gt_moe_desc* d, int64_t* bytes);
 
 /* Adapters of many requests beside a shared projection: with a = index[m],

@@ -152,6 +152,26 @@ def test_workspaces(stand_in):
         gt.gt_moe_workspace(moe_desc(x_dtype=gt.F32))
 
 
+def test_a_layers_workspace_is_what_its_kernels_use(stand_in):
+    # without tiles (one token, few that hardly share experts, rows shorter than 16 bytes, rows too far
+    # apart) only the activations
+    for change in (dict(M=1, K=65536, H=65536, E=64, topk=64, format=0), dict(M=1, K=4096, H=2048, E=4, topk=64),
+                   dict(M=3, K=2048, H=768, E=128, topk=8), dict(M=100, K=4, H=24), dict(M=20, gate_up_ld=1 << 28)):
+        d = moe_desc(**{**change, "gate_up": None, "gate_up_scales": None})
+        assert gt.gt_moe_workspace(d) == d.M * d.topk * d.H * 4, change
+    # about 64 MiB however long the rows, or one token's activations
+    for K in (64, 4096, 65536, 1 << 24):
+        for H in (64, 14336, 65536, 1 << 24):
+            for topk in (1, 8, 64):
+                for f in (-1, 0):
+                    for M in (1, 7, 64, 1000, 1 << 20):
+                        d = moe_desc(M=M, K=K, H=H, E=64, topk=topk, format=f)
+                        assert 0 < gt.gt_moe_workspace(d) <= max(81 << 20, topk * H * 4), (M, K, H, topk, f)
+    for bad in (dict(gate_up_stride=63), dict(down_ld=31), dict(format=0, down_scale_ldg=FAR)):
+        with pytest.raises(gt.GemmTuneError):
+            gt.gt_moe_workspace(moe_desc(**bad))
+
+
 def test_descriptor_sizes_match_the_header():
     assert ctypes.sizeof(gt.RouteDesc) == 3 * 8 + 6 * 8 + 3 * 4 + 4 + 8
     assert ctypes.sizeof(gt.MoeDesc) == 10 * 8 + 21 * 8 + 6 * 4 + 8
