@@ -178,6 +178,8 @@ gt_status moe(const gt_moe_desc* d) {
   GT_CHECK(operand(d->base, false, a.M, a.ldb, elem_bytes(a.out_dtype), "base"));
   GT_CHECK(operand(d->y, true, a.M, a.ldy, elem_bytes(a.out_dtype), "y"));
   if (d->base == d->y && a.ldb != a.ldy) return invalid("base is y with another leading dimension");
+  // a range of tokens reads its rows of x before it writes its rows of y, which then have to be the same ones
+  if (!empty && d->x == d->y && (a.ldx != a.ldy || a.x_dtype != a.out_dtype)) return invalid("x is y with another type or leading dimension");
   a.x = d->x;
   a.index = d->index;
   a.weight = d->weight;

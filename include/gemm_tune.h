@@ -432,7 +432,8 @@ typedef enum gt_activation { GT_ACT_SILU = 0, GT_ACT_GELU = 1 /* its tanh form *
  * takes them in 16-bit parts that hold all of a value (bf16 experts) or at least
  * 22 bits of it beside the row's largest; 16 bits only below a 16-bit y, where
  * bf16 experts have 16 rows or more on average.  y is rounded once.  A token may
- * name an expert twice; a slot whose index is outside 0..E-1 adds nothing.
+ * name an expert twice; a slot whose index is outside 0..E-1 adds nothing.  x may
+ * be y itself (same type and leading dimension); else they must not overlap.
  *
  * The weights of the experts that are named are read once for up to 16 of
  * their rows (64 where 16-bit experts have 16 rows or more on average), so

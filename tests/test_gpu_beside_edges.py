@@ -2,7 +2,8 @@
 take: default strides of scales, infinities between the
 products and in scales, values between the products that take all of fp32's
 bits, exponentials far from 0,
-more rows than a launch.
+more rows than a launch,
+results over the rows themselves.
 """
 import math
 
@@ -182,3 +183,17 @@ def test_choices_of_more_rows_than_one_launch_takes(E, k, M):
     for t, first in ((index, want.cuda()), (weight, weight[:4099])):
         whole = M // 4099 * 4099
         assert (t[:whole].view(-1, 4099, k) == first).all() and (t[whole:] == first[:M - whole]).all()
+
+
+@pytest.mark.parametrize("T,E,k", [(1, 3, 2), (7, 200, 3), (30, 4, 3), (1500, 4, 3)])
+def test_results_over_the_rows_themselves(T, E, k):
+    # x is y, and is the base too; many tokens run in several ranges
+    K, H = 72, 40
+    x, (index, weight) = ref.loud(T, K, 1).to(BF).cuda(), br.choices(T, E, k, 2)
+    gate_up, down = br.normal((E, 2 * H, K), K ** -0.5, BF, 3).cuda(), br.normal((E, K, H), H ** -0.5, BF, 4).cuda()
+    for base in (False, True):
+        here, there = x.clone(), torch.empty_like(x)
+        for xs, y in ((x, there), (here, here)):
+            gt.gt_moe(gt.make_moe_desc(xs, index.cuda(), weight.cuda(), gate_up, down, y, base=xs if base else None, stream=stream()))
+        torch.cuda.synchronize()
+        assert torch.equal(here, there)

@@ -126,6 +126,16 @@ def test_taken(stand_in, op, change):
     call(desc(**change))
 
 
+def test_x_that_is_y(stand_in):
+    gt.gt_moe(moe_desc(x=2 * P, y=2 * P))
+    gt.gt_moe(moe_desc(x=2 * P, y=2 * P, base=2 * P, ldx=70, ldy=70, ldb=70))
+    gt.gt_moe(moe_desc(x=2 * P, y=2 * P, E=0, out_dtype=gt.F32))  # x is not read
+    for change in (dict(out_dtype=gt.F32), dict(out_dtype=gt.F16), dict(ldy=70), dict(ldx=70)):
+        with pytest.raises(gt.GemmTuneError) as e:
+            gt.gt_moe(moe_desc(x=2 * P, y=2 * P, **change))
+        assert e.value.status == INVALID
+
+
 def test_null_arguments_are_refused(stand_in):
     L = gt.lib()
     n = ctypes.c_int64(7)
