@@ -3,7 +3,8 @@ take: default strides of scales, infinities between the
 products and in scales, values between the products that take all of fp32's
 bits, exponentials far from 0,
 more rows than a launch,
-results over the rows themselves.
+results over the rows themselves, NaN among the logits, one token's experts
+named many times.
 """
 import math
 
@@ -197,3 +198,56 @@ def test_results_over_the_rows_themselves(T, E, k):
             gt.gt_moe(gt.make_moe_desc(xs, index.cuda(), weight.cuda(), gate_up, down, y, base=xs if base else None, stream=stream()))
         torch.cuda.synchronize()
         assert torch.equal(here, there)
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF])
+@pytest.mark.parametrize("E", [50, 400])
+def test_a_nan_is_in_all_weights_that_are_divided(dtype, E):
+    # with a softmax or normalise a NaN makes all weights of its row NaN, and +infinity does with a softmax;
+    # a sigmoid by itself leaves the others
+    k = 8
+    logits = torch.randn(6, E, generator=ref.rng(1)).to(dtype)
+    logits[0, 7] = math.nan
+    logits[1, 7], logits[1, 30] = -math.nan, math.nan
+    logits[2, 9] = math.inf
+    logits[3] = math.nan
+    logits[4, 20:] = -math.inf
+    logits[4, 3] = math.nan
+    for score in ("softmax", "sigmoid"):
+        for normalise in (True, False):
+            index, weight = torch.empty(6, k, dtype=torch.int32, device="cuda"), torch.empty(6, k, device="cuda")
+            gt.gt_route(gt.make_route_desc(logits.cuda(), index, weight, score=score, normalise=normalise, stream=stream()))
+            torch.cuda.synchronize()
+            i, w = index.cpu(), weight.cpu()
+            want_i, want_w = br.route(logits, k, score, normalise)
+            assert torch.equal(i, want_i)
+            nan = torch.isnan(w)
+            if score == "softmax":
+                assert nan[:5].all() and not nan[5].any()
+            elif normalise:
+                assert nan[[0, 1, 3, 4]].all() and not nan[[2, 5]].any()
+            else:
+                assert torch.equal(nan, torch.isnan(logits.gather(1, i.long())))
+            # arguments up to 12: exponentials off by 2 u, a sum of up to 1024 and the quotients by 60 u together
+            ok = ~nan
+            assert ((w.double() - want_w)[ok].abs() <= 100 * br.U * want_w[ok]).all()
+
+
+@pytest.mark.parametrize("fmt", ["none", "int4"])
+@pytest.mark.parametrize("dtype", [BF, F16])
+def test_one_token_that_names_its_experts_many_times(dtype, fmt):
+    E, k, K, H = 2, 11, 100, 72
+    g = ref.rng(1)
+    if fmt == "none":
+        c = dict(gate_up=br.normal((E, 2 * H, K), K ** -0.5, dtype, 2), down=br.normal((E, K, H), H ** -0.5, dtype, 3), gs=None, ds=None)
+    else:
+        (gu, gs), (dn, ds) = br.nibbles(E, 2 * H, K, 32, "f16", 2), br.nibbles(E, K, H, 32, "f16", 3)
+        c = dict(gate_up=gu, down=dn, gs=gs, ds=ds)
+    x, index, weight = ref.loud(1, K, 4).to(dtype), torch.randint(-1, E, (1, k), generator=g, dtype=torch.int32), torch.rand(1, k, generator=g)
+    y = torch.empty(1, K, device="cuda")
+    d = {n: t if t is None else t.cuda() for n, t in c.items()}
+    gt.gt_moe(gt.make_moe_desc(x.cuda(), index.cuda(), weight.cuda(), d["gate_up"], d["down"], y, gate_up_scales=d["gs"],
+                               down_scales=d["ds"], format=fmt, group=32, stream=stream()))
+    torch.cuda.synchronize()
+    want, far = br.moe(x, index, weight, c["gate_up"], c["down"], c["gs"], c["ds"], fmt, 32)
+    ref.check(y.cpu(), want, far, "y")
