@@ -42,7 +42,6 @@ gt_status route(const gt_route_desc* d) {
   a.stream = stream_of(d->stream);
   DeviceState* dev = nullptr;
   GT_CHECK(current_device(&dev));
-  a.cus = dev->cus;
   if (dev->fake) return GT_OK;
   return launched(launch_route(a), "gt_route");
 }

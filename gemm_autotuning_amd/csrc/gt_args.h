@@ -110,7 +110,6 @@ struct RouteArgs {
   int E, topk, dtype;
   bool sigmoid, normalise;
   float scale;
-  int cus;
   hipStream_t stream;
 };
 

@@ -177,7 +177,7 @@ struct MoeCut : gtk::GroupedCut {
   int units, split;
 };
 MoeCut cut(const MoeArgs& a, bool down) {
-  MoeCut c;
+  MoeCut c{};
   const int64_t K = down ? a.H : a.K;
   if (a.wide) {
     c.units = (int)((K + 127) / 128);

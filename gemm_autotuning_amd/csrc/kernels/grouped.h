@@ -736,7 +736,7 @@ int grouped_sizes(const GroupedParams& p, const GroupedCut& c, hipStream_t strea
     constexpr int D = PHASE == GROUPED_DOWN ? 2 : 4;
     constexpr bool kThree = PHASE == GROUPED_DOWN && ValueParts<XT>::n == 3;  // rows' parts: registers for two units
     if constexpr (PHASE == GROUPED_SHRINK) GT_GROUPED(256, 1, 2, 1, 8, true)
-    GT_GROUPED(256, 2, 4, 1, 8, true)
+    if constexpr (PHASE == GROUPED_SHRINK || kThree) GT_GROUPED(256, 2, 4, 1, 8, true)
     if constexpr (!kThree) GT_GROUPED(256, 4, D, 1, 8, true)
     if constexpr (PHASE == GROUPED_GATE_UP) GT_GROUPED(256, 4, 4, 2, 8, false)
     if constexpr (PHASE == GROUPED_SHRINK) GT_GROUPED(256, 4, 4, 1, 8, false)
