@@ -472,9 +472,9 @@ bool few_rows(const LoraArgs& a) {
 }
 
 // The first product's slices: one workgroup's K where the tiles alone give
-// eight workgroups to a CU, more where they do not (4096 rows of 6 adapters rank 32, 4096
-// long: 42 us with 4 slices, 44 with one; a number of slices that does not
-// divide the waves' units loses, 50 with 3).
+// eight workgroups to a CU, more where they do not (300 rows of 2 adapters rank 32, 4096
+// long: 15.4 us with 4 slices, 22.3 with one; 4096 rows of 64 adapters rank 16: 43.1 and
+// 44.2; a number of slices that does not divide the waves' units loses, 50 with 3).
 struct LoraCut {
   gtk::GroupedCut c;
   int units, split;
