@@ -15,8 +15,9 @@
 // two; 4 of int4 experts 4096 x 2048 20.8 and 23.1).  Those 18.4 us are 75 MB
 // at 4.1 TB/s, of which the two launches' starts and ends, 2.5 us each, and
 // the chain from the choice over the loads to the joined sums are most of what
-// lies above 12; the int4 ones' 53 MB take two to three instructions to an
-// element besides.  The lanes' sums are joined at the end, the waves' through
+// lies above 12; the int4 ones' 53 MB take 18 instructions to eight weights
+// besides, some 6 us of the 20.8, and each wave has one unit, so that nothing is
+// loaded behind the choice's latency or between the launches.  The lanes' sums are joined at the end, the waves' through
 // LDS, in order.
 #include "elements.h"
 #include "grouped.h"

@@ -7,7 +7,7 @@
 // two buffers in turn, and each wave's weights come as in grouped.h.  A wave
 // has its columns' whole sums (64 rows x 32 columns in registers), so nothing
 // is joined.  8 experts 4096 x 2048 bf16, two to a token: 64 tokens 97 us (120
-// with tiles of 16 rows), 256 tokens 159 (299), 512 tokens 274 (582): at 64
+// with tiles of 16 rows), 256 tokens 160 (299), 512 tokens 274 to 291 (582): at 64
 // tokens 402 MB of weights are 4.1 TB/s, at 512 the products' 77 GFLOP (the
 // second one's rows are parts) and the waits of eight waves for each other
 // bound it.  Halving K between the waves (256 workgroups instead of 128 for

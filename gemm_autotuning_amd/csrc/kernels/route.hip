@@ -4,9 +4,11 @@
 // order of the floats (a NaN above all of them, -0 as +0); topk times the
 // largest key is joined over the lanes and taken out.  Equal logits go to the
 // lowest index: 16-bit ones' keys hold the index below the logit, so that one
-// join has both; fp32 ones' take a second join.  A row is a chain of joins, a
-// few rows one launch (128 f32, 8 of them: 4.1 us); 8192 rows of 256 bf16, 8 of
-// them, 6.4 us (7.6 with two joins) for 4.7 MB.
+// join has both; fp32 ones' take a second join.  A few rows take one launch and a
+// row's chain of choices (128 f32, 8 of them: 4.1 us); 8192 rows of 256 bf16, 8 of
+// them, 6.4 us (7.6 with two joins) for 4.7 MB: 950 vector instructions a wave,
+// most of them to find the largest of a lane's keys and to take it out, for every
+// choice anew; a join is 8 of some 90 a choice.
 #include "elements.h"
 #include "launchers.h"
 

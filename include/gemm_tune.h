@@ -436,8 +436,9 @@ typedef enum gt_activation { GT_ACT_SILU = 0, GT_ACT_GELU = 1 /* its tanh form *
  * be y itself (same type and leading dimension); else they must not overlap.
  *
  * The weights of the experts that are named are read once for up to 16 of
- * their rows (64 where 16-bit experts have 16 rows or more on average), so
- * this is for the few tokens of a decode batch: any M is taken, in ranges of
+ * their rows (64 where 16-bit experts have 16 rows or more on average; for each
+ * row where up to 8 tokens hardly share experts, and where a row of weights has
+ * less than 16 bytes or rows are 2^27 bytes apart), so this is for the few tokens of a decode batch: any M is taken, in ranges of
  * tokens whose intermediate values take about 64 MiB (one token's activations,
  * topk * H floats, may be more), but a prompt's rows belong in one product per
  * expert.
@@ -499,7 +500,9 @@ gt_status gt_moe_workspace(const gt_moe_desc* d, int64_t* bytes);
  * fp32 (in the second 16-bit parts that hold all of it, or at least 22 bits of
  * it with f16 rows, as gt_moe); y is rounded once.
  * An adapter's b is read once for up to 16 of its rows, its a once a row or, in
- * larger calls, for up to 16 or 64 rows.  Workspace as gt_moe. */
+ * larger calls, for up to 16 or 64 rows; a few rows of small matrices read b once
+ * a row and a once for 1024 columns of each.  Workspace as gt_moe, asked for also
+ * where the kernel that the sizes get leaves it alone. */
 typedef struct gt_lora_desc {
   const void* x;        /* M x K, ldx                                        */
   const int32_t* index; /* M                                                 */
