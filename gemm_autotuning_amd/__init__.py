@@ -487,6 +487,37 @@ def _expert_weights(w, scales, shape, format, group, dtype, what):
     return _matrices(w, (E, N, -(-K // 2)), what) + tuple(max(1, v) for v in strides) + (_type_of(scales, "scales of " + what),)
 
 
+def _meet(a, b):
+    """Whether two matrices with contiguous rows share a byte (rows of one may
+    lie between the other's, as the columns of a wider buffer)."""
+    if not (a.numel() and b.numel()):
+        return False
+    (pa, na, ra, sa), (pb, nb, rb, sb) = ((t.data_ptr(), t.shape[0], t.shape[1] * t.element_size(),
+                                           t.stride(0) * t.element_size()) for t in (a, b))
+    if pa + (na - 1) * sa + ra <= pb or pb + (nb - 1) * sb + rb <= pa:
+        return False
+    if na == 1:  # a stride that is not taken
+        sa = max(sb, ra)
+    if nb == 1:
+        sb = max(sa, rb)
+    if sa == sb:  # rows i and j meet where -rb < pb - pa + (j - i) * stride < ra
+        first = -((pb - pa + rb - 1) // sa)
+        return max(first, 1 - na) <= min((pa - pb + ra - 1) // sa, nb - 1)
+    import torch
+
+    at = pb - pa + torch.arange(nb, dtype=torch.int64) * sb  # of each row of b; a's last row that begins before its end
+    i = torch.div(at + rb - 1, sa, rounding_mode="floor").clamp(max=na - 1)
+    return bool(((i >= 0) & (i * sa + ra > at)).any())
+
+
+def _apart(t, y, what, itself):
+    """An operand that is read shares nothing with y, or (itself) is y."""
+    if t is None or t.device != y.device or not _meet(t, y):
+        return
+    if not (itself and t.data_ptr() == y.data_ptr() and t.dtype == y.dtype and (t.shape[0] < 2 or t.stride(0) == y.stride(0))):
+        raise ValueError("%s overlaps y" % what + (" and is not y itself" if itself else ""))
+
+
 def _workspace(t):
     """(address, bytes) of a workspace tensor, or none."""
     if t is None:
@@ -529,6 +560,8 @@ def make_moe_desc(x, index, weight, gate_up, down, y, base=None, gate_up_scales=
                 _matrix(weight, (M, k), "weight", F32), 0 if base is None else _matrix(base, (M, K), "base", odt),
                 _matrix(y, (M, K), "y"), gl, gs, dl, ds, ge, gn, gg, de, dn, dg, dt, odt, fmt, gdt, group,
                 _code(activation, ACTIVATIONS), _ptr(stream))
+    _apart(x, y, "x", True)
+    _apart(base, y, "base", True)
     return d.keep(x, index, weight, gate_up, down, y, base, gate_up_scales, down_scales, workspace)
 
 
@@ -550,6 +583,8 @@ def make_lora_desc(x, index, a, b, y, base=None, scale=None, workspace=None, str
     d = LoraDesc(_ptr(x), _ptr(index), _ptr(a), _ptr(b), _ptr(scale), _ptr(base), _ptr(y), ws, nbytes, M, K, N, L, r,
                  _matrix(x, (M, K), "x"), 0 if base is None else _matrix(base, (M, N), "base", odt), _matrix(y, (M, N), "y"), al,
                  as_, bl, bs, dt, odt, _ptr(stream))
+    _apart(x, y, "x", False)
+    _apart(base, y, "base", True)
     return d.keep(x, index, a, b, y, base, scale, workspace)
 
 

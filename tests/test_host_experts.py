@@ -253,6 +253,52 @@ def test_binding_refuses_more():
             gt.make_route_desc(**{**dict(logits=l, index=i, weight=w), **bad})
 
 
+def test_whether_matrices_meet():
+    # against every byte, for views of one buffer
+    g = ref.rng(1)
+    seen = {True: 0, False: 0}
+    buf = torch.zeros(400)
+    for _ in range(4000):
+        views, places = [], []
+        for t in (buf, buf):
+            n, c, at = (int(torch.randint(1, hi, (1,), generator=g)) for hi in (7, 9, 120))
+            s = c + int(torch.randint(0, 30, (1,), generator=g))
+            views.append(t.as_strided((n, c), (s, 1), at))
+            places.append({at + i * s + j for i in range(n) for j in range(c)})
+        want = bool(places[0] & places[1])
+        assert gt._meet(*views) == want and gt._meet(*views[::-1]) == want
+        if int(torch.randint(0, 2, (1,), generator=g)):  # rows of one length apart
+            a, b = views[0], buf.as_strided(tuple(views[1].shape), (views[0].stride(0), 1), views[1].storage_offset())
+            if b.stride(0) >= b.shape[1]:
+                want = bool(places[0] & {b.storage_offset() + i * b.stride(0) + j for i in range(b.shape[0]) for j in range(b.shape[1])})
+                assert gt._meet(a, b) == want
+        seen[want] += 1
+    assert min(seen.values()) > 500
+
+
+def test_binding_refuses_operands_that_overlap_the_result():
+    x, w = torch.zeros(3, 40, dtype=torch.bfloat16), tensors()
+    big = torch.zeros(8, 100, dtype=torch.bfloat16)
+    flat = torch.zeros(1000, dtype=torch.bfloat16)
+    for y in (x, big[:3, 40:80]):
+        gt.make_moe_desc(**{**w, "x": x, "y": y})
+    gt.make_moe_desc(**{**w, "x": big[:3, :40], "y": big[:3, 40:80], "base": big[:3, 40:80]})
+    gt.make_moe_desc(**{**w, "x": big[:3, :40], "y": big[3:6, :40], "base": big[:3, :40]})
+    gt.make_moe_desc(**{**w, "x": big[:3, :40], "y": big[:3, :40], "base": big[:3, :40]})
+    over = [dict(x=big[:3, :40], y=big[1:4, :40]), dict(x=big[:3, :40], y=big[:3, 39:79]),
+            dict(x=flat[:120].view(3, 40), y=flat.as_strided((3, 40), (50, 1), 0)),
+            dict(x=flat[:120].view(3, 40), y=flat.view(torch.float32)[:120].view(3, 40)),
+            dict(y=big[:3, :40], base=big[1:4, :40]), dict(y=big[:3, :40], base=big[:3, 1:41])]
+    for bad in over:
+        with pytest.raises(ValueError, match="overlaps y"):
+            gt.make_moe_desc(**{**w, **bad})
+    a, b, i = torch.zeros(2, 8, 40, dtype=torch.bfloat16), torch.zeros(2, 40, 8, dtype=torch.bfloat16), torch.zeros(3, dtype=torch.int32)
+    gt.make_lora_desc(big[:3, :40], i, a, b, big[:3, 40:80], base=big[:3, 40:80])
+    for bad in over + [dict(x=x, y=x)]:
+        with pytest.raises(ValueError, match="overlaps y"):
+            gt.make_lora_desc(bad.get("x", x), i, a, b, bad["y"], base=bad.get("base"))
+
+
 def test_host_tensors_are_refused(stand_in):
     for call, d in ((gt.gt_moe, gt.make_moe_desc(**tensors())), (gt.gt_route, gt.make_route_desc(torch.zeros(3, 16), torch.zeros(
             3, 2, dtype=torch.int32), torch.zeros(3, 2)))):
