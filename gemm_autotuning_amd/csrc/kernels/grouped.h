@@ -188,6 +188,8 @@ __device__ __forceinline__ float activated(float g, float u, int activation) {
 // of it, or the least subnormal, under a power of two that brings the largest of
 // the values in a sum to 2^14..2^15: row_power, the exponent field of that.
 // Beside an infinity or NaN it is 2^-114, under which no finite value becomes one.
+// The sums hold the power of two until they end: a group of 128 codes is up to
+// 2^25 times its scale there, which fp32 has room for below scales of 2^103.
 template <int XT>
 struct ValueParts {
   static constexpr int n = XT == DT_BF16 ? 3 : 2;

@@ -457,7 +457,7 @@ typedef struct gt_moe_desc {
   const void* gate_up;        /* E matrices of 2 H x K, rows gate_up_ld      */
   const void* gate_up_scales; /* 4 bits: (e, n, g) at e * _lde + n * _ldn + g * _ldg */
   const void* down;           /* E matrices of K x H, rows down_ld           */
-  const void* down_scales;
+  const void* down_scales;    /* magnitudes up to 2^100, or infinite         */
   const void* base;           /* M x K, ldb, of y's type, or NULL; may be y
                                  itself (same leading dimension)             */
   void* y;                    /* M x K, ldy                                  */
