@@ -17,8 +17,8 @@
 // the chain from the choice over the loads to the joined sums are most of what
 // lies above 12; the int4 ones' 53 MB take 18 instructions to eight weights
 // besides, some 6 us of the 20.8, and each wave has one unit, so that nothing is
-// loaded behind the choice's latency or between the launches.  The lanes' sums are joined at the end, the waves' through
-// LDS, in order.
+// loaded behind the choice's latency or between the launches.  The lanes' sums
+// are joined at the end, the waves' through LDS, in order.
 #include "elements.h"
 #include "grouped.h"
 #include "launchers.h"

@@ -438,10 +438,10 @@ typedef enum gt_activation { GT_ACT_SILU = 0, GT_ACT_GELU = 1 /* its tanh form *
  * The weights of the experts that are named are read once for up to 16 of
  * their rows (64 where 16-bit experts have 16 rows or more on average; for each
  * row where up to 8 tokens hardly share experts, and where a row of weights has
- * less than 16 bytes or rows are 2^27 bytes apart), so this is for the few tokens of a decode batch: any M is taken, in ranges of
- * tokens whose intermediate values take about 64 MiB (one token's activations,
- * topk * H floats, may be more), but a prompt's rows belong in one product per
- * expert.
+ * less than 16 bytes or rows are 2^27 bytes apart), so this is for the few
+ * tokens of a decode batch: any M is taken, in ranges of tokens whose
+ * intermediate values take about 64 MiB (one token's activations, topk * H
+ * floats, may be more), but a prompt's rows belong in one product per expert.
  *
  * The intermediate values take gt_moe_workspace bytes of device memory (fewer
  * tokens may take more than many, whose sums are cut into fewer slices: ask
